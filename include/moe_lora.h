@@ -442,6 +442,133 @@ int moe_lora_align_static_workspace(const int32_t *topk_ids, const int32_t *toke
                                     int max_num_tokens_padded, int max_num_m_blocks,
                                     int32_t *err_flag, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The 8-bit serving path beside the adapters: the base model's expert (and
+ * dense) products in 8-bit floating point, and the two row operators that
+ * feed them.  One MoE layer of a served model:
+ *
+ *   moe_add_rms_norm_fp8      hidden + residual -> residual, x (bf16), q, scales
+ *   moe_align_block_size      router's topk_ids -> blocks
+ *   moe_fp8_grouped_matmul    w13: y13 = x . w13[e]^T
+ *   moe_lora_fused_*          y13 += adapters (reads the bf16 x)
+ *   moe_silu_mul_fp8          silu(gate) * up -> q, scales
+ *   moe_fp8_grouped_matmul    w2, rows per pair, times the router's weights
+ *   moe_lora_fused_*          y2 += adapters
+ *   moe_add_rms_norm_fp8      the next norm sums each token's top-k rows of y2
+ *
+ * 8-bit values are e4m3 (finite: 448 is the largest, 0x7f and 0xff are NaN).
+ * A group is 128 consecutive columns; the last one of a row may be shorter.
+ * Row operands have one fp32 scale a group ([rows, ceil(n / 128)], dense);
+ * weights one a block of 128 x 128 ([.., ceil(N / 128), ceil(K / 128)], dense).
+ * A value is its 8 bits times its scale.  Leading dimensions are in elements.
+ * ------------------------------------------------------------------------ */
+
+typedef uint8_t moe_lora_fp8;
+
+/* Largest row of moe_add_rms_norm_fp8. */
+#define MOE_FP8_MAX_NORM_COLUMNS 16384
+
+/*
+ * moe_add_rms_norm_fp8 -- residual addition and root-mean-square norm with an
+ * 8-bit output.  For each row m, in fp32:
+ *   h[c]  = residual[m][c] + x[m][0][c] + x[m][1][c] + ...   (parts in order;
+ *           without a residual the sum starts at zero)
+ *   residual_out[m][c] = bf16(h[c])
+ *   n[c]  = h[c] / sqrt(mean_c(h^2) + eps) * weight[c]
+ *   normed[m][c] = bf16(n[c])
+ *   scales[m][g] = max(max |n| over group g / 448, 2^-126)
+ *   q[m][c] = e4m3(n[c] / scales[m][g])
+ * The norm and the 8 bits come from the fp32 h and n, not from their bf16
+ * roundings.  A NaN in a row makes that row's n, scales and q NaN.
+ *
+ *   x            [device] bf16, part p of row m at x + m*ldx + p*ld_part;
+ *                parts = 1 is the plain residual addition, parts = topk sums a
+ *                token's expert rows (y [M, topk, ld_part], ldx = topk*ld_part)
+ *   residual     [device] bf16 [M, ld_residual], or NULL
+ *   weight       [device] bf16 [H]
+ *   residual_out [device] bf16 [M, ld_residual_out], or NULL; may be residual
+ *   normed       [device] bf16 [M, ld_normed], or NULL
+ *   q            [device] e4m3 [M, ldq];  scales [device] fp32 [M, ceil(H / 128)]
+ * Sizes: M >= 0, parts >= 1, 1 <= H <= MOE_FP8_MAX_NORM_COLUMNS; each leading
+ * dimension at least H.  Any alignment of the elements; rows and pointers on
+ * 16 bytes (H % 8 == 0) are read and written 16 bytes at a time.  The outputs
+ * must not overlap x, weight or one another.
+ */
+int moe_add_rms_norm_fp8(const moe_lora_bf16 *x, long long ldx, long long ld_part, int parts,
+                         const moe_lora_bf16 *residual, long long ld_residual, const moe_lora_bf16 *weight,
+                         float eps, moe_lora_bf16 *residual_out, long long ld_residual_out,
+                         moe_lora_bf16 *normed, long long ld_normed, moe_lora_fp8 *q, long long ldq,
+                         float *scales, int M, int H, void *stream);
+
+/*
+ * moe_silu_mul_fp8 -- the gated activation with an 8-bit output:
+ *   a = x[r][c] / (1 + exp(-x[r][c])) * x[r][I + c]     (fp32, c < I)
+ * and scales and q of a as above.  The gate is in columns [0, I) of a row of
+ * x, the up projection in [I, 2I), as two slices of one w13 product.
+ *   x  [device] bf16 [rows, ldx], ldx >= 2*I
+ *   q  [device] e4m3 [rows, ldq], ldq >= I;  scales [device] fp32 [rows, ceil(I / 128)]
+ * Sizes: rows >= 0, I >= 1; alignment as above.
+ */
+int moe_silu_mul_fp8(const moe_lora_bf16 *x, long long ldx, moe_lora_fp8 *q, long long ldq, float *scales, int rows,
+                     int I, void *stream);
+
+/*
+ * moe_fp8_matmul -- y[m][n] = bf16( sum_k x[m][k] * w[n][k] ), 8-bit operands
+ * with their scales.  Within a group of 128 columns the products are summed by
+ * the tensor cores in fp32; the groups' sums are scaled and added in fp32, in
+ * ascending order (where K is split over a cluster of CTAs: ascending within
+ * each CTA's share, then the shares in ascending order).  The same call gives
+ * the same bits.
+ *   x [device] e4m3 [M, ldx], x_scales [device] fp32 [M, ceil(K / 128)]
+ *   w [device] e4m3 [N, ldw], w_scales [device] fp32 [ceil(N / 128), ceil(K / 128)]
+ *   y [device] bf16 [M, ldy]
+ * Sizes: M >= 0, N >= 1, K >= 1; x and w on 16 bytes with ldx, ldw multiples of
+ * 16 (columns from K on are not used); y and ldy are not restricted (rows on 16
+ * bytes are written 16 bytes at a time).
+ */
+int moe_fp8_matmul(const moe_lora_fp8 *x, long long ldx, const float *x_scales, const moe_lora_fp8 *w,
+                   long long ldw, const float *w_scales, moe_lora_bf16 *y, long long ldy, int M, int N, int K,
+                   int32_t *err_flag, void *stream);
+
+/*
+ * moe_fp8_grouped_matmul -- the same product over a MoE layer's experts, on
+ * the blocks of moe_align_block_size.  For every block b <
+ * num_tokens_post_padded[0] / block_size with e = expert_ids[b] and every pair
+ * f = sorted_token_ids[b*block_size + i] that is not the sentinel M*topk:
+ *   y[f][n] = bf16( (topk_weights ? topk_weights[f] : 1) * sum_k x[r][k] * w[e][n][k] )
+ * with r = f when x_per_pair, else f / topk.  Rows of y of pairs in no block
+ * are not touched.
+ *   x [device] e4m3 [M, ldx] ([M*topk, ldx] when x_per_pair) and its scales
+ *   w [device] e4m3 [num_experts, N, ldw]
+ *   w_scales [device] fp32 [num_experts, ceil(N / 128), ceil(K / 128)]
+ *   y [device] bf16 [M*topk, ldy];  topk_weights [device] fp32 [M, topk] or NULL
+ *   sorted_token_ids, expert_ids, num_tokens_post_padded: as written by
+ *     moe_align_block_size with the same M, topk, num_experts, block_size and
+ *     capacities
+ * block_size 16, 32 and 64 run the kernel for few pairs an expert (bound by the
+ * weight's bytes), 128 the one for many (bound by the tensor cores); other
+ * sizes and limits as for moe_align_block_size and moe_fp8_matmul.  An expert
+ * id out of range skips its block (MOE_LORA_DEVERR_EXPERT_ID), a pair id that
+ * is neither a pair nor the sentinel is skipped (MOE_LORA_DEVERR_PAIR_ID).
+ */
+int moe_fp8_grouped_matmul(const moe_lora_fp8 *x, int x_per_pair, long long ldx, const float *x_scales,
+                           const moe_lora_fp8 *w, long long ldw, const float *w_scales, moe_lora_bf16 *y,
+                           long long ldy, const float *topk_weights, const int32_t *sorted_token_ids,
+                           const int32_t *expert_ids, const int32_t *num_tokens_post_padded, int M, int topk,
+                           int num_experts, int K, int N, int block_size, int max_num_tokens_padded,
+                           int max_num_m_blocks, int32_t *err_flag, void *stream);
+
+/*
+ * moe_fp8_grouped_matmul_naive -- the same without an align: each pair f is a
+ * work item of its own with e = topk_ids[f] (int32 [M, topk]); pairs whose
+ * expert is out of range are skipped (MOE_LORA_DEVERR_EXPERT_ID).  For a few
+ * tokens: pairs that share an expert each read its weight.
+ */
+int moe_fp8_grouped_matmul_naive(const moe_lora_fp8 *x, int x_per_pair, long long ldx, const float *x_scales,
+                                 const moe_lora_fp8 *w, long long ldw, const float *w_scales, moe_lora_bf16 *y,
+                                 long long ldy, const float *topk_weights, const int32_t *topk_ids, int M, int topk,
+                                 int num_experts, int K, int N, int32_t *err_flag, void *stream);
+
 /* Human-readable name of a moe_lora_status value (static string). */
 const char *moe_lora_status_string(int status);
 

@@ -83,6 +83,17 @@ def lib() -> ctypes.CDLL:
             L.moe_lora_fused_resolve_path.argtypes = [I] * 10
             L.moe_lora_fused_naive_resolve_path.restype = I
             L.moe_lora_fused_naive_resolve_path.argtypes = [I] * 9
+            Q, F = ctypes.c_longlong, ctypes.c_float
+            L.moe_add_rms_norm_fp8.restype = I
+            L.moe_add_rms_norm_fp8.argtypes = [P, Q, Q, I, P, Q, P, F, P, Q, P, Q, P, Q, P, I, I, P]
+            L.moe_silu_mul_fp8.restype = I
+            L.moe_silu_mul_fp8.argtypes = [P, Q, P, Q, P, I, I, P]
+            L.moe_fp8_matmul.restype = I
+            L.moe_fp8_matmul.argtypes = [P, Q, P, P, Q, P, P, Q, I, I, I, P, P]
+            L.moe_fp8_grouped_matmul.restype = I
+            L.moe_fp8_grouped_matmul.argtypes = [P, I, Q, P, P, Q, P, P, Q, P, P, P, P, I, I, I, I, I, I, I, I, P, P]
+            L.moe_fp8_grouped_matmul_naive.restype = I
+            L.moe_fp8_grouped_matmul_naive.argtypes = [P, I, Q, P, P, Q, P, P, Q, P, P, I, I, I, I, I, P, P]
             _lib = L
     return _lib
 
@@ -348,6 +359,180 @@ def moe_lora_test_withheld_copy(x, lora_a, lora_b, y, topk_ids, token_lora_mappi
         _ptr(lora_ids, torch.int32, "lora_ids"), None, M, topk, E, K, N, r, L, lora_ids.numel(),
         int(bool(add_inputs)), int(wait_limit_ns), _ptr(err_flag, torch.int32, "err_flag"), _stream(stream))
     _check(st, "moe_lora_test_withheld_copy")
+
+
+FP8_GROUP = 128   # columns that share a scale
+
+_BF16, _F8, _F32, _I32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32
+
+
+def fp8_groups(columns: int) -> int:
+    """Scales of a row of `columns` 8-bit values."""
+    return -(-columns // FP8_GROUP)
+
+
+def _dense(t, dtype, name):
+    """Address of a contiguous CUDA tensor (0 for None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _rows(t, dtype, name, columns):
+    """Address and leading dimension of the rows of a CUDA tensor: its last
+    dimension dense, the ones before it as if they were one."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    shape, stride = t.shape, t.stride()
+    if len(shape) < 2 or shape[-1] != columns or (stride[-1] != 1 and columns > 1):
+        raise ValueError("%s must have dense rows of %d, got shape %s, strides %s" % (name, columns, tuple(shape), stride))
+    ld = stride[-2]
+    if shape[-2] == 1:        # one row: its stride says nothing
+        ld = max(ld, columns)
+        if len(shape) > 2 and shape[-3] > 1:
+            ld = stride[-3]
+    if len(shape) > 2:
+        step = ld * shape[-2]
+        for d in range(len(shape) - 3, -1, -1):
+            if shape[d] > 1 and stride[d] != step:
+                raise ValueError("%s's rows must be evenly spaced, got shape %s, strides %s" % (name, tuple(shape), stride))
+            step *= shape[d]
+    return t.data_ptr(), ld
+
+
+def _raw_stream(stream, t):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def moe_add_rms_norm_fp8(x, weight, q, scales, residual=None, residual_out=None, normed=None, eps=1e-6, stream=None):
+    """Residual addition and root-mean-square norm with an 8-bit output; see
+    include/moe_lora.h.
+
+    x: bf16 [M, H], or [M, parts, H] (a token's rows, summed).  residual,
+    residual_out, normed: bf16 [M, H] or None.  q: float8_e4m3fn [M, H];
+    scales: float32 [M, ceil(H / 128)].  Rows may be strided."""
+    H = x.shape[-1]
+    M = x.shape[0]
+    parts = 1
+    if x.dim() == 3:
+        parts = x.shape[1]
+        if x.dtype != _BF16 or not x.is_cuda:
+            raise TypeError("x must be a bfloat16 CUDA tensor")
+        ldx, ld_part, one = x.stride()
+        if one != 1 and H > 1:
+            raise ValueError("x must have dense rows")
+        px = x.data_ptr()
+        if M == 1:
+            ldx = max(ldx, H)
+    else:
+        px, ldx = _rows(x, _BF16, "x", H)
+        ld_part = 0
+    for t, name in ((residual, "residual"), (residual_out, "residual_out"), (normed, "normed"), (q, "q")):
+        if t is not None and tuple(t.shape) != (M, H):
+            raise ValueError("%s must be [%d, %d], got %s" % (name, M, H, tuple(t.shape)))
+    if weight.numel() != H or scales.numel() != M * fp8_groups(H):
+        raise ValueError("weight must be [%d] and scales [%d, %d]" % (H, M, fp8_groups(H)))
+    pr, ldr = (None, 0) if residual is None else _rows(residual, _BF16, "residual", H)
+    po, ldo = (None, 0) if residual_out is None else _rows(residual_out, _BF16, "residual_out", H)
+    pn, ldn = (None, 0) if normed is None else _rows(normed, _BF16, "normed", H)
+    pq, ldq = _rows(q, _F8, "q", H)
+    _check(lib().moe_add_rms_norm_fp8(px, ldx, ld_part, parts, pr, ldr, _dense(weight, _BF16, "weight"), eps, po, ldo,
+                                      pn, ldn, pq, ldq, _dense(scales, _F32, "scales"), M, H, _raw_stream(stream, x)),
+           "moe_add_rms_norm_fp8")
+
+
+def moe_silu_mul_fp8(x, q, scales, stream=None):
+    """silu(gate) * up with an 8-bit output; see include/moe_lora.h.
+
+    x: bf16 [..., 2*I], gate then up.  q: float8_e4m3fn [..., I]; scales:
+    float32 [..., ceil(I / 128)].  Rows may be strided, evenly."""
+    I = q.shape[-1]
+    if x.shape[:-1].numel() != q.shape[:-1].numel():
+        raise ValueError("x and q must have the same rows")
+    rows = q.shape[:-1].numel()
+    if scales.numel() != rows * fp8_groups(I):
+        raise ValueError("scales must be [%d, %d]" % (rows, fp8_groups(I)))
+    px, ldx = _rows(x, _BF16, "x", 2 * I)
+    pq, ldq = _rows(q, _F8, "q", I)
+    _check(lib().moe_silu_mul_fp8(px, ldx, pq, ldq, _dense(scales, _F32, "scales"), rows, I, _raw_stream(stream, x)),
+           "moe_silu_mul_fp8")
+
+
+def moe_fp8_matmul(x, x_scales, w, w_scales, y, err_flag=None, stream=None):
+    """y = x @ w.T, 8-bit operands with a scale for each block of 128; see
+    include/moe_lora.h.
+
+    x: float8_e4m3fn [M, K], x_scales: float32 [M, ceil(K / 128)]; w:
+    float8_e4m3fn [N, K], w_scales: float32 [ceil(N / 128), ceil(K / 128)]; y:
+    bf16 [M, N].  Rows of x, w and y may be strided (x, w: by multiples of 16)."""
+    M, K = x.shape
+    N = w.shape[0]
+    kb = fp8_groups(K)
+    if tuple(y.shape) != (M, N) or x_scales.numel() != M * kb or w_scales.numel() != fp8_groups(N) * kb:
+        raise ValueError("inconsistent shapes")
+    px, ldx = _rows(x, _F8, "x", K)
+    pw, ldw = _rows(w, _F8, "w", K)
+    py, ldy = _rows(y, _BF16, "y", N)
+    _check(lib().moe_fp8_matmul(px, ldx, _dense(x_scales, _F32, "x_scales"), pw, ldw,
+                                _dense(w_scales, _F32, "w_scales"), py, ldy, M, N, K,
+                                _dense(err_flag, _I32, "err_flag"), _raw_stream(stream, y)), "moe_fp8_matmul")
+
+
+def _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair):
+    M, topk, N = y.shape
+    E, N2, K = w.shape
+    kb = fp8_groups(K)
+    rows = M * topk if x_per_pair else M
+    if N2 != N or tuple(x.shape) != (rows, K) or x_scales.numel() != rows * kb:
+        raise ValueError("inconsistent shapes")
+    if w_scales.numel() != E * fp8_groups(N) * kb:
+        raise ValueError("w_scales must be [%d, %d, %d]" % (E, fp8_groups(N), kb))
+    if topk_weights is not None and topk_weights.numel() != M * topk:
+        raise ValueError("topk_weights must be [M, topk]")
+    px, ldx = _rows(x, _F8, "x", K)
+    pw, ldw = _rows(w, _F8, "w", K)
+    py, ldy = _rows(y, _BF16, "y", N)
+    return M, topk, E, K, N, (px, int(bool(x_per_pair)), ldx, _dense(x_scales, _F32, "x_scales"), pw, ldw,
+                              _dense(w_scales, _F32, "w_scales"), py, ldy, _dense(topk_weights, _F32, "topk_weights"))
+
+
+def moe_fp8_grouped_matmul(x, x_scales, w, w_scales, y, sorted_token_ids, expert_ids, num_tokens_post_padded,
+                           block_size, topk_weights=None, x_per_pair=False, err_flag=None, stream=None):
+    """moe_fp8_matmul over a MoE layer's experts, on moe_align_block_size's
+    blocks; see include/moe_lora.h.
+
+    x: float8_e4m3fn [M, K] ([M*topk, K] with x_per_pair); w: float8_e4m3fn [E,
+    N, K], w_scales: float32 [E, ceil(N / 128), ceil(K / 128)]; y: bf16 [M,
+    topk, N], written in place for every pair of a block; topk_weights: float32
+    [M, topk] or None."""
+    M, topk, E, K, N, operands = _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair)
+    _check(lib().moe_fp8_grouped_matmul(
+        *operands, _dense(sorted_token_ids, _I32, "sorted_token_ids"), _dense(expert_ids, _I32, "expert_ids"),
+        _dense(num_tokens_post_padded, _I32, "num_tokens_post_padded"), M, topk, E, K, N, block_size,
+        sorted_token_ids.numel(), expert_ids.numel(), _dense(err_flag, _I32, "err_flag"), _raw_stream(stream, y)),
+        "moe_fp8_grouped_matmul")
+
+
+def moe_fp8_grouped_matmul_naive(x, x_scales, w, w_scales, y, topk_ids, topk_weights=None, x_per_pair=False,
+                                 err_flag=None, stream=None):
+    """moe_fp8_grouped_matmul without an align, one work item per (token,
+    top-k) pair; topk_ids: int32 [M, topk]."""
+    M, topk, E, K, N, operands = _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair)
+    if topk_ids.numel() != M * topk:
+        raise ValueError("topk_ids must be [M, topk]")
+    _check(lib().moe_fp8_grouped_matmul_naive(*operands, _dense(topk_ids, _I32, "topk_ids"), M, topk, E, K, N,
+                                              _dense(err_flag, _I32, "err_flag"), _raw_stream(stream, y)),
+           "moe_fp8_grouped_matmul_naive")
 
 
 class AlignBuffers:

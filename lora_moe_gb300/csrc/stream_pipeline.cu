@@ -51,6 +51,20 @@ int encode_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint
   return res == CUDA_SUCCESS ? 0 : MOE_LORA_ERR_LAUNCH;
 }
 
+int encode_u8(CUtensorMap *map, const void *base, int rank, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
+              uint64_t s2, uint32_t rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return MOE_LORA_ERR_LAUNCH;
+  const cuuint64_t dims[3] = {d0, d1, d2};
+  const cuuint64_t strides[2] = {s1, s2};
+  const cuuint32_t box[3] = {128, rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult res = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(base), dims,
+                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return res == CUDA_SUCCESS ? 0 : MOE_LORA_ERR_LAUNCH;
+}
+
 int make_tensor_maps(const FusedArgs &f, const Cfg &cfg, TmapSet *maps) {
   const uint64_t LE = (uint64_t)f.max_loras * f.num_experts;
   const CUtensorMapSwizzle bsw = cfg.ka == 64 ? CU_TENSOR_MAP_SWIZZLE_128B

@@ -319,6 +319,11 @@ __device__ void expand_producer(const FusedArgs &p, const Cfg &cfg, Meta &meta, 
 
 int encode_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0, uint32_t b1,
               CUtensorMapSwizzle swizzle);
+// Map of an 8-bit tensor [d2][d1][d0] (rank 3) or [d1][d0] (rank 2) whose rows
+// are s1 bytes apart and matrices s2: boxes of `rows` rows of 128 bytes, in the
+// 128-byte swizzled layout.
+int encode_u8(CUtensorMap *map, const void *base, int rank, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
+              uint64_t s2, uint32_t rows);
 
 // Tensor maps of every slice's A ([L*E, r, K], 64 x r_pad boxes, 128-byte
 // swizzle) and B ([L*E, N, r], ka x 128 boxes, swizzle matched to ka).
