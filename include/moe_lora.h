@@ -545,18 +545,28 @@ int moe_fp8_matmul(const moe_lora_fp8 *x, long long ldx, const float *x_scales, 
  *   sorted_token_ids, expert_ids, num_tokens_post_padded: as written by
  *     moe_align_block_size with the same M, topk, num_experts, block_size and
  *     capacities
- * block_size 16, 32 and 64 run the kernel for few pairs an expert (bound by the
- * weight's bytes), 128 the one for many (bound by the tensor cores); other
- * sizes and limits as for moe_align_block_size and moe_fp8_matmul.  An expert
- * id out of range skips its block (MOE_LORA_DEVERR_EXPERT_ID), a pair id that
- * is neither a pair nor the sentinel is skipped (MOE_LORA_DEVERR_PAIR_ID).
+ *   workspace: moe_fp8_grouped_workspace_bytes(M, topk, num_experts, K,
+ *     block_size) bytes, [device], 16-byte aligned; may be NULL when that is 0.
+ *     Its contents need no initialisation and are overwritten.
+ * Calls with at least 128 pairs an expert on average gather x into the order
+ * of the blocks (in the workspace) and run the kernel bound by the tensor
+ * cores; others the one bound by the weight's bytes.  Sizes and limits as for
+ * moe_align_block_size and moe_fp8_matmul.  An expert id out of range skips its
+ * block (MOE_LORA_DEVERR_EXPERT_ID), a pair id that is neither a pair nor the
+ * sentinel is skipped (MOE_LORA_DEVERR_PAIR_ID, as is a pair that follows 16 or
+ * more sentinels of its block).
  */
 int moe_fp8_grouped_matmul(const moe_lora_fp8 *x, int x_per_pair, long long ldx, const float *x_scales,
                            const moe_lora_fp8 *w, long long ldw, const float *w_scales, moe_lora_bf16 *y,
                            long long ldy, const float *topk_weights, const int32_t *sorted_token_ids,
                            const int32_t *expert_ids, const int32_t *num_tokens_post_padded, int M, int topk,
                            int num_experts, int K, int N, int block_size, int max_num_tokens_padded,
-                           int max_num_m_blocks, int32_t *err_flag, void *stream);
+                           int max_num_m_blocks, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                           void *stream);
+
+/* Bytes of workspace of a moe_fp8_grouped_matmul call with these sizes (0: none,
+ * or invalid sizes).  Host only. */
+size_t moe_fp8_grouped_workspace_bytes(int M, int topk, int num_experts, int K, int block_size);
 
 /*
  * moe_fp8_grouped_matmul_naive -- the same without an align: each pair f is a

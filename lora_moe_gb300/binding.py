@@ -91,7 +91,9 @@ def lib() -> ctypes.CDLL:
             L.moe_fp8_matmul.restype = I
             L.moe_fp8_matmul.argtypes = [P, Q, P, P, Q, P, P, Q, I, I, I, P, P]
             L.moe_fp8_grouped_matmul.restype = I
-            L.moe_fp8_grouped_matmul.argtypes = [P, I, Q, P, P, Q, P, P, Q, P, P, P, P, I, I, I, I, I, I, I, I, P, P]
+            L.moe_fp8_grouped_matmul.argtypes = [P, I, Q, P, P, Q, P, P, Q, P, P, P, P, I, I, I, I, I, I, I, I, P, S, P, P]
+            L.moe_fp8_grouped_workspace_bytes.restype = S
+            L.moe_fp8_grouped_workspace_bytes.argtypes = [I, I, I, I, I]
             L.moe_fp8_grouped_matmul_naive.restype = I
             L.moe_fp8_grouped_matmul_naive.argtypes = [P, I, Q, P, P, Q, P, P, Q, P, P, I, I, I, I, I, P, P]
             _lib = L
@@ -506,21 +508,43 @@ def _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair):
                               _dense(w_scales, _F32, "w_scales"), py, ldy, _dense(topk_weights, _F32, "topk_weights"))
 
 
+def fp8_grouped_workspace_bytes(M, topk, num_experts, K, block_size) -> int:
+    """Bytes of workspace of a moe_fp8_grouped_matmul call with these sizes."""
+    return lib().moe_fp8_grouped_workspace_bytes(M, topk, num_experts, K, block_size)
+
+
 def moe_fp8_grouped_matmul(x, x_scales, w, w_scales, y, sorted_token_ids, expert_ids, num_tokens_post_padded,
-                           block_size, topk_weights=None, x_per_pair=False, err_flag=None, stream=None):
+                           block_size, topk_weights=None, x_per_pair=False, workspace=None, err_flag=None,
+                           stream=None):
     """moe_fp8_matmul over a MoE layer's experts, on moe_align_block_size's
     blocks; see include/moe_lora.h.
 
     x: float8_e4m3fn [M, K] ([M*topk, K] with x_per_pair); w: float8_e4m3fn [E,
     N, K], w_scales: float32 [E, ceil(N / 128), ceil(K / 128)]; y: bf16 [M,
     topk, N], written in place for every pair of a block; topk_weights: float32
-    [M, topk] or None."""
+    [M, topk] or None.  workspace: a uint8 tensor of at least
+    fp8_grouped_workspace_bytes(...) bytes; without one, calls that need one
+    take it from torch's allocator."""
     M, topk, E, K, N, operands = _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair)
-    _check(lib().moe_fp8_grouped_matmul(
+    L = lib()
+    raw = _raw_stream(stream, y)
+    if workspace is None:
+        need = L.moe_fp8_grouped_workspace_bytes(M, topk, E, K, block_size)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
+            if stream is not None:
+                # its memory may be another tensor's once this stream is done with it; its last use may be
+                # unfinished on the current stream
+                side = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, y.device)
+                side.wait_stream(torch.cuda.current_stream(y.device))
+                workspace.record_stream(side)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(L.moe_fp8_grouped_matmul(
         *operands, _dense(sorted_token_ids, _I32, "sorted_token_ids"), _dense(expert_ids, _I32, "expert_ids"),
         _dense(num_tokens_post_padded, _I32, "num_tokens_post_padded"), M, topk, E, K, N, block_size,
-        sorted_token_ids.numel(), expert_ids.numel(), _dense(err_flag, _I32, "err_flag"), _raw_stream(stream, y)),
-        "moe_fp8_grouped_matmul")
+        sorted_token_ids.numel(), expert_ids.numel(),
+        None if workspace is None else _dense(workspace, workspace.dtype, "workspace"), nbytes,
+        _dense(err_flag, _I32, "err_flag"), raw), "moe_fp8_grouped_matmul")
 
 
 def moe_fp8_grouped_matmul_naive(x, x_scales, w, w_scales, y, topk_ids, topk_weights=None, x_per_pair=False,

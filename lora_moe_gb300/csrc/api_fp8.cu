@@ -33,7 +33,7 @@ int check_product(const Fp8Args &a, bool *empty) {
   return 0;
 }
 
-int grouped(Fp8Args a, Fp8Mode mode, int M, void *stream) {
+int grouped(Fp8Args a, Fp8Mode mode, int M, void *workspace, size_t workspace_bytes, void *stream) {
   if (M < 0 || a.topk < 1 || a.E < 1) return MOE_LORA_ERR_INVALID_ARG;
   if (a.E > kMaxExperts || a.topk > a.E) return MOE_LORA_ERR_UNSUPPORTED;
   const long long pairs = (long long)M * a.topk;
@@ -50,10 +50,17 @@ int grouped(Fp8Args a, Fp8Mode mode, int M, void *stream) {
     if (!ids[i] && (i == 3) == (mode == kFp8Naive)) return MOE_LORA_ERR_INVALID_ARG;
     if (!on(ids[i], 4)) return MOE_LORA_ERR_MISALIGNED;
   }
+  if (mode == kFp8Sorted) {
+    const size_t need = fp8_sorted_workspace(a);
+    if (need && (!workspace || workspace_bytes < need)) return MOE_LORA_ERR_WORKSPACE;
+    if (need && !on(workspace, 16)) return MOE_LORA_ERR_MISALIGNED;
+  }
   DeviceInfo dev;
   if (int st = current_device_info(&dev)) return st;
-  return launch_fp8_matmul(a, mode, dev, static_cast<cudaStream_t>(stream));
+  return launch_fp8_matmul(a, mode, workspace, dev, static_cast<cudaStream_t>(stream));
 }
+
+bool valid_block(int bs) { return bs == 16 || bs == 32 || bs == 64 || bs == 128; }
 
 }  // namespace
 
@@ -145,7 +152,22 @@ int moe_fp8_matmul(const moe_lora_fp8 *x, long long ldx, const float *x_scales, 
   a.NB = fp8_groups(N);
   DeviceInfo dev;
   if (int st = current_device_info(&dev)) return st;
-  return launch_fp8_matmul(a, kFp8Dense, dev, static_cast<cudaStream_t>(stream));
+  return launch_fp8_matmul(a, kFp8Dense, nullptr, dev, static_cast<cudaStream_t>(stream));
+}
+
+size_t moe_fp8_grouped_workspace_bytes(int M, int topk, int num_experts, int K, int block_size) {
+  if (M < 0 || topk < 1 || num_experts < 1 || num_experts > kMaxExperts || topk > num_experts || K < 1 ||
+      K > INT32_MAX - 128 || !valid_block(block_size))
+    return 0;
+  const long long cap = (long long)M * topk + (long long)num_experts * (block_size - 1);
+  if (cap > INT32_MAX / 2) return 0;
+  Fp8Args a = {};
+  a.pairs = M * topk;
+  a.E = num_experts;
+  a.K = K;
+  a.block = block_size;
+  a.max_blocks = (int)(cap / block_size);
+  return a.pairs == 0 ? 0 : fp8_sorted_workspace(a);
 }
 
 int moe_fp8_grouped_matmul(const moe_lora_fp8 *x, int x_per_pair, long long ldx, const float *x_scales,
@@ -153,9 +175,10 @@ int moe_fp8_grouped_matmul(const moe_lora_fp8 *x, int x_per_pair, long long ldx,
                            long long ldy, const float *topk_weights, const int32_t *sorted_token_ids,
                            const int32_t *expert_ids, const int32_t *num_tokens_post_padded, int M, int topk,
                            int num_experts, int K, int N, int block_size, int max_num_tokens_padded,
-                           int max_num_m_blocks, int32_t *err_flag, void *stream) {
+                           int max_num_m_blocks, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                           void *stream) {
   if (M < 0 || topk < 1 || num_experts < 1) return MOE_LORA_ERR_INVALID_ARG;
-  if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128) return MOE_LORA_ERR_UNSUPPORTED;
+  if (!valid_block(block_size)) return MOE_LORA_ERR_UNSUPPORTED;
   const long long cap = (long long)M * topk + (long long)num_experts * (block_size - 1);
   if (cap > INT32_MAX / 2) return MOE_LORA_ERR_UNSUPPORTED;
   if (max_num_tokens_padded < cap || (long long)max_num_m_blocks * block_size < cap) return MOE_LORA_ERR_INVALID_ARG;
@@ -178,10 +201,9 @@ int moe_fp8_grouped_matmul(const moe_lora_fp8 *x, int x_per_pair, long long ldx,
   a.K = K;
   a.N = N;
   a.block = block_size;
-  // whole blocks that lie inside both arrays
-  a.max_blocks = max_num_tokens_padded / block_size < max_num_m_blocks ? max_num_tokens_padded / block_size : max_num_m_blocks;
+  a.max_blocks = (int)(cap / block_size);   // an align's blocks are whole ones
   a.err = err_flag;
-  return grouped(a, kFp8Sorted, M, stream);
+  return grouped(a, kFp8Sorted, M, workspace, workspace_bytes, stream);
 }
 
 int moe_fp8_grouped_matmul_naive(const moe_lora_fp8 *x, int x_per_pair, long long ldx, const float *x_scales,
@@ -206,7 +228,7 @@ int moe_fp8_grouped_matmul_naive(const moe_lora_fp8 *x, int x_per_pair, long lon
   a.N = N;
   a.block = 16;
   a.err = err_flag;
-  return grouped(a, kFp8Naive, M, stream);
+  return grouped(a, kFp8Naive, M, nullptr, 0, stream);
 }
 
 }  // extern "C"

@@ -45,20 +45,30 @@ struct Fp8Cfg {
   int smem_bytes;
 };
 
-// The blocks of a call: on the device for the sorted arrays.
-template <int MODE>
-__device__ __forceinline__ int num_blocks(const Fp8Args &p, int bt) {
-  if (MODE == kFp8Dense) return (p.pairs + bt - 1) / bt;
-  if (MODE == kFp8Naive) return p.pairs;
-  const int n = __ldg(p.num_tokens_post_padded) / bt;
+// Blocks that the sorted arrays hold.
+__device__ __forceinline__ int num_blocks(const Fp8Args &p) {
+  const int n = __ldg(p.num_tokens_post_padded) / p.block;
   return n < 0 ? 0 : (n > p.max_blocks ? p.max_blocks : n);
 }
-// Expert of block b, or -1 where the id is out of range (the block is skipped).
+// The narrow kernel's units of bt positions: a block of the sorted arrays is
+// `block / bt` of them.
 template <int MODE>
-__device__ __forceinline__ int block_expert(const Fp8Args &p, int b) {
+__device__ __forceinline__ int num_units(const Fp8Args &p, int bt) {
+  if (MODE == kFp8Dense) return (p.pairs + bt - 1) / bt;
+  if (MODE == kFp8Naive) return p.pairs;
+  return num_blocks(p) * (p.block / bt);
+}
+constexpr int kBadExpert = -1, kNoPairs = -2;
+// Expert of unit b; negative where the unit is skipped: its id is out of
+// range, or its first position holds the sentinel and it does not begin a
+// block (a block's pairs precede its sentinels).
+template <int MODE>
+__device__ __forceinline__ int block_expert(const Fp8Args &p, int b, int bt) {
   if (MODE == kFp8Dense) return 0;
-  const int e = MODE == kFp8Sorted ? __ldg(p.expert_ids + b) : __ldg(p.topk_ids + b);
-  return (unsigned)e < (unsigned)p.E ? e : -1;
+  const int e = MODE == kFp8Sorted ? __ldg(p.expert_ids + b / (p.block / bt)) : __ldg(p.topk_ids + b);
+  if ((unsigned)e >= (unsigned)p.E) return kBadExpert;
+  if (MODE == kFp8Sorted && b % (p.block / bt) && __ldg(p.sorted_token_ids + (size_t)b * bt) == p.pairs) return kNoPairs;
+  return e;
 }
 // Pair at position t of block b, or -1.  `bt` positions a block.
 template <int MODE>
@@ -113,7 +123,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     fp8_narrow_kernel(const __grid_constant__ Fp8Maps maps, const Fp8Args p, const Fp8Cfg cfg) {
   using C = Narrow<BT>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   NarrowCtrl &ctl = *reinterpret_cast<NarrowCtrl *>(smem + cfg.off_ctrl);
   float *scales = reinterpret_cast<float *>(smem + cfg.off_scale);
   volatile int *abort = &ctl.abort;
@@ -154,7 +164,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     cluster_wait();
   }
   const uint32_t tmem = ctl.tmem;
-  const int items = num_blocks<MODE>(p, BT) * cfg.nt;
+  const int items = num_units<MODE>(p, BT) * cfg.nt;
   const int kb0 = (int)((long long)p.KB * rank / cs), kb1 = (int)((long long)p.KB * (rank + 1) / cs);
 
   if (warp == 0) {
@@ -162,7 +172,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     for (int it = cid; it < items; it += nclusters) {
-      const int b = it / cfg.nt, nt = it - b * cfg.nt, e = block_expert<MODE>(p, b);
+      const int b = it / cfg.nt, nt = it - b * cfg.nt, e = block_expert<MODE>(p, b, BT);
       if (e < 0) continue;
       int row[4];
       bool mine = false;   // lane i gathers rows 4i .. 4i+3; groups without a pair are left as they are
@@ -183,7 +193,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       for (int kb = kb0; kb < kb1; ++kb) {
         mbar_wait(&ctl.empty[s], ph ^ 1, abort, p.err);
         uint8_t *st = smem + (size_t)s * C::kStage;
-        if (lane == 0) {
+        if (elect_one()) {
           mbar_arrive_expect_tx(&ctl.full[s], kTileBytes + groups * 4 * kFp8Group);
           tma_load_3d(st, &maps.w, kb * kFp8Group, nt * kRows, e, &ctl.full[s]);
           if (MODE == kFp8Dense) tma_load_2d(st + kTileBytes, &maps.x, kb * kFp8Group, b * BT, &ctl.full[s]);
@@ -196,37 +206,41 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------- MMA: each group of 128 columns into an accumulator of its own
-    if (lane == 0) {
-      constexpr uint32_t idesc = make_idesc_e4m3(kRows, BT);
-      int s = 0, a = 0;
-      uint32_t ph = 0, aph = 0;
-      for (int it = cid; it < items; it += nclusters) {
-        if (block_expert<MODE>(p, it / cfg.nt) < 0) continue;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          mbar_wait(&ctl.tempty[a], aph ^ 1, abort, p.err);
-          mbar_wait(&ctl.full[s], ph, abort, p.err);
-          tc_fence_after();
-          const uint32_t st = smem_addr(smem + (size_t)s * C::kStage);
+    constexpr uint32_t idesc = make_idesc_e4m3(kRows, BT);
+    const uint64_t desc0 = make_sdesc_sw128(smem_addr(smem));   // (addresses in units of 16 bytes)
+    int s = 0, a = 0;
+    uint32_t ph = 0, aph = 0;
+    for (int it = cid; it < items; it += nclusters) {
+      if (block_expert<MODE>(p, it / cfg.nt, BT) < 0) continue;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        mbar_wait(&ctl.tempty[a], aph ^ 1, abort, p.err);
+        mbar_wait(&ctl.full[s], ph, abort, p.err);
+        tc_fence_after();
+        const uint64_t dw = desc0 + s * (C::kStage >> 4), dx = dw + (kTileBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kFp8Group / 32; ++k)
-            tc_mma_f8(tmem + a * BT, make_sdesc_sw128(st + k * 32), make_sdesc_sw128(st + kTileBytes + k * 32), idesc,
-                      k > 0);
+          for (int k = 0; k < kFp8Group / 32; ++k) tc_mma_f8(tmem + a * BT, dw + k * 2, dx + k * 2, idesc, k > 0);
           tc_commit(&ctl.empty[s]);
           tc_commit(&ctl.tfull[a]);
-          if (++s == cfg.stages) { s = 0; ph ^= 1; }
-          if (++a == C::kBufs) { a = 0; aph ^= 1; }
         }
+        __syncwarp();
+        if (++s == cfg.stages) { s = 0; ph ^= 1; }
+        if (++a == C::kBufs) { a = 0; aph ^= 1; }
       }
     }
-    __syncwarp();
   } else if (warp == 2) {
     // ---------------- scales: a row of BT + 1 for each group
     int s = 0;
     uint32_t ph = 0;
     for (int it = cid; it < items; it += nclusters) {
-      const int b = it / cfg.nt, nt = it - b * cfg.nt, e = block_expert<MODE>(p, b);
+      const int b = it / cfg.nt, nt = it - b * cfg.nt, e = block_expert<MODE>(p, b, BT);
       if (e < 0) {
-        if (lane == 0 && nt == 0 && rank == 0) flag_error(p.err, MOE_LORA_DEVERR_EXPERT_ID);
+        if (nt == 0 && rank == 0) {
+          if (e == kBadExpert && lane == 0) flag_error(p.err, MOE_LORA_DEVERR_EXPERT_ID);
+          if (e == kNoPairs)   // a pair after a sentinel
+            for (int t = lane; t < BT; t += 32)
+              if (__ldg(p.sorted_token_ids + (size_t)b * BT + t) != p.pairs) flag_error(p.err, MOE_LORA_DEVERR_PAIR_ID);
+        }
         continue;
       }
       constexpr int kPer = (BT + 31) / 32;
@@ -263,7 +277,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     uint32_t rph = 0;
     for (int it = cid; it < items; it += nclusters) {
       const int b = it / cfg.nt, nt = it - b * cfg.nt;
-      if (block_expert<MODE>(p, b) < 0) continue;
+      if (block_expert<MODE>(p, b, BT) < 0) continue;
       float acc[BT];
 #pragma unroll
       for (int c = 0; c < BT; ++c) acc[c] = 0.f;
@@ -365,198 +379,331 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
 
 // ------------------------------------------------------------------ wide
 
+// The rows of the sorted pairs, gathered once into the order of
+// sorted_token_ids: the wide kernel reads each of them N / 256 times, and TMA
+// fetches gathered rows four at a time at 80 clk each, cp.async by the
+// kernel's own warps at 40 % of the tensor cores' time.  CTA 0 also lists the
+// tiles of at most 256 rows of one expert.
+struct WideTile {
+  int row0, rows, expert, pad;
+};
+constexpr int kGatherThreads = 256;
+constexpr int kTileRows = 256;
+
+struct WideSpace {   // offsets into the workspace
+  size_t tiles, x, bytes;
+  long long rows, ld;   // capacity of the sorted arrays in whole blocks; bytes from row to row
+};
+WideSpace wide_space(long long rows, int K) {
+  WideSpace w;
+  w.rows = rows;
+  w.ld = (long long)fp8_groups(K) * kFp8Group;
+  w.tiles = 0;
+  // at most a tile for each of the sorted arrays' smallest blocks, and the count
+  w.x = ((size_t)(rows / 16 + 1) * sizeof(WideTile) + sizeof(WideTile) + 127) / 128 * 128;
+  w.bytes = w.x + (size_t)rows * w.ld;
+  return w;
+}
+
+__global__ void __launch_bounds__(kGatherThreads)
+    fp8_gather_kernel(const Fp8Args p, WideTile *tiles, uint8_t *xg, long long ld) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bs = p.block;
+  const int nb = num_blocks(p);
+  if (blockIdx.x == 0) {
+    // Tile list.  A block heads a tile when the blocks before it of the same
+    // expert are a multiple of 256 rows: blocks of one expert are neighbours.
+    __shared__ int warp_last[kGatherThreads / 32], warp_heads[kGatherThreads / 32], carry_first, carry_heads;
+    if (tid == 0) carry_first = carry_heads = 0;
+    __syncthreads();
+    const int per_tile = kTileRows / bs;
+    for (int base = 0; base < nb; base += kGatherThreads) {
+      const int b = base + tid;
+      const int e = b < nb ? __ldg(p.expert_ids + b) : -1;
+      const bool first = b < nb && (b == 0 || __ldg(p.expert_ids + b - 1) != e);
+      int run = first ? b : -1;   // first block of b's run: the last `first` at or before b
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, run, d);
+        if (lane >= d) run = max(run, o);
+      }
+      if (lane == 31) warp_last[warp] = run;
+      __syncthreads();
+      int before = carry_first;
+      for (int w = 0; w < warp; ++w) before = max(before, warp_last[w]);
+      run = max(run, before);
+      const bool good = (unsigned)e < (unsigned)p.E;
+      const bool head = b < nb && good && (b - run) % per_tile == 0;
+      if (b < nb && !good) flag_error(p.err, MOE_LORA_DEVERR_EXPERT_ID);
+      const uint32_t heads = __ballot_sync(0xFFFFFFFFu, head);
+      if (lane == 31) warp_heads[warp] = __popc(heads);
+      __syncthreads();
+      int at = carry_heads + __popc(heads & ((1u << lane) - 1));
+      for (int w = 0; w < warp; ++w) at += warp_heads[w];
+      if (head) {
+        int n = 1;
+        while (n < per_tile && b + n < nb && __ldg(p.expert_ids + b + n) == e) ++n;
+        tiles[1 + at] = {b * bs, n * bs, e, 0};
+      }
+      __syncthreads();
+      if (tid == 0) {
+        for (int w = 0; w < kGatherThreads / 32; ++w) {
+          carry_first = max(carry_first, warp_last[w]);
+          carry_heads += warp_heads[w];
+        }
+      }
+      __syncthreads();
+    }
+    if (tid == 0) tiles[0] = {carry_heads, 0, 0, 0};
+  }
+  // one warp a row
+  const long long warps = (long long)gridDim.x * (kGatherThreads / 32);
+  for (long long r = (long long)blockIdx.x * (kGatherThreads / 32) + warp; r < (long long)nb * bs; r += warps) {
+    const int f = __ldg(p.sorted_token_ids + r);
+    if ((unsigned)f >= (unsigned)p.pairs) {
+      if (f != p.pairs && lane == 0) flag_error(p.err, MOE_LORA_DEVERR_PAIR_ID);
+      continue;
+    }
+    const int xr = pair_row<kFp8Sorted>(p, f);
+    const uint8_t *src = p.x + (size_t)xr * p.ldx;
+    uint8_t *dst = xg + (size_t)r * ld;
+    const int whole = p.K / 16;
+    for (int c = lane; c < whole; c += 32)
+      *reinterpret_cast<uint4 *>(dst + c * 16) = __ldg(reinterpret_cast<const uint4 *>(src + c * 16));
+    for (int c = whole * 16 + lane; c < p.K; c += 32) dst[c] = __ldg(src + c);
+  }
+}
+
+// The wide kernel: pairs of CTAs (cta_group::2), 256 rows by 256 output
+// columns.  Each CTA holds 128 of the rows and half of the weight's columns in
+// shared memory and 128 x 256 of the accumulators in tensor memory.
 constexpr int kWideThreads = 384;
 constexpr int kWideN = 256;
-constexpr int kWideStage = kTileBytes + kWideN * kFp8Group;   // 48 KB
-constexpr int kWideStages = 4;
+constexpr int kHalf = kWideN / 2;
+constexpr int kWideStage = 2 * kTileBytes;       // 128 rows, and 128 columns of the weight
+constexpr int kWideStages = 6;
+constexpr int kWideOut = 32 * 128;               // an epilogue warp's rows on their way out: 32 rows of 64 bf16
 constexpr int kWideRegsIssue = 56, kWideRegsEpilogue = 216;   // registers a thread: loading and MMA warps, epilogue warps
 
 struct WideCtrl {
   uint64_t full[kWideStages], empty[kWideStages];
-  uint64_t tfull[2], tempty[2];
+  uint64_t tfull[4], tempty[4];
   uint32_t tmem;
   int abort;
 };
 
+struct WideArgs {
+  const WideTile *tiles;   // sorted: count, then the tiles
+};
+
 template <int MODE>
 __global__ void __launch_bounds__(kWideThreads, 1)
-    fp8_wide_kernel(const __grid_constant__ Fp8Maps maps, const Fp8Args p, const Fp8Cfg cfg) {
+    fp8_wide_kernel(const __grid_constant__ Fp8Maps maps, const Fp8Args p, const WideArgs g, const Fp8Cfg cfg) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   WideCtrl &ctl = *reinterpret_cast<WideCtrl *>(smem + cfg.off_ctrl);
   volatile int *abort = &ctl.abort;
-  constexpr int BT = kRows;
+  const int rank = blockIdx.x & 1;   // rank 0 issues the pair's MMAs
 
   if (tid == 0) {
     for (int s = 0; s < kWideStages; ++s) {
       mbar_init(&ctl.full[s], 1);
       mbar_init(&ctl.empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&ctl.tfull[s], 1);
-      mbar_init(&ctl.tempty[s], 8);
+      mbar_init(&ctl.tempty[s], 8);   // four epilogue warps of each CTA
     }
     ctl.abort = 0;
     fence_barrier_init();
     prefetch_tensor_map(&maps.w);
     prefetch_tensor_map(&maps.x);
   }
-  if (warp == 1) {
-    tmem_alloc(&ctl.tmem, 512);
-    tmem_relinquish();
-  }
+  if (warp == 1) tmem_alloc_pair(&ctl.tmem, 512);
   tc_fence_before();
   __syncthreads();
+  cluster_arrive_release();
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
-  const int nb = num_blocks<MODE>(p, BT);
-  const long long items = (long long)nb * cfg.nt;   // blocks fastest: CTAs at work share the weight's tiles
+  const int ntiles = MODE == kFp8Dense ? (p.pairs + kTileRows - 1) / kTileRows : __ldg(&g.tiles[0].row0);
+  const int items = ntiles * cfg.nt;   // rows fastest: pairs at work share the weight's columns
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  auto tile = [&](int t) {
+    if (MODE == kFp8Dense) return WideTile{t * kTileRows, min(kTileRows, p.pairs - t * kTileRows), 0, 0};
+    const int4 v = __ldg(reinterpret_cast<const int4 *>(g.tiles) + 1 + t);
+    return WideTile{v.x, v.y, v.z, 0};
+  };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideRegsIssue));
     if (warp == 0) {
+      // ---------------- operands: this CTA's rows, and its 64 of each 128 columns
+      const uint32_t full0 = cluster_map(smem_addr(&ctl.full[0]), 0);   // rank 0's
       int s = 0;
       uint32_t ph = 0;
-      for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-        const int nt = (int)(it / nb), b = (int)(it - (long long)nt * nb), e = block_expert<MODE>(p, b);
-        if (e < 0) continue;
-        int row[4];
-        bool mine = false;
-        if (MODE != kFp8Dense) {
-          int some = -1;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int f = block_pair<MODE>(p, b, lane * 4 + i, BT);
-            row[i] = f < 0 ? -1 : pair_row<MODE>(p, f);
-            if (row[i] >= 0) some = row[i];
-          }
-          mine = some >= 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (row[i] < 0) row[i] = some;
-        }
-        const int groups = MODE == kFp8Dense ? BT / 4 : __popc(__ballot_sync(0xFFFFFFFFu, mine));
+      for (int it = first; it < items; it += step) {
+        const int nt = it / ntiles;
+        const WideTile t = tile(it - nt * ntiles);
+        const bool have = t.rows > rank * kRows;
+        const uint32_t bytes = 2 * kTileBytes + (t.rows > kRows ? 2 : 1) * kTileBytes;
         for (int kb = 0; kb < p.KB; ++kb) {
           mbar_wait(&ctl.empty[s], ph ^ 1, abort, p.err);
           uint8_t *st = smem + (size_t)s * kWideStage;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&ctl.full[s], kWideN * kFp8Group + groups * 4 * kFp8Group);
-            tma_load_3d(st + kTileBytes, &maps.w, kb * kFp8Group, nt * kWideN, e, &ctl.full[s]);
-            tma_load_3d(st + 2 * kTileBytes, &maps.w, kb * kFp8Group, nt * kWideN + kRows, e, &ctl.full[s]);
-            if (MODE == kFp8Dense) tma_load_2d(st, &maps.x, kb * kFp8Group, b * BT, &ctl.full[s]);
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
+            if (have) tma_load_2d_pair(st, &maps.x, kb * kFp8Group, t.row0 + rank * kRows, full0 + s * 8);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d_pair(st + kTileBytes + h * (kTileBytes / 2), &maps.w, kb * kFp8Group,
+                               nt * kWideN + h * kHalf + rank * (kHalf / 2), t.expert, full0 + s * 8);
           }
           __syncwarp();
-          if (MODE != kFp8Dense && mine)
-            tma_gather4(st + lane * 4 * kFp8Group, &maps.x, kb * kFp8Group, row, &ctl.full[s]);
           if (++s == kWideStages) { s = 0; ph ^= 1; }
         }
       }
-    } else if (warp == 1 && lane == 0) {
-      constexpr uint32_t idesc = make_idesc_e4m3(kRows, kWideN);
+    } else if (warp == 1 && rank == 0) {
+      // ---------------- MMA, for both CTAs: each half of the columns into an accumulator of its own
+      constexpr uint32_t idesc = make_idesc_e4m3(2 * kRows, kHalf);
+      const uint64_t desc0 = make_sdesc_sw128(smem_addr(smem));   // (addresses in units of 16 bytes)
       int s = 0, a = 0;
       uint32_t ph = 0, aph = 0;
-      for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-        if (block_expert<MODE>(p, (int)(it % nb)) < 0) continue;
+      for (int it = first; it < items; it += step) {
         for (int kb = 0; kb < p.KB; ++kb) {
-          mbar_wait(&ctl.tempty[a], aph ^ 1, abort, p.err);
           mbar_wait(&ctl.full[s], ph, abort, p.err);
-          tc_fence_after();
-          const uint32_t st = smem_addr(smem + (size_t)s * kWideStage);
+          const uint64_t dx = desc0 + s * (kWideStage >> 4), dw = dx + (kTileBytes >> 4);
 #pragma unroll
-          for (int k = 0; k < kFp8Group / 32; ++k)
-            tc_mma_f8(tmem + a * kWideN, make_sdesc_sw128(st + k * 32), make_sdesc_sw128(st + kTileBytes + k * 32),
-                      idesc, k > 0);
-          tc_commit(&ctl.empty[s]);
-          tc_commit(&ctl.tfull[a]);
+          for (int h = 0; h < 2; ++h) {
+            mbar_wait(&ctl.tempty[a + h], aph ^ 1, abort, p.err);
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < kFp8Group / 32; ++k)
+                tc_mma_f8_pair(tmem + (a + h) * kHalf, dx + k * 2, dw + h * (kTileBytes >> 5) + k * 2, idesc, k > 0);
+              tc_commit_pair(&ctl.tfull[a + h]);
+              if (h == 1) tc_commit_pair(&ctl.empty[s]);
+            }
+            __syncwarp();
+          }
           if (++s == kWideStages) { s = 0; ph ^= 1; }
-          if (++a == 2) { a = 0; aph ^= 1; }
+          a ^= 2;
+          if (a == 0) aph ^= 1;
         }
-      }
-    } else if (warp == 2 && MODE == kFp8Sorted) {
-      // the ids that are out of range, reported once
-      for (int b = blockIdx.x; b < nb; b += gridDim.x) {
-        if (block_expert<MODE>(p, b) < 0) {
-          if (lane == 0) flag_error(p.err, MOE_LORA_DEVERR_EXPERT_ID);
-          continue;
-        }
-        for (int t = lane; t < BT; t += 32) flag_block<MODE>(p, b, t, BT);
       }
     }
-    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWideRegsEpilogue));
-    // this thread's pair, one half (128 columns: one scale) of the output tile
+    // ---------------- epilogue: this thread's row, one half (128 columns: one scale) of the output tile
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t lane_addr = tmem + ((uint32_t)quarter << 21) + half * 128;
+    const uint32_t lane_addr = tmem + ((uint32_t)quarter << 21) + half * kHalf;
+    const uint32_t tempty0 = cluster_map(smem_addr(&ctl.tempty[half]), 0);   // rank 0's
     int a = 0;
     uint32_t aph = 0;
-    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-      const int nt = (int)(it / nb), b = (int)(it - (long long)nt * nb), e = block_expert<MODE>(p, b);
-      if (e < 0) continue;
-      const int f = block_pair<MODE>(p, b, quarter * 32 + lane, BT);
+    for (int it = first; it < items; it += step) {
+      const int nt = it / ntiles;
+      const WideTile t = tile(it - nt * ntiles);
+      const int r = rank * kRows + quarter * 32 + lane;   // row of the tile
+      int f = -1;
+      if (r < t.rows) f = MODE == kFp8Dense ? t.row0 + r : __ldg(p.sorted_token_ids + t.row0 + r);
+      if ((unsigned)f >= (unsigned)p.pairs) f = -1;
       const int nblk = nt * 2 + half;
       const float *sx = f < 0 ? nullptr : p.x_scales + (size_t)pair_row<MODE>(p, f) * p.KB;
-      const float *sw = nblk < p.NB ? p.w_scales + ((size_t)e * p.NB + nblk) * p.KB : nullptr;
-      float acc[128];
+      const float *sw = nblk < p.NB ? p.w_scales + ((size_t)t.expert * p.NB + nblk) * p.KB : nullptr;
+      f32x2 acc[64];
 #pragma unroll
-      for (int c = 0; c < 128; ++c) acc[c] = 0.f;
-      float sx0 = sx ? __ldg(sx) : 0.f, sw0 = sw ? __ldg(sw) : 0.f;
+      for (int c = 0; c < 64; ++c) acc[c] = 0;
+      // the scales of the next two groups are on their way
+      auto load = [](const float *s, int kb, int n) { return s && kb < n ? __ldg(s + kb) : 0.f; };
+      float sc0 = load(sx, 0, p.KB) * load(sw, 0, p.KB), sx1 = load(sx, 1, p.KB), sw1 = load(sw, 1, p.KB);
       for (int kb = 0; kb < p.KB; ++kb) {
-        const float sc = sx0 * sw0;
-        if (kb + 1 < p.KB) {
-          sx0 = sx ? __ldg(sx + kb + 1) : 0.f;
-          sw0 = sw ? __ldg(sw + kb + 1) : 0.f;
-        }
-        mbar_wait(&ctl.tfull[a], aph, abort, p.err);
+        const f32x2 sc2 = f2_pack(sc0, sc0);
+        const float sx2 = load(sx, kb + 2, p.KB), sw2 = load(sw, kb + 2, p.KB);
+        mbar_wait(&ctl.tfull[a + half], aph, abort, p.err);
         tc_fence_after();
+        const uint32_t src = lane_addr + a * kHalf;
+        // the next 32 columns are on their way while these are added
+        uint32_t v[2][32];
+        tmem_ld32(src, v[0]);
 #pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          uint32_t v[32];
-          tmem_ld32(lane_addr + a * kWideN + c0, v);
+        for (int q = 0; q < 4; ++q) {
           tc_wait_ld();
-          tc_pin(v);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) acc[c0 + c] += __uint_as_float(v[c]) * sc;
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.tempty[a]);
-        if (++a == 2) { a = 0; aph ^= 1; }
-      }
-      if (f >= 0) {
-        const float w = pair_weight<MODE>(p, f);
-        const int n0 = nblk * kRows;
-        uint16_t *dst = p.y + (size_t)f * p.ldy + n0;
-        if (n0 + 128 <= p.N && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
-#pragma unroll
-          for (int c = 0; c < 128; c += 8) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(acc[c + 2 * i + 1] * w), "f"(acc[c + 2 * i] * w));
-            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[0], o[1], o[2], o[3]);
+          tc_pin(v[q & 1]);
+          if (q < 3) {
+            tmem_ld32(src + (q + 1) * 32, v[(q + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_relaxed(tempty0 + a * 8);   // (only tensor memory is handed back)
           }
-        } else {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (n0 + c < p.N) dst[c] = float_to_bf16_bits(acc[c] * w);
+          for (int c = 0; c < 16; ++c)
+            acc[q * 16 + c] = ffma2(f2_pack(__uint_as_float(v[q & 1][2 * c]), __uint_as_float(v[q & 1][2 * c + 1])), sc2,
+                                    acc[q * 16 + c]);
+        }
+        sc0 = sx1 * sw1;
+        sx1 = sx2;
+        sw1 = sw2;
+        a ^= 2;
+        if (a == 0) aph ^= 1;
+      }
+      // Out through shared memory, 64 columns at a time, so that 8 lanes write
+      // 128 consecutive bytes of one row (a lane writing its own row touches 32
+      // lines an instruction: 4096 clk a tile).
+      const float w = f < 0 ? 0.f : pair_weight<MODE>(p, f);
+      const int n0 = nblk * kRows;
+      const bool vec = (p.ldy & 7) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
+      uint8_t *out = smem + kWideStages * kWideStage + (warp - 4) * kWideOut;
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            f2_unpack(acc[part * 32 + c * 4 + i], lo, hi);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(hi * w), "f"(lo * w));
+          }
+          *reinterpret_cast<uint4 *>(out + lane * 128 + ((c ^ (lane & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        __syncwarp();
+        const int chunk = lane & 7, n = n0 + part * 64 + chunk * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 4 + (lane >> 3);
+          const int fr = __shfl_sync(0xFFFFFFFFu, f, r);
+          const uint4 o = *reinterpret_cast<const uint4 *>(out + r * 128 + ((chunk ^ (r & 7)) << 4));
+          if (fr < 0 || n >= p.N) continue;
+          uint16_t *dst = p.y + (size_t)fr * p.ldy + n;
+          if (vec && n + 8 <= p.N) {
+            *reinterpret_cast<uint4 *>(dst) = o;
+          } else {
+            const uint32_t v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (n + j < p.N) dst[j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+          }
         }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
+  cluster_arrive_release();   // the pair's accumulators are read, and no barrier of the peer is used any more
+  cluster_wait();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
 // ------------------------------------------------------------------ launch
 
-int make_maps(const Fp8Args &a, int x_box_rows, Fp8Maps *maps) {
-  if (int st = stream::encode_u8(&maps->w, a.w, 3, a.K, a.N, a.E, a.ldw, (uint64_t)a.ldw * a.N, kRows)) return st;
-  return stream::encode_u8(&maps->x, a.x, 2, a.K, a.rows, 1, a.ldx, 0, x_box_rows);
+int make_maps(const Fp8Args &a, const uint8_t *x, long long rows, long long ldx, int w_box_rows, int x_box_rows,
+              Fp8Maps *maps) {
+  if (int st = stream::encode_u8(&maps->w, a.w, 3, a.K, a.N, a.E, a.ldw, (uint64_t)a.ldw * a.N, w_box_rows)) return st;
+  return stream::encode_u8(&maps->x, x, 2, a.K, rows, 1, ldx, 0, x_box_rows);
 }
 
 // The wide kernel's warps trade registers after the launch: the shares must
@@ -568,9 +715,9 @@ bool register_shares_fit(Kernel kernel) {
   return attr.numRegs * kWideThreads >= 128 * kWideRegsIssue + 256 * kWideRegsEpilogue;
 }
 
-template <typename Kernel>
-int launch(Kernel kernel, const Fp8Maps &maps, const Fp8Args &a, const Fp8Cfg &cfg, unsigned grid, int threads,
-           cudaStream_t stream) {
+template <typename... Params, typename... Args>
+int launch(void (*kernel)(Params...), const Fp8Cfg &cfg, unsigned grid, int threads, cudaStream_t stream,
+           const Args &...args) {
   if (cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.smem_bytes) !=
       cudaSuccess)
     return MOE_LORA_ERR_LAUNCH;
@@ -586,14 +733,14 @@ int launch(Kernel kernel, const Fp8Maps &maps, const Fp8Args &a, const Fp8Cfg &c
   attr[0].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, kernel, maps, a, cfg) == cudaSuccess ? 0 : MOE_LORA_ERR_LAUNCH;
+  return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? 0 : MOE_LORA_ERR_LAUNCH;
 }
 
 // Upper bound of the call's blocks.
 long long block_bound(const Fp8Args &a, Fp8Mode mode, int bt) {
   if (mode == kFp8Dense) return ((long long)a.pairs + bt - 1) / bt;
   if (mode == kFp8Naive) return a.pairs;
-  return std::min<long long>(a.max_blocks, fused_block_bound(a.pairs, 1, a.E, 1, bt));
+  return std::min<long long>((long long)a.max_blocks * (a.block / bt), fused_block_bound(a.pairs, 1, a.E, 1, bt));
 }
 
 template <int BT, int MODE>
@@ -616,45 +763,71 @@ int launch_narrow(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) 
   cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(NarrowCtrl);
   const unsigned clusters = (unsigned)std::min<long long>(items, dev.sm_count / cs);
   Fp8Maps maps;
-  if (int st = make_maps(a, MODE == kFp8Dense ? BT : 1, &maps)) return st;
-  return launch(fp8_narrow_kernel<BT, MODE>, maps, a, cfg, clusters * cs, kNarrowThreads, stream);
+  if (int st = make_maps(a, a.x, a.rows, a.ldx, kRows, MODE == kFp8Dense ? BT : 1, &maps)) return st;
+  return launch(fp8_narrow_kernel<BT, MODE>, cfg, clusters * cs, kNarrowThreads, stream, maps, a, cfg);
 }
 
 template <int MODE>
-int launch_wide(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) {
+int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaStream_t stream) {
   Fp8Cfg cfg = {};
   cfg.nt = (a.N + kWideN - 1) / kWideN;
-  const long long items = block_bound(a, (Fp8Mode)MODE, kRows) * cfg.nt;
-  if (items <= 0) return 0;
-  cfg.cluster = 1;
+  const long long rows = (long long)a.max_blocks * a.block;
+  const long long tiles = MODE == kFp8Dense ? ((long long)a.pairs + kTileRows - 1) / kTileRows
+                                            : a.pairs / kTileRows + std::min(a.E, a.pairs);
+  if (tiles <= 0) return 0;
+  cfg.cluster = 2;
   cfg.stages = kWideStages;
-  cfg.off_ctrl = kWideStages * kWideStage;
+  cfg.off_ctrl = kWideStages * kWideStage + 8 * kWideOut;
   cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(WideCtrl);
   static const bool fits = register_shares_fit(fp8_wide_kernel<MODE>);
   if (!fits) return MOE_LORA_ERR_LAUNCH;
   Fp8Maps maps;
-  if (int st = make_maps(a, MODE == kFp8Dense ? kRows : 1, &maps)) return st;
-  return launch(fp8_wide_kernel<MODE>, maps, a, cfg, (unsigned)std::min<long long>(items, dev.sm_count), kWideThreads,
-                stream);
+  WideArgs g = {};
+  if (MODE == kFp8Dense) {
+    if (int st = make_maps(a, a.x, a.rows, a.ldx, kHalf / 2, kRows, &maps)) return st;
+  } else {
+    const WideSpace w = wide_space(rows, a.K);
+    uint8_t *base = static_cast<uint8_t *>(workspace);
+    g.tiles = reinterpret_cast<WideTile *>(base + w.tiles);
+    if (int st = make_maps(a, base + w.x, rows, w.ld, kHalf / 2, kRows, &maps)) return st;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)std::min<long long>((rows + 7) / 8, dev.sm_count * 8ll), 1, 1);
+    lc.blockDim = dim3(kGatherThreads, 1, 1);
+    lc.stream = stream;
+    if (cudaLaunchKernelEx(&lc, fp8_gather_kernel, a, reinterpret_cast<WideTile *>(base + w.tiles),
+                           base + w.x, w.ld) != cudaSuccess)
+      return MOE_LORA_ERR_LAUNCH;
+  }
+  const long long items = tiles * cfg.nt;   // (the sorted arrays' own tiles are no more, but for entries that no align writes)
+  if (items > INT32_MAX / 16) return MOE_LORA_ERR_UNSUPPORTED;
+  const unsigned grid = 2 * (unsigned)std::min<long long>(items, dev.sm_count / 2);
+  return launch(fp8_wide_kernel<MODE>, cfg, grid, kWideThreads, stream, maps, a, g, cfg);
 }
 
 }  // namespace
 
-int launch_fp8_matmul(const Fp8Args &a, Fp8Mode mode, const DeviceInfo &dev, cudaStream_t s) {
+// The wide kernel from 128 pairs an expert on (on average): below that a call
+// is bound by the weight's bytes, and tiles of 256 rows would be half empty.
+bool fp8_sorted_is_wide(const Fp8Args &a) { return a.pairs >= 128ll * a.E; }
+
+size_t fp8_sorted_workspace(const Fp8Args &a) {
+  return fp8_sorted_is_wide(a) ? wide_space((long long)a.max_blocks * a.block, a.K).bytes : 0;
+}
+
+int launch_fp8_matmul(const Fp8Args &a, Fp8Mode mode, void *workspace, const DeviceInfo &dev, cudaStream_t s) {
   if (mode == kFp8Naive) return launch_narrow<16, kFp8Naive>(a, dev, s);
   if (mode == kFp8Sorted) {
-    switch (a.block) {
-      case 16: return launch_narrow<16, kFp8Sorted>(a, dev, s);
-      case 32: return launch_narrow<32, kFp8Sorted>(a, dev, s);
-      case 64: return launch_narrow<64, kFp8Sorted>(a, dev, s);
-      case 128: return launch_wide<kFp8Sorted>(a, dev, s);
-      default: return MOE_LORA_ERR_UNSUPPORTED;
-    }
+    if (fp8_sorted_is_wide(a)) return launch_wide<kFp8Sorted>(a, workspace, dev, s);
+    // units of about twice an expert's average pairs, within the block
+    const int want = std::min<long long>(a.block, 2ll * a.pairs / a.E);
+    if (want <= 16) return launch_narrow<16, kFp8Sorted>(a, dev, s);
+    if (want <= 32) return launch_narrow<32, kFp8Sorted>(a, dev, s);
+    return launch_narrow<64, kFp8Sorted>(a, dev, s);
   }
   if (a.pairs <= 16) return launch_narrow<16, kFp8Dense>(a, dev, s);
   if (a.pairs <= 32) return launch_narrow<32, kFp8Dense>(a, dev, s);
   if (a.pairs <= 256) return launch_narrow<64, kFp8Dense>(a, dev, s);
-  return launch_wide<kFp8Dense>(a, dev, s);
+  return launch_wide<kFp8Dense>(a, nullptr, dev, s);
 }
 
 }  // namespace moe_lora

@@ -32,7 +32,7 @@ def _dense(**kw):
 
 def _grouped(**kw):
     a = dict(x=P0, per_pair=0, ldx=256, xs=P0, w=P0, ldw=256, ws=P0, y=P0, ldy=128, weights=None, sorted=P0, experts=P0,
-             padded=P0, M=2, topk=2, E=8, K=256, N=128, block=16, cap=124, capb=8, err=None, stream=None)
+             padded=P0, M=2, topk=2, E=8, K=256, N=128, block=16, cap=124, capb=8, ws_ptr=None, ws_bytes=0, err=None, stream=None)
     a.update(kw)
     return B.lib().moe_fp8_grouped_matmul(*a.values())
 
@@ -93,6 +93,18 @@ def test_grouped_sizes(call, want, kw):
     if call is _naive:
         kw = {k: v for k, v in kw.items() if k not in ("cap", "capb")}
     assert call(**kw) == want
+
+
+def test_grouped_workspace():
+    need = B.fp8_grouped_workspace_bytes
+    assert need(64, 2, 8, 256, 16) == 0                    # few pairs an expert: none
+    n = need(8192, 2, 8, 4096, 128)
+    rows = (8192 * 2 + 8 * 127) // 128 * 128
+    assert rows * 4096 < n < rows * 4096 * 1.1
+    assert need(-1, 2, 8, 256, 16) == need(4, 9, 8, 256, 16) == need(4, 2, 8, 0, 16) == need(4, 2, 8, 256, 8) == 0
+    big = dict(M=8192, cap=1 << 20, capb=1 << 16, block=128, ldx=4096, ldw=4096, K=4096)
+    assert _grouped(**big) == 4 and _grouped(ws_ptr=P0, ws_bytes=n - 1, **big) == 4
+    assert _grouped(ws_ptr=P0 + 8, ws_bytes=n, **big) == MISALIGNED
 
 
 def test_naive_ids():

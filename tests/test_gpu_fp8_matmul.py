@@ -173,6 +173,52 @@ def test_grouped_larger(M, topk, E, K, N, block):
 
 
 @pytest.mark.parametrize("block", [16, 32, 64, 128])
+@pytest.mark.parametrize("M,topk,E,K,N,kind", [(400, 1, 2, 256, 300, "even"), (130, 2, 2, 130, 520, "even"),
+                                               (513, 1, 1, 400, 257, "one"), (2000, 2, 8, 512, 256, "skew"),
+                                               (700, 3, 16, 272, 128, "skew"), (3000, 4, 60, 128, 96, "even")])
+def test_grouped_many_pairs_an_expert(block, M, topk, E, K, N, kind):
+    _grouped(M, topk, E, K, N, block, kind, per_pair=block > 32, weighted=block == 64, pad=block // 4)
+
+
+def test_grouped_with_a_workspace():
+    g = _gen(3)
+    M, topk, E, K, N, block = 600, 2, 4, 256, 320, 64
+    x, xs = f8_rows(M, K, g)
+    w, ws = f8_weight(N, K, g, E)
+    ids = _route(M, topk, E, g, "even")
+    n = B.fp8_grouped_workspace_bytes(M, topk, E, K, block)
+    assert n > 0
+    space = torch.full((n + 64,), 0x7f, dtype=torch.uint8, device="cuda")
+    y, want = (torch.empty((M, topk, N), dtype=BF, device="cuda") for _ in range(2))
+    blocks = _align(ids, E, block)
+    B.moe_fp8_grouped_matmul(x, xs, w, ws, y, *blocks, block, workspace=space[:n])
+    B.moe_fp8_grouped_matmul(x, xs, w, ws, want, *blocks, block)
+    assert torch.equal(y, want) and (space[n:] == 0x7f).all()
+    with pytest.raises(B.MoeLoraError):
+        B.moe_fp8_grouped_matmul(x, xs, w, ws, y, *blocks, block, workspace=space[:n - 1])
+
+
+@pytest.mark.parametrize("block", [32, 64, 128])
+def test_grouped_pair_after_sentinels_is_reported(block):
+    """The units after a block's first that begin with the sentinel are skipped; a pair in one of them is reported."""
+    g = _gen(block)
+    M, topk, E, K, N = 20, 1, 4, 256, 128
+    x, xs = f8_rows(M, K, g)
+    w, ws = f8_weight(N, K, g, E)
+    ids = (torch.arange(M, device="cuda") % E).to(torch.int32)[:, None].contiguous()
+    s, e, n = _align(ids, E, block)
+    y, err = torch.empty((M, topk, N), dtype=BF, device="cuda"), _err()
+    B.moe_fp8_grouped_matmul(x, xs, w, ws, y, s, e, n, block, err_flag=err)
+    ref, bound = _reference(x, xs, w, ws, ids, False, None)
+    assert err.item() == 0
+    assert_bf16_close(y.reshape(-1, N), ref, bound)
+    s.reshape(-1)[block - 1] = 0          # the first block's last position
+    B.moe_fp8_grouped_matmul(x, xs, w, ws, y, s, e, n, block, err_flag=err)
+    assert err.item() == B.DEVERR_PAIR_ID
+    assert_bf16_close(y.reshape(-1, N), ref, bound)
+
+
+@pytest.mark.parametrize("block", [16, 32, 64, 128])
 def test_grouped_no_tokens(block):
     g = _gen(0)
     w, ws = f8_weight(64, 64, g, 4)
