@@ -373,12 +373,14 @@ def fp8_groups(columns: int) -> int:
     return -(-columns // FP8_GROUP)
 
 
-def _dense(t, dtype, name):
-    """Address of a contiguous CUDA tensor (0 for None)."""
+def _dense(t, dtype, name, numel=None):
+    """Address of a contiguous CUDA tensor (None for None)."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if numel is not None and t.numel() != numel:
+        raise ValueError("%s must have %d elements, got shape %s" % (name, numel, tuple(t.shape)))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if not t.is_contiguous():
@@ -386,33 +388,43 @@ def _dense(t, dtype, name):
     return t.data_ptr()
 
 
-def _rows(t, dtype, name, columns):
+def _rows(t, dtype, name, rows, columns):
     """Address and leading dimension of the rows of a CUDA tensor: its last
-    dimension dense, the ones before it as if they were one."""
-    if t.dtype != dtype:
+    dimension dense, the ones before it as if they were one of `rows`."""
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    shape = t.shape
+    if shape[-1] != columns or t.numel() != rows * columns:
+        raise ValueError("%s: inconsistent shapes: [.., %d, %d] wanted, got %s" % (name, rows, columns, tuple(shape)))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    shape, stride = t.shape, t.stride()
-    if len(shape) < 2 or shape[-1] != columns or (stride[-1] != 1 and columns > 1):
-        raise ValueError("%s must have dense rows of %d, got shape %s, strides %s" % (name, columns, tuple(shape), stride))
-    ld = stride[-2]
-    if shape[-2] == 1:        # one row: its stride says nothing
-        ld = max(ld, columns)
-        if len(shape) > 2 and shape[-3] > 1:
-            ld = stride[-3]
-    if len(shape) > 2:
-        step = ld * shape[-2]
-        for d in range(len(shape) - 3, -1, -1):
-            if shape[d] > 1 and stride[d] != step:
-                raise ValueError("%s's rows must be evenly spaced, got shape %s, strides %s" % (name, tuple(shape), stride))
-            step *= shape[d]
+    if rows == 1:            # one row: any leading dimension will do
+        if columns > 1 and t.stride(-1) != 1:
+            raise ValueError("%s must have dense rows" % name)
+        return t.data_ptr(), -(-columns // 16) * 16
+    if t.is_contiguous():
+        return t.data_ptr(), columns
+    stride = t.stride()
+    if len(shape) < 2 or (stride[-1] != 1 and columns > 1):
+        raise ValueError("%s must have dense rows, got shape %s, strides %s" % (name, tuple(shape), stride))
+    # the dimensions of one row each say nothing
+    dims = [(n, st) for n, st in zip(shape[:-1], stride[:-1]) if n > 1]
+    step = ld = dims[-1][1]
+    for n, st in reversed(dims):
+        if st != step:
+            raise ValueError("%s's rows must be evenly spaced, got shape %s, strides %s" % (name, tuple(shape), stride))
+        step *= n
     return t.data_ptr(), ld
+
+
+_raw_current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
 
 def _raw_stream(stream, t):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.device.index)
+        if _raw_current_stream is None:
+            return torch.cuda.current_stream(t.device).cuda_stream
+        return _raw_current_stream(t.get_device())
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -423,34 +435,30 @@ def moe_add_rms_norm_fp8(x, weight, q, scales, residual=None, residual_out=None,
     x: bf16 [M, H], or [M, parts, H] (a token's rows, summed).  residual,
     residual_out, normed: bf16 [M, H] or None.  q: float8_e4m3fn [M, H];
     scales: float32 [M, ceil(H / 128)].  Rows may be strided."""
-    H = x.shape[-1]
-    M = x.shape[0]
-    parts = 1
-    if x.dim() == 3:
-        parts = x.shape[1]
-        if x.dtype != _BF16 or not x.is_cuda:
+    shape = x.shape
+    M, H = shape[0], shape[-1]
+    parts, ld_part = 1, 0
+    if len(shape) == 3:
+        parts = shape[1]
+        if x.dtype is not _BF16 or not x.is_cuda:
             raise TypeError("x must be a bfloat16 CUDA tensor")
         ldx, ld_part, one = x.stride()
         if one != 1 and H > 1:
             raise ValueError("x must have dense rows")
-        px = x.data_ptr()
+        if parts == 1:
+            ld_part = 0
         if M == 1:
             ldx = max(ldx, H)
+        px = x.data_ptr()
     else:
-        px, ldx = _rows(x, _BF16, "x", H)
-        ld_part = 0
-    for t, name in ((residual, "residual"), (residual_out, "residual_out"), (normed, "normed"), (q, "q")):
-        if t is not None and tuple(t.shape) != (M, H):
-            raise ValueError("%s must be [%d, %d], got %s" % (name, M, H, tuple(t.shape)))
-    if weight.numel() != H or scales.numel() != M * fp8_groups(H):
-        raise ValueError("weight must be [%d] and scales [%d, %d]" % (H, M, fp8_groups(H)))
-    pr, ldr = (None, 0) if residual is None else _rows(residual, _BF16, "residual", H)
-    po, ldo = (None, 0) if residual_out is None else _rows(residual_out, _BF16, "residual_out", H)
-    pn, ldn = (None, 0) if normed is None else _rows(normed, _BF16, "normed", H)
-    pq, ldq = _rows(q, _F8, "q", H)
-    _check(lib().moe_add_rms_norm_fp8(px, ldx, ld_part, parts, pr, ldr, _dense(weight, _BF16, "weight"), eps, po, ldo,
-                                      pn, ldn, pq, ldq, _dense(scales, _F32, "scales"), M, H, _raw_stream(stream, x)),
-           "moe_add_rms_norm_fp8")
+        px, ldx = _rows(x, _BF16, "x", M, H)
+    pr, ldr = (None, 0) if residual is None else _rows(residual, _BF16, "residual", M, H)
+    po, ldo = (None, 0) if residual_out is None else _rows(residual_out, _BF16, "residual_out", M, H)
+    pn, ldn = (None, 0) if normed is None else _rows(normed, _BF16, "normed", M, H)
+    pq, ldq = _rows(q, _F8, "q", M, H)
+    _check((_lib or lib()).moe_add_rms_norm_fp8(
+        px, ldx, ld_part, parts, pr, ldr, _dense(weight, _BF16, "weight", H), eps, po, ldo, pn, ldn, pq, ldq,
+        _dense(scales, _F32, "scales", M * -(-H // FP8_GROUP)), M, H, _raw_stream(stream, q)), "moe_add_rms_norm_fp8")
 
 
 def moe_silu_mul_fp8(x, q, scales, stream=None):
@@ -459,15 +467,11 @@ def moe_silu_mul_fp8(x, q, scales, stream=None):
     x: bf16 [..., 2*I], gate then up.  q: float8_e4m3fn [..., I]; scales:
     float32 [..., ceil(I / 128)].  Rows may be strided, evenly."""
     I = q.shape[-1]
-    if x.shape[:-1].numel() != q.shape[:-1].numel():
-        raise ValueError("x and q must have the same rows")
-    rows = q.shape[:-1].numel()
-    if scales.numel() != rows * fp8_groups(I):
-        raise ValueError("scales must be [%d, %d]" % (rows, fp8_groups(I)))
-    px, ldx = _rows(x, _BF16, "x", 2 * I)
-    pq, ldq = _rows(q, _F8, "q", I)
-    _check(lib().moe_silu_mul_fp8(px, ldx, pq, ldq, _dense(scales, _F32, "scales"), rows, I, _raw_stream(stream, x)),
-           "moe_silu_mul_fp8")
+    rows = q.numel() // I if I else 0
+    px, ldx = _rows(x, _BF16, "x", rows, 2 * I)
+    pq, ldq = _rows(q, _F8, "q", rows, I)
+    _check((_lib or lib()).moe_silu_mul_fp8(px, ldx, pq, ldq, _dense(scales, _F32, "scales", rows * -(-I // FP8_GROUP)),
+                                            rows, I, _raw_stream(stream, q)), "moe_silu_mul_fp8")
 
 
 def moe_fp8_matmul(x, x_scales, w, w_scales, y, err_flag=None, stream=None):
@@ -477,35 +481,29 @@ def moe_fp8_matmul(x, x_scales, w, w_scales, y, err_flag=None, stream=None):
     x: float8_e4m3fn [M, K], x_scales: float32 [M, ceil(K / 128)]; w:
     float8_e4m3fn [N, K], w_scales: float32 [ceil(N / 128), ceil(K / 128)]; y:
     bf16 [M, N].  Rows of x, w and y may be strided (x, w: by multiples of 16)."""
-    M, K = x.shape
-    N = w.shape[0]
-    kb = fp8_groups(K)
-    if tuple(y.shape) != (M, N) or x_scales.numel() != M * kb or w_scales.numel() != fp8_groups(N) * kb:
-        raise ValueError("inconsistent shapes")
-    px, ldx = _rows(x, _F8, "x", K)
-    pw, ldw = _rows(w, _F8, "w", K)
-    py, ldy = _rows(y, _BF16, "y", N)
-    _check(lib().moe_fp8_matmul(px, ldx, _dense(x_scales, _F32, "x_scales"), pw, ldw,
-                                _dense(w_scales, _F32, "w_scales"), py, ldy, M, N, K,
-                                _dense(err_flag, _I32, "err_flag"), _raw_stream(stream, y)), "moe_fp8_matmul")
+    M, N = y.shape
+    K = x.shape[-1]
+    kb = -(-K // FP8_GROUP)
+    px, ldx = _rows(x, _F8, "x", M, K)
+    pw, ldw = _rows(w, _F8, "w", N, K)
+    py, ldy = _rows(y, _BF16, "y", M, N)
+    _check((_lib or lib()).moe_fp8_matmul(
+        px, ldx, _dense(x_scales, _F32, "x_scales", M * kb), pw, ldw,
+        _dense(w_scales, _F32, "w_scales", -(-N // FP8_GROUP) * kb), py, ldy, M, N, K,
+        _dense(err_flag, _I32, "err_flag"), _raw_stream(stream, y)), "moe_fp8_matmul")
 
 
 def _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair):
     M, topk, N = y.shape
-    E, N2, K = w.shape
-    kb = fp8_groups(K)
+    E, _, K = w.shape
+    kb = -(-K // FP8_GROUP)
     rows = M * topk if x_per_pair else M
-    if N2 != N or tuple(x.shape) != (rows, K) or x_scales.numel() != rows * kb:
-        raise ValueError("inconsistent shapes")
-    if w_scales.numel() != E * fp8_groups(N) * kb:
-        raise ValueError("w_scales must be [%d, %d, %d]" % (E, fp8_groups(N), kb))
-    if topk_weights is not None and topk_weights.numel() != M * topk:
-        raise ValueError("topk_weights must be [M, topk]")
-    px, ldx = _rows(x, _F8, "x", K)
-    pw, ldw = _rows(w, _F8, "w", K)
-    py, ldy = _rows(y, _BF16, "y", N)
-    return M, topk, E, K, N, (px, int(bool(x_per_pair)), ldx, _dense(x_scales, _F32, "x_scales"), pw, ldw,
-                              _dense(w_scales, _F32, "w_scales"), py, ldy, _dense(topk_weights, _F32, "topk_weights"))
+    px, ldx = _rows(x, _F8, "x", rows, K)
+    pw, ldw = _rows(w, _F8, "w", E * N, K)
+    py, ldy = _rows(y, _BF16, "y", M * topk, N)
+    return M, topk, E, K, N, (px, 1 if x_per_pair else 0, ldx, _dense(x_scales, _F32, "x_scales", rows * kb), pw, ldw,
+                              _dense(w_scales, _F32, "w_scales", E * -(-N // FP8_GROUP) * kb), py, ldy,
+                              _dense(topk_weights, _F32, "topk_weights", M * topk))
 
 
 def fp8_grouped_workspace_bytes(M, topk, num_experts, K, block_size) -> int:
@@ -526,19 +524,20 @@ def moe_fp8_grouped_matmul(x, x_scales, w, w_scales, y, sorted_token_ids, expert
     fp8_grouped_workspace_bytes(...) bytes; without one, calls that need one
     take it from torch's allocator."""
     M, topk, E, K, N, operands = _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair)
-    L = lib()
+    L = _lib or lib()
     raw = _raw_stream(stream, y)
+    nbytes = 0
     if workspace is None:
-        need = L.moe_fp8_grouped_workspace_bytes(M, topk, E, K, block_size)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
+        nbytes = L.moe_fp8_grouped_workspace_bytes(M, topk, E, K, block_size)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=y.device)
             if stream is not None:
-                # its memory may be another tensor's once this stream is done with it; its last use may be
-                # unfinished on the current stream
+                # the allocator's earlier work on this memory is ordered on the current stream, its next on either
                 side = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, y.device)
                 side.wait_stream(torch.cuda.current_stream(y.device))
                 workspace.record_stream(side)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
     _check(L.moe_fp8_grouped_matmul(
         *operands, _dense(sorted_token_ids, _I32, "sorted_token_ids"), _dense(expert_ids, _I32, "expert_ids"),
         _dense(num_tokens_post_padded, _I32, "num_tokens_post_padded"), M, topk, E, K, N, block_size,
@@ -552,11 +551,9 @@ def moe_fp8_grouped_matmul_naive(x, x_scales, w, w_scales, y, topk_ids, topk_wei
     """moe_fp8_grouped_matmul without an align, one work item per (token,
     top-k) pair; topk_ids: int32 [M, topk]."""
     M, topk, E, K, N, operands = _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair)
-    if topk_ids.numel() != M * topk:
-        raise ValueError("topk_ids must be [M, topk]")
-    _check(lib().moe_fp8_grouped_matmul_naive(*operands, _dense(topk_ids, _I32, "topk_ids"), M, topk, E, K, N,
-                                              _dense(err_flag, _I32, "err_flag"), _raw_stream(stream, y)),
-           "moe_fp8_grouped_matmul_naive")
+    _check((_lib or lib()).moe_fp8_grouped_matmul_naive(
+        *operands, _dense(topk_ids, _I32, "topk_ids", M * topk), M, topk, E, K, N,
+        _dense(err_flag, _I32, "err_flag"), _raw_stream(stream, y)), "moe_fp8_grouped_matmul_naive")
 
 
 class AlignBuffers:

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     cluster_arrive_release();
     cluster_wait();
   }
+  wait_for_prior_grid();
   const uint32_t tmem = ctl.tmem;
   const int items = num_units<MODE>(p, BT) * cfg.nt;
   const int kb0 = (int)((long long)p.KB * rank / cs), kb1 = (int)((long long)p.KB * (rank + 1) / cs);
@@ -409,6 +410,7 @@ __global__ void __launch_bounds__(kGatherThreads)
     fp8_gather_kernel(const Fp8Args p, WideTile *tiles, uint8_t *xg, long long ld) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bs = p.block;
+  wait_for_prior_grid();
   const int nb = num_blocks(p);
   if (blockIdx.x == 0) {
     // Tile list.  A block heads a tile when the blocks before it of the same
@@ -525,6 +527,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   cluster_arrive_release();
   cluster_wait();
   tc_fence_after();
+  wait_for_prior_grid();
   const uint32_t tmem = ctl.tmem;
   const int ntiles = MODE == kFp8Dense ? (p.pairs + kTileRows - 1) / kTileRows : __ldg(&g.tiles[0].row0);
   const int items = ntiles * cfg.nt;   // rows fastest: pairs at work share the weight's columns
@@ -718,21 +721,26 @@ bool register_shares_fit(Kernel kernel) {
 template <typename... Params, typename... Args>
 int launch(void (*kernel)(Params...), const Fp8Cfg &cfg, unsigned grid, int threads, cudaStream_t stream,
            const Args &...args) {
-  if (cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.smem_bytes) !=
-      cudaSuccess)
+  if (cfg.smem_bytes > 0 &&
+      cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.smem_bytes) !=
+          cudaSuccess)
     return MOE_LORA_ERR_LAUNCH;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(grid, 1, 1);
   lc.blockDim = dim3(threads, 1, 1);
   lc.dynamicSmemBytes = cfg.smem_bytes;
   lc.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cfg.cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  // May start while the kernel before it is finishing: barriers, tensor memory
+  // and tensor maps are set up before it waits for that kernel.
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cfg.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
-  lc.numAttrs = 1;
+  lc.numAttrs = cfg.cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? 0 : MOE_LORA_ERR_LAUNCH;
 }
 
@@ -790,13 +798,11 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
     uint8_t *base = static_cast<uint8_t *>(workspace);
     g.tiles = reinterpret_cast<WideTile *>(base + w.tiles);
     if (int st = make_maps(a, base + w.x, rows, w.ld, kHalf / 2, kRows, &maps)) return st;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)std::min<long long>((rows + 7) / 8, dev.sm_count * 8ll), 1, 1);
-    lc.blockDim = dim3(kGatherThreads, 1, 1);
-    lc.stream = stream;
-    if (cudaLaunchKernelEx(&lc, fp8_gather_kernel, a, reinterpret_cast<WideTile *>(base + w.tiles),
-                           base + w.x, w.ld) != cudaSuccess)
-      return MOE_LORA_ERR_LAUNCH;
+    Fp8Cfg gather = {};
+    gather.cluster = 1;
+    if (int st = launch(fp8_gather_kernel, gather, (unsigned)std::min<long long>((rows + 7) / 8, dev.sm_count * 8ll),
+                        kGatherThreads, stream, a, reinterpret_cast<WideTile *>(base + w.tiles), base + w.x, w.ld))
+      return st;
   }
   const long long items = tiles * cfg.nt;   // (the sorted arrays' own tiles are no more, but for entries that no align writes)
   if (items > INT32_MAX / 16) return MOE_LORA_ERR_UNSUPPORTED;

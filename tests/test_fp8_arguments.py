@@ -129,7 +129,7 @@ def test_binding_refuses_host_tensors_and_wrong_layouts():
     with pytest.raises(ValueError, match="CUDA"):
         B.moe_fp8_matmul(q, s, torch.zeros((128, 256), dtype=f8), torch.zeros((1, 2)), y)
     with pytest.raises(ValueError, match="inconsistent"):
-        B.moe_fp8_matmul(q, s, torch.zeros((128, 256), dtype=f8), torch.zeros((1, 3)), y)
+        B.moe_fp8_matmul(q, s, torch.zeros((128, 256), dtype=f8), torch.zeros((1, 2)), torch.zeros((3, 128), dtype=bf))
     with pytest.raises(TypeError):
         B.moe_fp8_matmul(x, s, torch.zeros((128, 256), dtype=f8), torch.zeros((1, 2)), y)
 
@@ -142,19 +142,29 @@ def test_rows_layout():
         def __init__(self, shape, stride):
             self.shape, self._s = torch.Size(shape), stride
 
-        def stride(self):
-            return self._s
+        def stride(self, d=None):
+            return self._s if d is None else self._s[d]
 
         def data_ptr(self):
             return 64
 
+        def numel(self):
+            return self.shape.numel()
+
+        def is_contiguous(self):
+            return False
+
     def ld(shape, stride):
-        return B._rows(Fake(shape, stride), torch.bfloat16, "t", shape[-1])[1]
+        rows = 1
+        for n in shape[:-1]:
+            rows *= n
+        return B._rows(Fake(shape, stride), torch.bfloat16, "t", rows, shape[-1])[1]
     assert ld((4, 8), (8, 1)) == 8 and ld((4, 8), (24, 1)) == 24
-    assert ld((1, 8), (1, 1)) == 8
+    assert ld((1, 8), (1, 1)) == 16               # one row: any will do
     assert ld((3, 2, 8), (32, 16, 1)) == 16
     assert ld((3, 1, 8), (32, 8, 1)) == 32
-    assert ld((1, 1, 8), (5, 3, 1)) == 8
-    for shape, stride in (((4, 8), (8, 2)), ((3, 2, 8), (20, 8, 1)), ((8,), (1,))):
+    assert ld((1, 1, 24), (5, 3, 1)) == 32
+    assert ld((3, 1, 1, 8), (32, 2, 7, 1)) == 32
+    for shape, stride in (((4, 8), (8, 2)), ((3, 2, 8), (20, 8, 1)), ((1, 8), (8, 2))):
         with pytest.raises(ValueError):
             ld(shape, stride)
