@@ -59,6 +59,8 @@ struct Fp8Args {
   int max_blocks;             // blocks that the sorted arrays hold
   int x_per_pair;             // row of pair f is f, else f / topk
 };
+// Naive calls, and dense ones of at most 16 rows, whose weights are small.
+int launch_fp8_stream(const Fp8Args &a, Fp8Mode mode, const DeviceInfo &dev, cudaStream_t stream);
 // Sorted calls with many pairs an expert gather x into the workspace (the
 // bytes it needs; 0: none).
 size_t fp8_sorted_workspace(const Fp8Args &a);

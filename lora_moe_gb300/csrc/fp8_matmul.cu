@@ -19,9 +19,11 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "device_utils.cuh"
 #include "fp8.h"
+#include "fp8_blocks.cuh"
 #include "stream_pipeline.cuh"
 
 namespace moe_lora {
@@ -44,55 +46,6 @@ struct Fp8Cfg {
   int off_scale, off_red, off_ctrl;
   int smem_bytes;
 };
-
-// Blocks that the sorted arrays hold.
-__device__ __forceinline__ int num_blocks(const Fp8Args &p) {
-  const int n = __ldg(p.num_tokens_post_padded) / p.block;
-  return n < 0 ? 0 : (n > p.max_blocks ? p.max_blocks : n);
-}
-// The narrow kernel's units of bt positions: a block of the sorted arrays is
-// `block / bt` of them.
-template <int MODE>
-__device__ __forceinline__ int num_units(const Fp8Args &p, int bt) {
-  if (MODE == kFp8Dense) return (p.pairs + bt - 1) / bt;
-  if (MODE == kFp8Naive) return p.pairs;
-  return num_blocks(p) * (p.block / bt);
-}
-constexpr int kBadExpert = -1, kNoPairs = -2;
-// Expert of unit b; negative where the unit is skipped: its id is out of
-// range, or its first position holds the sentinel and it does not begin a
-// block (a block's pairs precede its sentinels).
-template <int MODE>
-__device__ __forceinline__ int block_expert(const Fp8Args &p, int b, int bt) {
-  if (MODE == kFp8Dense) return 0;
-  const int e = MODE == kFp8Sorted ? __ldg(p.expert_ids + b / (p.block / bt)) : __ldg(p.topk_ids + b);
-  if ((unsigned)e >= (unsigned)p.E) return kBadExpert;
-  if (MODE == kFp8Sorted && b % (p.block / bt) && __ldg(p.sorted_token_ids + (size_t)b * bt) == p.pairs) return kNoPairs;
-  return e;
-}
-// Pair at position t of block b, or -1.  `bt` positions a block.
-template <int MODE>
-__device__ __forceinline__ int block_pair(const Fp8Args &p, int b, int t, int bt) {
-  if (MODE == kFp8Naive) return t == 0 ? b : -1;
-  int f;
-  if (MODE == kFp8Dense) f = b * bt + t;
-  else f = __ldg(p.sorted_token_ids + (size_t)b * bt + t);
-  return (unsigned)f < (unsigned)p.pairs ? f : -1;
-}
-template <int MODE>
-__device__ __forceinline__ int pair_row(const Fp8Args &p, int f) {
-  return MODE == kFp8Dense || p.x_per_pair ? f : f / p.topk;
-}
-// Report the entries of the sorted arrays that are out of range.
-template <int MODE>
-__device__ __forceinline__ void flag_block(const Fp8Args &p, int b, int t, int bt) {
-  if (MODE != kFp8Sorted) return;
-  if ((unsigned)__ldg(p.sorted_token_ids + (size_t)b * bt + t) > (unsigned)p.pairs) flag_error(p.err, MOE_LORA_DEVERR_PAIR_ID);
-}
-template <int MODE>
-__device__ __forceinline__ float pair_weight(const Fp8Args &p, int f) {
-  return MODE != kFp8Dense && p.topk_weights ? __ldg(p.topk_weights + f) : 1.f;
-}
 
 // ------------------------------------------------------------------ narrow
 
@@ -235,25 +188,15 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     uint32_t ph = 0;
     for (int it = cid; it < items; it += nclusters) {
       const int b = it / cfg.nt, nt = it - b * cfg.nt, e = block_expert<MODE>(p, b, BT);
-      if (e < 0) {
-        if (nt == 0 && rank == 0) {
-          if (e == kBadExpert && lane == 0) flag_error(p.err, MOE_LORA_DEVERR_EXPERT_ID);
-          if (e == kNoPairs)   // a pair after a sentinel
-            for (int t = lane; t < BT; t += 32)
-              if (__ldg(p.sorted_token_ids + (size_t)b * BT + t) != p.pairs) flag_error(p.err, MOE_LORA_DEVERR_PAIR_ID);
-        }
-        continue;
-      }
+      if (nt == 0 && rank == 0) flag_unit<MODE>(p, b, BT, e, lane);
+      if (e < 0) continue;
       constexpr int kPer = (BT + 31) / 32;
       const float *src[kPer];
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int t = j * 32 + lane;
         int f = -1;
-        if (t < BT) {
-          f = block_pair<MODE>(p, b, t, BT);
-          if (nt == 0 && rank == 0) flag_block<MODE>(p, b, t, BT);
-        }
+        if (t < BT) f = block_pair<MODE>(p, b, t, BT);
         src[j] = f < 0 ? nullptr : p.x_scales + (size_t)pair_row<MODE>(p, f) * p.KB;
       }
       const float *sw = p.w_scales + ((size_t)e * p.NB + nt) * p.KB;
@@ -744,6 +687,42 @@ int launch(void (*kernel)(Params...), const Fp8Cfg &cfg, unsigned grid, int thre
   return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? 0 : MOE_LORA_ERR_LAUNCH;
 }
 
+// Clusters of this shape that are resident at once; asked once for each shape.
+template <typename Kernel>
+int resident_clusters(Kernel kernel, const Fp8Cfg &cfg, int threads, const DeviceInfo &dev) {
+  if (cfg.cluster == 1) return dev.sm_count;
+  struct Entry {
+    int device, cluster, smem, clusters;
+  };
+  static std::mutex mu;
+  static Entry known[64];
+  static int n = 0;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < n; ++i)
+    if (known[i].device == dev.device && known[i].cluster == cfg.cluster && known[i].smem == cfg.smem_bytes)
+      return known[i].clusters;
+  cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.smem_bytes);
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)cfg.cluster, 1, 1);
+  lc.blockDim = dim3(threads, 1, 1);
+  lc.dynamicSmemBytes = cfg.smem_bytes;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cfg.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, (const void *)kernel, &lc) != cudaSuccess) {
+    cudaGetLastError();   // a failed query leaves no sticky error
+    clusters = 0;
+  }
+  if (clusters < 1) clusters = std::max(1, dev.sm_count / cfg.cluster / 2);
+  if (n < 64) known[n++] = {dev.device, cfg.cluster, cfg.smem_bytes, clusters};
+  return clusters;
+}
+
 // Upper bound of the call's blocks.
 long long block_bound(const Fp8Args &a, Fp8Mode mode, int bt) {
   if (mode == kFp8Dense) return ((long long)a.pairs + bt - 1) / bt;
@@ -759,17 +738,25 @@ int launch_narrow(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) 
   const long long items = block_bound(a, (Fp8Mode)MODE, BT) * cfg.nt;
   if (items <= 0) return 0;
   if (items > INT32_MAX) return MOE_LORA_ERR_UNSUPPORTED;
-  // K is split while there are too few items for the SMs and each CTA keeps two groups
+  // K is split over a cluster while there are too few items for the SMs, each
+  // CTA keeps two groups and the clusters fit at once.  A ring no longer than
+  // a CTA's share lets more of them fit (clusters of 8 with 200 KB each: 15).
+  auto shape = [&](int cs) {
+    cfg.cluster = cs;
+    const int fixed = kScaleSlots * C::kScaleRow * 4 + (cs > 1 ? 2 * C::kRedBytes : 0) + (int)sizeof(NarrowCtrl) + 128;
+    const long long share = ((long long)a.KB + cs - 1) / cs * ((items * cs + dev.sm_count - 1) / dev.sm_count);
+    cfg.stages = (int)std::max(2ll, std::min<long long>(share, std::min(kMaxRing, (200 * 1024 - fixed) / C::kStage)));
+    cfg.off_scale = cfg.stages * C::kStage;
+    cfg.off_red = cfg.off_scale + kScaleSlots * C::kScaleRow * 4;
+    cfg.off_ctrl = cfg.off_red + (cs > 1 ? 2 * C::kRedBytes : 0);
+    cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(NarrowCtrl);
+    return resident_clusters(fp8_narrow_kernel<BT, MODE>, cfg, kNarrowThreads, dev);
+  };
   int cs = 1;
   while (cs < 8 && items * cs * 2 <= dev.sm_count && a.KB >= cs * 4) cs *= 2;
-  cfg.cluster = cs;
-  const int fixed = kScaleSlots * C::kScaleRow * 4 + (cs > 1 ? 2 * C::kRedBytes : 0) + (int)sizeof(NarrowCtrl) + 128;
-  cfg.stages = std::min(kMaxRing, (200 * 1024 - fixed) / C::kStage);
-  cfg.off_scale = cfg.stages * C::kStage;
-  cfg.off_red = cfg.off_scale + kScaleSlots * C::kScaleRow * 4;
-  cfg.off_ctrl = cfg.off_red + (cs > 1 ? 2 * C::kRedBytes : 0);
-  cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(NarrowCtrl);
-  const unsigned clusters = (unsigned)std::min<long long>(items, dev.sm_count / cs);
+  int fit = shape(cs);
+  while (cs > 1 && fit < items) fit = shape(cs /= 2);
+  const unsigned clusters = (unsigned)std::min<long long>(items, std::min(fit, dev.sm_count / cs));
   Fp8Maps maps;
   if (int st = make_maps(a, a.x, a.rows, a.ldx, kRows, MODE == kFp8Dense ? BT : 1, &maps)) return st;
   return launch(fp8_narrow_kernel<BT, MODE>, cfg, clusters * cs, kNarrowThreads, stream, maps, a, cfg);
@@ -814,6 +801,12 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
 
 // The wide kernel from 128 pairs an expert on (on average): below that a call
 // is bound by the weight's bytes, and tiles of 256 rows would be half empty.
+// Up to this many bytes of weights, calls of single pairs or of at most 16 rows
+// run the kernel that streams the weight through registers: it starts in half
+// the time (2048 x 2048 and one row: 2.5 us against 4.9), but has fewer bytes
+// in flight (8192 x 8192: 19 us against 16).
+constexpr double kStreamBytes = 32e6;
+
 bool fp8_sorted_is_wide(const Fp8Args &a) { return a.pairs >= 128ll * a.E; }
 
 size_t fp8_sorted_workspace(const Fp8Args &a) {
@@ -821,7 +814,8 @@ size_t fp8_sorted_workspace(const Fp8Args &a) {
 }
 
 int launch_fp8_matmul(const Fp8Args &a, Fp8Mode mode, void *workspace, const DeviceInfo &dev, cudaStream_t s) {
-  if (mode == kFp8Naive) return launch_narrow<16, kFp8Naive>(a, dev, s);
+  const bool small = (mode == kFp8Naive ? (double)a.pairs : 1.0) * a.N * a.K <= kStreamBytes;
+  if (mode == kFp8Naive) return small ? launch_fp8_stream(a, mode, dev, s) : launch_narrow<16, kFp8Naive>(a, dev, s);
   if (mode == kFp8Sorted) {
     if (fp8_sorted_is_wide(a)) return launch_wide<kFp8Sorted>(a, workspace, dev, s);
     // units of about twice an expert's average pairs, within the block
@@ -830,6 +824,7 @@ int launch_fp8_matmul(const Fp8Args &a, Fp8Mode mode, void *workspace, const Dev
     if (want <= 32) return launch_narrow<32, kFp8Sorted>(a, dev, s);
     return launch_narrow<64, kFp8Sorted>(a, dev, s);
   }
+  if (small && a.pairs <= 16) return launch_fp8_stream(a, mode, dev, s);
   if (a.pairs <= 16) return launch_narrow<16, kFp8Dense>(a, dev, s);
   if (a.pairs <= 32) return launch_narrow<32, kFp8Dense>(a, dev, s);
   if (a.pairs <= 256) return launch_narrow<64, kFp8Dense>(a, dev, s);
