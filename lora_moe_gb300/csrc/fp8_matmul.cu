@@ -12,14 +12,16 @@
 // issues the MMAs and epilogue warps:
 //   narrow  the weight on the 128 rows of the MMA, 16 to 64 pairs on its
 //           columns: few pairs for each weight (decode), bound by the weight's
-//           bytes.  A cluster of CTAs may split K, its partial sums exchanged
-//           through distributed shared memory in a fixed order.
+//           bytes.  Where there are few items, clusters of CTAs split K, their
+//           partial sums exchanged through distributed shared memory and added
+//           in a fixed order.
 //   wide    128 pairs on the rows, 256 output columns: bound by the tensor cores.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "device_utils.cuh"
 #include "fp8.h"
@@ -55,21 +57,68 @@ constexpr int kScaleSlots = 16;   // ring of scale rows, one group each
 
 template <int BT>
 struct Narrow {
-  static constexpr int kStage = kTileBytes + BT * kFp8Group;
+  static constexpr int kGroup = kTileBytes + BT * kFp8Group;
+  // Two groups a stage, requested together: 256 consecutive bytes of each of
+  // the weight's rows (gpt-oss-shaped w2 decode 140 us, against 145 with one).
+  static constexpr int kStage = 2 * kGroup;
   static constexpr int kScaleRow = BT + 4;    // BT row scales and the weight's, padded to 16 bytes
   static constexpr int kBufs = 4;             // accumulators in tensor memory
   static constexpr int kCols = kBufs * BT;    // power of two, >= 32
-  static constexpr int kRedBytes = BT * kRows * 4;   // one exchange buffer: every rank's partial sums of this CTA's columns
+  static constexpr int kRedBytes = BT * kRows * 4;   // every rank's partial sums of this CTA's columns
 };
 
 struct NarrowCtrl {
   uint64_t full[kMaxRing], empty[kMaxRing];
   uint64_t sfull[kScaleSlots], sempty[kScaleSlots];
   uint64_t tfull[4], tempty[4];
-  uint64_t red_full[2], red_empty[2];
+  uint64_t red_full;
   uint32_t tmem;
   int abort;
 };
+
+// The items of a CTA, in the order of its warps' loops: all of K, or (a cluster
+// of cs > 1 CTAs, which has one item at most) this CTA's share of it.
+struct NarrowWork {
+  int items, next, step, it, kb0, kb1, rank;
+  __device__ __forceinline__ NarrowWork(int n, int KB, int cs) : items(n) {
+    rank = blockIdx.x % cs;   // (a cluster is cs consecutive CTAs)
+    next = blockIdx.x / cs;
+    step = cs > 1 ? items : gridDim.x;
+    kb0 = (int)((long long)KB * rank / cs);
+    kb1 = (int)((long long)KB * (rank + 1) / cs);
+  }
+  __device__ __forceinline__ bool advance() {
+    if (next >= items) return false;
+    it = next;
+    next += step;   // (cs > 1: past the last)
+    return true;
+  }
+};
+
+// The sums of one CTA's positions over CS ranks, in rank order; Q of 4
+// positions (or 2) at a time.
+template <int CS, int W>
+__device__ __forceinline__ void sum_ranks(const float *buf, int per_rank, int at, int row, float (&v)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = 0.f;
+#pragma unroll
+  for (int q = 0; q < CS; ++q) {
+    const float *src = buf + ((q * per_rank + at) * kRows + row) * W;
+    if constexpr (W == 4) {
+      const float4 u = *reinterpret_cast<const float4 *>(src);
+      v[0] += u.x;
+      v[1] += u.y;
+      v[2] += u.z;
+      v[3] += u.w;
+    } else if constexpr (W == 2) {
+      const float2 u = *reinterpret_cast<const float2 *>(src);
+      v[0] += u.x;
+      v[1] += u.y;
+    } else {
+      v[0] += *src;
+    }
+  }
+}
 
 template <int BT, int MODE>
 __global__ void __launch_bounds__(kNarrowThreads, 1)
@@ -80,8 +129,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   NarrowCtrl &ctl = *reinterpret_cast<NarrowCtrl *>(smem + cfg.off_ctrl);
   float *scales = reinterpret_cast<float *>(smem + cfg.off_scale);
   volatile int *abort = &ctl.abort;
-  const int cs = cfg.cluster, rank = blockIdx.x % cs;   // (a cluster is cs consecutive CTAs)
-  const int cid = blockIdx.x / cs, nclusters = gridDim.x / cs;
+  const int cs = cfg.cluster;
 
   if (tid == 0) {
     for (int s = 0; s < cfg.stages; ++s) {
@@ -96,10 +144,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       mbar_init(&ctl.tfull[s], 1);
       mbar_init(&ctl.tempty[s], 4);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&ctl.red_full[s], 1);
-      mbar_init(&ctl.red_empty[s], cs);
-    }
+    mbar_init(&ctl.red_full, 1);
     ctl.abort = 0;
     fence_barrier_init();
     prefetch_tensor_map(&maps.w);
@@ -112,21 +157,19 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (cs > 1) {   // peers' barriers are initialised before anything is sent to them
-    cluster_arrive_release();
-    cluster_wait();
-  }
+  if (cs > 1) cluster_arrive_release();   // this CTA's barriers are initialised; waited for before anything is sent
   wait_for_prior_grid();
   const uint32_t tmem = ctl.tmem;
   const int items = num_units<MODE>(p, BT) * cfg.nt;
-  const int kb0 = (int)((long long)p.KB * rank / cs), kb1 = (int)((long long)p.KB * (rank + 1) / cs);
+  NarrowWork wk(items, p.KB, cs);
+  bool waited = false;   // for the cluster's barriers
 
   if (warp == 0) {
     // ---------------- operands: the weight's tile, and the pairs' rows
     int s = 0;
     uint32_t ph = 0;
-    for (int it = cid; it < items; it += nclusters) {
-      const int b = it / cfg.nt, nt = it - b * cfg.nt, e = block_expert<MODE>(p, b, BT);
+    while (wk.advance()) {
+      const int b = wk.it / cfg.nt, nt = wk.it - b * cfg.nt, e = block_expert<MODE>(p, b, BT);
       if (e < 0) continue;
       int row[4];
       bool mine = false;   // lane i gathers rows 4i .. 4i+3; groups without a pair are left as they are
@@ -144,17 +187,23 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
           if (row[i] < 0) row[i] = some;
       }
       const int groups = MODE == kFp8Dense ? BT / 4 : __popc(__ballot_sync(0xFFFFFFFFu, mine));
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = wk.kb0; kb < wk.kb1; kb += 2) {
         mbar_wait(&ctl.empty[s], ph ^ 1, abort, p.err);
         uint8_t *st = smem + (size_t)s * C::kStage;
+        const int n = min(2, wk.kb1 - kb);
         if (elect_one()) {
-          mbar_arrive_expect_tx(&ctl.full[s], kTileBytes + groups * 4 * kFp8Group);
-          tma_load_3d(st, &maps.w, kb * kFp8Group, nt * kRows, e, &ctl.full[s]);
-          if (MODE == kFp8Dense) tma_load_2d(st + kTileBytes, &maps.x, kb * kFp8Group, b * BT, &ctl.full[s]);
+          mbar_arrive_expect_tx(&ctl.full[s], n * (kTileBytes + groups * 4 * kFp8Group));
+          for (int i = 0; i < n; ++i)
+            tma_load_3d(st + i * C::kGroup, &maps.w, (kb + i) * kFp8Group, nt * kRows, e, &ctl.full[s]);
+          if (MODE == kFp8Dense)
+            for (int i = 0; i < n; ++i)
+              tma_load_2d(st + i * C::kGroup + kTileBytes, &maps.x, (kb + i) * kFp8Group, b * BT, &ctl.full[s]);
         }
         __syncwarp();
         if (MODE != kFp8Dense && mine)
-          tma_gather4(st + kTileBytes + lane * 4 * kFp8Group, &maps.x, kb * kFp8Group, row, &ctl.full[s]);
+          for (int i = 0; i < n; ++i)
+            tma_gather4(st + i * C::kGroup + kTileBytes + lane * 4 * kFp8Group, &maps.x, (kb + i) * kFp8Group, row,
+                        &ctl.full[s]);
         if (++s == cfg.stages) { s = 0; ph ^= 1; }
       }
     }
@@ -164,31 +213,35 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     const uint64_t desc0 = make_sdesc_sw128(smem_addr(smem));   // (addresses in units of 16 bytes)
     int s = 0, a = 0;
     uint32_t ph = 0, aph = 0;
-    for (int it = cid; it < items; it += nclusters) {
-      if (block_expert<MODE>(p, it / cfg.nt, BT) < 0) continue;
-      for (int kb = kb0; kb < kb1; ++kb) {
+    while (wk.advance()) {
+      if (block_expert<MODE>(p, wk.it / cfg.nt, BT) < 0) continue;
+      for (int kb = wk.kb0; kb < wk.kb1; ++kb) {
         mbar_wait(&ctl.tempty[a], aph ^ 1, abort, p.err);
-        mbar_wait(&ctl.full[s], ph, abort, p.err);
+        const int i = (kb - wk.kb0) & 1;
+        const bool last = i == 1 || kb + 1 == wk.kb1;   // of the stage
+        if (i == 0) mbar_wait(&ctl.full[s], ph, abort, p.err);
         tc_fence_after();
-        const uint64_t dw = desc0 + s * (C::kStage >> 4), dx = dw + (kTileBytes >> 4);
+        const uint64_t dw = desc0 + (s * C::kStage + i * C::kGroup) / 16, dx = dw + kTileBytes / 16;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kFp8Group / 32; ++k) tc_mma_f8(tmem + a * BT, dw + k * 2, dx + k * 2, idesc, k > 0);
-          tc_commit(&ctl.empty[s]);
+          if (last) tc_commit(&ctl.empty[s]);
           tc_commit(&ctl.tfull[a]);
         }
         __syncwarp();
-        if (++s == cfg.stages) { s = 0; ph ^= 1; }
+        if (last && ++s == cfg.stages) { s = 0; ph ^= 1; }
         if (++a == C::kBufs) { a = 0; aph ^= 1; }
       }
     }
   } else if (warp == 2) {
     // ---------------- scales: a row of BT + 1 for each group
+    // (clusters have an item each for all blocks that an align writes)
+    if (cs > 1 && blockIdx.x == 0 && lane == 0 && items > (int)gridDim.x / cs) flag_error(p.err, MOE_LORA_DEVERR_CAPACITY);
     int s = 0;
     uint32_t ph = 0;
-    for (int it = cid; it < items; it += nclusters) {
-      const int b = it / cfg.nt, nt = it - b * cfg.nt, e = block_expert<MODE>(p, b, BT);
-      if (nt == 0 && rank == 0) flag_unit<MODE>(p, b, BT, e, lane);
+    while (wk.advance()) {
+      const int b = wk.it / cfg.nt, nt = wk.it - b * cfg.nt, e = block_expert<MODE>(p, b, BT);
+      if (nt == 0 && wk.rank == 0) flag_unit<MODE>(p, b, BT, e, lane);
       if (e < 0) continue;
       constexpr int kPer = (BT + 31) / 32;
       const float *src[kPer];
@@ -200,7 +253,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         src[j] = f < 0 ? nullptr : p.x_scales + (size_t)pair_row<MODE>(p, f) * p.KB;
       }
       const float *sw = p.w_scales + ((size_t)e * p.NB + nt) * p.KB;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = wk.kb0; kb < wk.kb1; ++kb) {
         mbar_wait(&ctl.sempty[s], ph ^ 1, abort, p.err);
         float *dst = scales + s * C::kScaleRow;
 #pragma unroll
@@ -217,15 +270,13 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(warp - 4) << 21);   // lane offset 32 * quarter in bits 16..31
     int s = 0, a = 0;
     uint32_t sph = 0, aph = 0;
-    int red = 0;
-    uint32_t rph = 0;
-    for (int it = cid; it < items; it += nclusters) {
-      const int b = it / cfg.nt, nt = it - b * cfg.nt;
+    while (wk.advance()) {
+      const int b = wk.it / cfg.nt, nt = wk.it - b * cfg.nt;
       if (block_expert<MODE>(p, b, BT) < 0) continue;
       float acc[BT];
 #pragma unroll
       for (int c = 0; c < BT; ++c) acc[c] = 0.f;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kb = wk.kb0; kb < wk.kb1; ++kb) {
         mbar_wait(&ctl.sfull[s], sph, abort, p.err);
         mbar_wait(&ctl.tfull[a], aph, abort, p.err);
         tc_fence_after();
@@ -266,58 +317,65 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         continue;
       }
       // Rank q sums the positions [q * tc, (q + 1) * tc) of every rank's
-      // partial sums, in rank order (one position: rank 0 does).
+      // partial sums, in rank order (one position: rank 0 does).  There is one
+      // item at most, so that the buffer is used once, and every CTA waits for
+      // all that is sent to it: nothing reaches a CTA that has left.
       const int tc = MODE == kFp8Naive ? 1 : BT / cs, lg = __ffs(tc) - 1;
-      const uint32_t red_base = smem_addr(smem + cfg.off_red) + red * C::kRedBytes;
-      const bool receives = MODE != kFp8Naive || rank == 0;
-      if (row == 0 && receives) mbar_arrive_expect_tx(&ctl.red_full[red], (MODE == kFp8Naive ? cs : BT) * kRows * 4);
-      mbar_wait_cluster(&ctl.red_empty[red], rph ^ 1, abort, p.err);
+      const uint32_t red_base = smem_addr(smem + cfg.off_red), red_bar = smem_addr(&ctl.red_full);
+      const bool receives = MODE != kFp8Naive || wk.rank == 0;
+      if (row == 0 && receives) mbar_arrive_expect_tx(&ctl.red_full, (MODE == kFp8Naive ? cs : BT) * kRows * 4);
+      cluster_wait();
+      waited = true;
       if constexpr (MODE == kFp8Naive) {
-        st_async_f1(cluster_map(red_base + (rank * kRows + row) * 4, 0), acc[0],
-                    cluster_map(smem_addr(&ctl.red_full[red]), 0));
-      } else {
+        st_async_f1(cluster_map(red_base + (wk.rank * kRows + row) * 4, 0), acc[0], cluster_map(red_bar, 0));
+      } else if (tc >= 4) {
 #pragma unroll
-        for (int c = 0; c < BT; c += 2) {
-          const int q = c >> lg, tl = c - (q << lg);
-          st_async_f2(cluster_map(red_base + (((rank * tc + tl) >> 1) * kRows + row) * 8, q), acc[c], acc[c + 1],
-                      cluster_map(smem_addr(&ctl.red_full[red]), q));
+        for (int c = 0; c < BT; c += 4) {
+          const int q = c >> lg, quad = (c - (q << lg)) >> 2;
+          st_async_v4(cluster_map(red_base + (((wk.rank * tc) >> 2) + quad) * kRows * 16 + row * 16, q),
+                      make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]), cluster_map(red_bar, q));
         }
+      } else {   // two positions a rank
+#pragma unroll
+        for (int c = 0; c < BT; c += 2)
+          st_async_f2(cluster_map(red_base + (wk.rank * kRows + row) * 8, c >> 1), acc[c], acc[c + 1],
+                      cluster_map(red_bar, c >> 1));
       }
-      if (receives) {
-        mbar_wait_cluster(&ctl.red_full[red], rph, abort, p.err);
-        const float *buf = reinterpret_cast<const float *>(smem + cfg.off_red + red * C::kRedBytes);
+      if (!receives) continue;
+      mbar_wait_cluster(&ctl.red_full, 0, abort, p.err);
+      const float *buf = reinterpret_cast<const float *>(smem + cfg.off_red);
+      auto finish = [&](auto ranks) {
+        constexpr int CS = decltype(ranks)::value;
         if constexpr (MODE == kFp8Naive) {
-          float v = 0.f;
-          for (int q = 0; q < cs; ++q) v += buf[q * kRows + row];
-          store(b, v);
-        } else {
-          for (int tl = 0; tl < tc; tl += 2) {
-            float v0 = 0.f, v1 = 0.f;
-            for (int q = 0; q < cs; ++q) {
-              const float2 u = *reinterpret_cast<const float2 *>(buf + (((q * tc + tl) >> 1) * kRows + row) * 2);
-              v0 += u.x;
-              v1 += u.y;
-            }
-            store(block_pair<MODE>(p, b, rank * tc + tl, BT), v0);
-            store(block_pair<MODE>(p, b, rank * tc + tl + 1, BT), v1);
+          float v[1];
+          sum_ranks<CS>(buf, 1, 0, row, v);
+          store(b, v[0]);
+        } else if constexpr (BT / CS >= 4) {
+#pragma unroll 4
+          for (int quad = 0; quad < BT / CS / 4; ++quad) {
+            float v[4];
+            sum_ranks<CS>(buf, BT / CS / 4, quad, row, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store(block_pair<MODE>(p, b, wk.rank * (BT / CS) + quad * 4 + i, BT), v[i]);
           }
+        } else {
+          float v[2];
+          sum_ranks<CS>(buf, 1, 0, row, v);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) store(block_pair<MODE>(p, b, wk.rank * 2 + i, BT), v[i]);
         }
-      }
-      // the buffer may be written again once every rank has read its own
-      named_barrier(1, 128);
-      if (row < cs) mbar_arrive_remote(cluster_map(smem_addr(&ctl.red_empty[red]), row));
-      if (++red == 2) { red = 0; rph ^= 1; }
+      };
+      if (cs == 2) finish(std::integral_constant<int, 2>());
+      else if (cs == 4) finish(std::integral_constant<int, 4>());
+      else finish(std::integral_constant<int, 8>());
     }
   }
+  if (cs > 1 && !waited) cluster_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
-  }
-  if (cs > 1) {   // no CTA leaves while a peer may still arrive on its barriers
-    cluster_arrive_release();
-    cluster_wait();
   }
 }
 
@@ -723,11 +781,11 @@ int resident_clusters(Kernel kernel, const Fp8Cfg &cfg, int threads, const Devic
   return clusters;
 }
 
-// Upper bound of the call's blocks.
+// Upper bound of the call's units (skipped ones included).
 long long block_bound(const Fp8Args &a, Fp8Mode mode, int bt) {
   if (mode == kFp8Dense) return ((long long)a.pairs + bt - 1) / bt;
   if (mode == kFp8Naive) return a.pairs;
-  return std::min<long long>((long long)a.max_blocks * (a.block / bt), fused_block_bound(a.pairs, 1, a.E, 1, bt));
+  return std::min<long long>(a.max_blocks, fused_block_bound(a.pairs, 1, a.E, 1, a.block)) * (a.block / bt);
 }
 
 template <int BT, int MODE>
@@ -738,17 +796,19 @@ int launch_narrow(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) 
   const long long items = block_bound(a, (Fp8Mode)MODE, BT) * cfg.nt;
   if (items <= 0) return 0;
   if (items > INT32_MAX) return MOE_LORA_ERR_UNSUPPORTED;
-  // K is split over a cluster while there are too few items for the SMs, each
-  // CTA keeps two groups and the clusters fit at once.  A ring no longer than
-  // a CTA's share lets more of them fit (clusters of 8 with 200 KB each: 15).
+  // Clusters that split K: while there are too few items for the SMs, as large
+  // as leaves each CTA two groups and every item a cluster of its own.  A ring
+  // no longer than a CTA's share lets more clusters fit (of 8 CTAs with 200 KB
+  // each: 15).  (Pairs that split the last of several rounds cost more than
+  // they gave: gpt-oss-shaped w2 decode 146 us against 140.)
   auto shape = [&](int cs) {
     cfg.cluster = cs;
-    const int fixed = kScaleSlots * C::kScaleRow * 4 + (cs > 1 ? 2 * C::kRedBytes : 0) + (int)sizeof(NarrowCtrl) + 128;
-    const long long share = ((long long)a.KB + cs - 1) / cs * ((items * cs + dev.sm_count - 1) / dev.sm_count);
-    cfg.stages = (int)std::max(2ll, std::min<long long>(share, std::min(kMaxRing, (200 * 1024 - fixed) / C::kStage)));
+    const int fixed = kScaleSlots * C::kScaleRow * 4 + (cs > 1 ? C::kRedBytes : 0) + (int)sizeof(NarrowCtrl) + 128;
+    const int share = items * cs <= dev.sm_count ? ((a.KB + cs - 1) / cs + 1) / 2 : kMaxRing;
+    cfg.stages = std::max(2, std::min(share, std::min(kMaxRing, (200 * 1024 - fixed) / C::kStage)));
     cfg.off_scale = cfg.stages * C::kStage;
     cfg.off_red = cfg.off_scale + kScaleSlots * C::kScaleRow * 4;
-    cfg.off_ctrl = cfg.off_red + (cs > 1 ? 2 * C::kRedBytes : 0);
+    cfg.off_ctrl = cfg.off_red + (cs > 1 ? C::kRedBytes : 0);
     cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(NarrowCtrl);
     return resident_clusters(fp8_narrow_kernel<BT, MODE>, cfg, kNarrowThreads, dev);
   };
