@@ -451,9 +451,9 @@ int moe_lora_align_static_workspace(const int32_t *topk_ids, const int32_t *toke
  *   moe_align_block_size      router's topk_ids -> blocks
  *   moe_fp8_grouped_matmul    w13: y13 = x . w13[e]^T
  *   moe_lora_fused_*          y13 += adapters (reads the bf16 x)
- *   moe_silu_mul_fp8          silu(gate) * up -> q, scales
+ *   moe_silu_mul_fp8          silu(gate) * up -> act (bf16), q, scales
  *   moe_fp8_grouped_matmul    w2, rows per pair, times the router's weights
- *   moe_lora_fused_*          y2 += adapters
+ *   moe_lora_fused_*          y2 += adapters (reads act)
  *   moe_add_rms_norm_fp8      the next norm sums each token's top-k rows of y2
  *
  * 8-bit values are e4m3 (finite: 448 is the largest, 0x7f and 0xff are NaN).
@@ -503,14 +503,17 @@ int moe_add_rms_norm_fp8(const moe_lora_bf16 *x, long long ldx, long long ld_par
 /*
  * moe_silu_mul_fp8 -- the gated activation with an 8-bit output:
  *   a = x[r][c] / (1 + exp(-x[r][c])) * x[r][I + c]     (fp32, c < I)
- * and scales and q of a as above.  The gate is in columns [0, I) of a row of
- * x, the up projection in [I, 2I), as two slices of one w13 product.
+ *   act[r][c] = bf16(a)
+ * and scales and q of the fp32 a as above.  The gate is in columns [0, I) of a
+ * row of x, the up projection in [I, 2I), as two slices of one w13 product.
+ * act is what w2's adapters read.
  *   x  [device] bf16 [rows, ldx], ldx >= 2*I
+ *   act [device] bf16 [rows, ld_act], or NULL
  *   q  [device] e4m3 [rows, ldq], ldq >= I;  scales [device] fp32 [rows, ceil(I / 128)]
  * Sizes: rows >= 0, I >= 1; alignment as above.
  */
-int moe_silu_mul_fp8(const moe_lora_bf16 *x, long long ldx, moe_lora_fp8 *q, long long ldq, float *scales, int rows,
-                     int I, void *stream);
+int moe_silu_mul_fp8(const moe_lora_bf16 *x, long long ldx, moe_lora_bf16 *act, long long ld_act, moe_lora_fp8 *q,
+                     long long ldq, float *scales, int rows, int I, void *stream);
 
 /*
  * moe_fp8_matmul -- y[m][n] = bf16( sum_k x[m][k] * w[n][k] ), 8-bit operands
@@ -548,7 +551,7 @@ int moe_fp8_matmul(const moe_lora_fp8 *x, long long ldx, const float *x_scales, 
  *   workspace: moe_fp8_grouped_workspace_bytes(M, topk, num_experts, K,
  *     block_size) bytes, [device], 16-byte aligned; may be NULL when that is 0.
  *     Its contents need no initialisation and are overwritten.
- * Calls with at least 128 pairs an expert on average gather x into the order
+ * Calls with at least 24 pairs an expert on average gather x into the order
  * of the blocks (in the workspace) and run the kernel bound by the tensor
  * cores; others the one bound by the weight's bytes.  Sizes and limits as for
  * moe_align_block_size and moe_fp8_matmul.  An expert id out of range skips its

@@ -87,7 +87,7 @@ def lib() -> ctypes.CDLL:
             L.moe_add_rms_norm_fp8.restype = I
             L.moe_add_rms_norm_fp8.argtypes = [P, Q, Q, I, P, Q, P, F, P, Q, P, Q, P, Q, P, I, I, P]
             L.moe_silu_mul_fp8.restype = I
-            L.moe_silu_mul_fp8.argtypes = [P, Q, P, Q, P, I, I, P]
+            L.moe_silu_mul_fp8.argtypes = [P, Q, P, Q, P, Q, P, I, I, P]
             L.moe_fp8_matmul.restype = I
             L.moe_fp8_matmul.argtypes = [P, Q, P, P, Q, P, P, Q, I, I, I, P, P]
             L.moe_fp8_grouped_matmul.restype = I
@@ -461,17 +461,20 @@ def moe_add_rms_norm_fp8(x, weight, q, scales, residual=None, residual_out=None,
         _dense(scales, _F32, "scales", M * -(-H // FP8_GROUP)), M, H, _raw_stream(stream, q)), "moe_add_rms_norm_fp8")
 
 
-def moe_silu_mul_fp8(x, q, scales, stream=None):
+def moe_silu_mul_fp8(x, q, scales, act=None, stream=None):
     """silu(gate) * up with an 8-bit output; see include/moe_lora.h.
 
     x: bf16 [..., 2*I], gate then up.  q: float8_e4m3fn [..., I]; scales:
-    float32 [..., ceil(I / 128)].  Rows may be strided, evenly."""
+    float32 [..., ceil(I / 128)]; act: bf16 [..., I] or None.  Rows may be
+    strided, evenly."""
     I = q.shape[-1]
     rows = q.numel() // I if I else 0
     px, ldx = _rows(x, _BF16, "x", rows, 2 * I)
+    pa, lda = (None, 0) if act is None else _rows(act, _BF16, "act", rows, I)
     pq, ldq = _rows(q, _F8, "q", rows, I)
-    _check((_lib or lib()).moe_silu_mul_fp8(px, ldx, pq, ldq, _dense(scales, _F32, "scales", rows * -(-I // FP8_GROUP)),
-                                            rows, I, _raw_stream(stream, q)), "moe_silu_mul_fp8")
+    _check((_lib or lib()).moe_silu_mul_fp8(px, ldx, pa, lda, pq, ldq,
+                                            _dense(scales, _F32, "scales", rows * -(-I // FP8_GROUP)), rows, I,
+                                            _raw_stream(stream, q)), "moe_silu_mul_fp8")
 
 
 def moe_fp8_matmul(x, x_scales, w, w_scales, y, err_flag=None, stream=None):

@@ -103,18 +103,20 @@ int moe_add_rms_norm_fp8(const moe_lora_bf16 *x, long long ldx, long long ld_par
   return launch_norm_fp8(a, dev, static_cast<cudaStream_t>(stream));
 }
 
-int moe_silu_mul_fp8(const moe_lora_bf16 *x, long long ldx, moe_lora_fp8 *q, long long ldq, float *scales, int rows,
-                     int I, void *stream) {
+int moe_silu_mul_fp8(const moe_lora_bf16 *x, long long ldx, moe_lora_bf16 *act, long long ld_act, moe_lora_fp8 *q,
+                     long long ldq, float *scales, int rows, int I, void *stream) {
   if (rows < 0 || I < 1) return MOE_LORA_ERR_INVALID_ARG;
-  if (!ld_ok(ldx, 2ll * I) || !ld_ok(ldq, I)) return MOE_LORA_ERR_INVALID_ARG;
+  if (!ld_ok(ldx, 2ll * I) || !ld_ok(ldq, I) || (act && !ld_ok(ld_act, I))) return MOE_LORA_ERR_INVALID_ARG;
   if (I > INT32_MAX - 256) return MOE_LORA_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_LORA_OK;
   if (!x || !q || !scales) return MOE_LORA_ERR_INVALID_ARG;
-  if (!on(x, 2) || !on(scales, 4)) return MOE_LORA_ERR_MISALIGNED;
+  if (!on(x, 2) || !on(act, 2) || !on(scales, 4)) return MOE_LORA_ERR_MISALIGNED;
   DeviceInfo dev;
   if (int st = current_device_info(&dev)) return st;
   ActArgs a = {};
   a.x = x;
+  a.act = act;
+  a.ld_act = act ? ld_act : 0;
   a.q = q;
   a.scales = scales;
   a.ldx = ldx;

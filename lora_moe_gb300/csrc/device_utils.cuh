@@ -101,6 +101,45 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
   }
 }
 
+// mbar_wait in few registers, for loops that hold most of them: the clock in 32
+// bits of nanoseconds (which kWaitTimeoutNs fits).
+static_assert(kWaitTimeoutNs < 0xFFFFFFFFull - kSuspendHintNs, "a 32-bit clock must show the limit");
+__device__ __forceinline__ uint32_t global_timer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ void mbar_wait_lean(uint32_t bar, uint32_t parity, volatile int *abort, int32_t *err) {
+  auto done = [&](bool sleep) {
+    uint32_t ok;
+    if (sleep)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}\n"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}\n"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity)
+          : "memory");
+    return ok != 0;
+  };
+  if (done(false)) return;
+  const uint32_t t0 = global_timer_lo();
+  while (!*abort && !done(true)) {
+    if (global_timer_lo() - t0 > (uint32_t)kWaitTimeoutNs) {
+      *abort = 1;
+      flag_error(err, MOE_LORA_DEVERR_TIMEOUT);
+    }
+  }
+}
+
 // Wait for the phase with the given parity, acquiring at cluster scope (for
 // phases completed by peers' remote arrivals or st.async writes).  Bounded
 // like mbar_wait.

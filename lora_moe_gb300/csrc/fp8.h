@@ -34,9 +34,10 @@ constexpr int kNormMaxH = 16384;
 // silu(gate) * up, 8-bit output.
 struct ActArgs {
   const uint16_t *x;   // bf16 [rows, ldx]: gate in columns [0, I), up in [I, 2I)
+  uint16_t *act;       // bf16 [rows, ld_act] or null
   uint8_t *q;          // e4m3 [rows, ldq]
   float *scales;       // fp32 [rows, groups]
-  long long ldx, ldq;
+  long long ldx, ld_act, ldq;
   int rows, I;
 };
 int launch_act_fp8(const ActArgs &a, const DeviceInfo &dev, cudaStream_t stream);

@@ -414,8 +414,9 @@ __global__ void __launch_bounds__(kGatherThreads)
   wait_for_prior_grid();
   const int nb = num_blocks(p);
   if (blockIdx.x == 0) {
-    // Tile list.  A block heads a tile when the blocks before it of the same
-    // expert are a multiple of 256 rows: blocks of one expert are neighbours.
+    // Tile list.  Blocks of one expert are neighbours: a run.  A block heads a
+    // tile when the blocks before it in its run are a multiple of 256 rows; the
+    // last block of a tile writes it down.
     __shared__ int warp_last[kGatherThreads / 32], warp_heads[kGatherThreads / 32], carry_first, carry_heads;
     if (tid == 0) carry_first = carry_heads = 0;
     __syncthreads();
@@ -423,8 +424,8 @@ __global__ void __launch_bounds__(kGatherThreads)
     for (int base = 0; base < nb; base += kGatherThreads) {
       const int b = base + tid;
       const int e = b < nb ? __ldg(p.expert_ids + b) : -1;
-      const bool first = b < nb && (b == 0 || __ldg(p.expert_ids + b - 1) != e);
-      int run = first ? b : -1;   // first block of b's run: the last `first` at or before b
+      const int before_e = b > 0 && b < nb ? __ldg(p.expert_ids + b - 1) : e, after_e = b + 1 < nb ? __ldg(p.expert_ids + b + 1) : e;
+      int run = b < nb && (b == 0 || before_e != e) ? b : -1;   // first block of b's run: the last such at or before b
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xFFFFFFFFu, run, d);
@@ -436,18 +437,16 @@ __global__ void __launch_bounds__(kGatherThreads)
       for (int w = 0; w < warp; ++w) before = max(before, warp_last[w]);
       run = max(run, before);
       const bool good = (unsigned)e < (unsigned)p.E;
-      const bool head = b < nb && good && (b - run) % per_tile == 0;
       if (b < nb && !good) flag_error(p.err, MOE_LORA_DEVERR_EXPERT_ID);
-      const uint32_t heads = __ballot_sync(0xFFFFFFFFu, head);
+      const int at = (b - run) % per_tile;   // place in the tile
+      const uint32_t heads = __ballot_sync(0xFFFFFFFFu, b < nb && good && at == 0);
       if (lane == 31) warp_heads[warp] = __popc(heads);
       __syncthreads();
-      int at = carry_heads + __popc(heads & ((1u << lane) - 1));
-      for (int w = 0; w < warp; ++w) at += warp_heads[w];
-      if (head) {
-        int n = 1;
-        while (n < per_tile && b + n < nb && __ldg(p.expert_ids + b + n) == e) ++n;
-        tiles[1 + at] = {b * bs, n * bs, e, 0};
-      }
+      int index = carry_heads + __popc(heads & (0xFFFFFFFFu >> (31 - lane)));   // heads up to b, b among them
+      for (int w = 0; w < warp; ++w) index += warp_heads[w];
+      // (tiles[0] is the count: tile i is tiles[1 + i])
+      if (b < nb && good && (at == per_tile - 1 || b + 1 == nb || after_e != e))
+        tiles[index] = {(b - at) * bs, (at + 1) * bs, e, 0};
       __syncthreads();
       if (tid == 0) {
         for (int w = 0; w < kGatherThreads / 32; ++w) {
@@ -511,7 +510,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < kWideStages; ++s) {
       mbar_init(&ctl.full[s], 1);
-      mbar_init(&ctl.empty[s], 1);
+      mbar_init(&ctl.empty[s], 2);   // a commit for each half of the columns
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&ctl.tfull[s], 1);
@@ -566,41 +565,43 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (++s == kWideStages) { s = 0; ph ^= 1; }
         }
       }
-    } else if (warp == 1 && rank == 0) {
-      // ---------------- MMA, for both CTAs: each half of the columns into an accumulator of its own
+    } else if (warp <= 2 && rank == 0) {
+      // ---------------- MMA, for both CTAs: a warp for each half of the
+      // columns, with accumulators of its own.  (An MMA takes 51 to 64 clk to
+      // issue, and 64 to run.)
       constexpr uint32_t idesc = make_idesc_e4m3(2 * kRows, kHalf);
+      const int h = warp - 1;
       const uint64_t desc0 = make_sdesc_sw128(smem_addr(smem));   // (addresses in units of 16 bytes)
       int s = 0, a = 0;
       uint32_t ph = 0, aph = 0;
       for (int it = first; it < items; it += step) {
         for (int kb = 0; kb < p.KB; ++kb) {
+          mbar_wait(&ctl.tempty[a + h], aph ^ 1, abort, p.err);
           mbar_wait(&ctl.full[s], ph, abort, p.err);
-          const uint64_t dx = desc0 + s * (kWideStage >> 4), dw = dx + (kTileBytes >> 4);
+          tc_fence_after();
+          const uint64_t dx = desc0 + s * (kWideStage >> 4), dw = dx + (kTileBytes >> 4) + h * (kTileBytes >> 5);
+          if (elect_one()) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            mbar_wait(&ctl.tempty[a + h], aph ^ 1, abort, p.err);
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-              for (int k = 0; k < kFp8Group / 32; ++k)
-                tc_mma_f8_pair(tmem + (a + h) * kHalf, dx + k * 2, dw + h * (kTileBytes >> 5) + k * 2, idesc, k > 0);
-              tc_commit_pair(&ctl.tfull[a + h]);
-              if (h == 1) tc_commit_pair(&ctl.empty[s]);
-            }
-            __syncwarp();
+            for (int k = 0; k < kFp8Group / 32; ++k)
+              tc_mma_f8_pair(tmem + (a + h) * kHalf, dx + k * 2, dw + k * 2, idesc, k > 0);
+            tc_commit_pair(&ctl.tfull[a + h]);
+            tc_commit_pair(&ctl.empty[s]);
           }
+          __syncwarp();
           if (++s == kWideStages) { s = 0; ph ^= 1; }
           a ^= 2;
           if (a == 0) aph ^= 1;
         }
       }
     }
+    __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWideRegsEpilogue));
     // ---------------- epilogue: this thread's row, one half (128 columns: one scale) of the output tile
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_addr = tmem + ((uint32_t)quarter << 21) + half * kHalf;
     const uint32_t tempty0 = cluster_map(smem_addr(&ctl.tempty[half]), 0);   // rank 0's
+    const uint32_t tfull0 = smem_addr(&ctl.tfull[half]);
     int a = 0;
     uint32_t aph = 0;
     for (int it = first; it < items; it += step) {
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       for (int kb = 0; kb < p.KB; ++kb) {
         const f32x2 sc2 = f2_pack(sc0, sc0);
         const float sx2 = load(sx, kb + 2, p.KB), sw2 = load(sw, kb + 2, p.KB);
-        mbar_wait(&ctl.tfull[a + half], aph, abort, p.err);
+        mbar_wait_lean(tfull0 + a * 8, aph, abort, p.err);
         tc_fence_after();
         const uint32_t src = lane_addr + a * kHalf;
         // the next 32 columns are on their way while these are added
@@ -867,7 +868,12 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
 // in flight (8192 x 8192: 19 us against 16).
 constexpr double kStreamBytes = 32e6;
 
-bool fp8_sorted_is_wide(const Fp8Args &a) { return a.pairs >= 128ll * a.E; }
+// The wide kernel from 24 pairs an expert on (on average): below that a call is
+// bound by the weight's bytes, and mostly empty tiles of 256 rows and the
+// gather cost more than the narrow kernel's units of 16 to 64.  Measured, 128
+// experts of 2048 x 1536: 16 pairs an expert 87 us narrow, 93 wide; 32: 96 and
+// 95; 64: 177 and 102.
+bool fp8_sorted_is_wide(const Fp8Args &a) { return a.pairs >= 24ll * a.E; }
 
 size_t fp8_sorted_workspace(const Fp8Args &a) {
   return fp8_sorted_is_wide(a) ? wide_space((long long)a.max_blocks * a.block, a.K).bytes : 0;
@@ -887,7 +893,11 @@ int launch_fp8_matmul(const Fp8Args &a, Fp8Mode mode, void *workspace, const Dev
   if (small && a.pairs <= 16) return launch_fp8_stream(a, mode, dev, s);
   if (a.pairs <= 16) return launch_narrow<16, kFp8Dense>(a, dev, s);
   if (a.pairs <= 32) return launch_narrow<32, kFp8Dense>(a, dev, s);
-  if (a.pairs <= 256) return launch_narrow<64, kFp8Dense>(a, dev, s);
+  // The narrow kernel while one round of its 64 x 128 items covers the output
+  // (192 x 4096 x 4096: 14.2 us, 16.2 wide), else the wide one (192 x 8192 x
+  // 8192: 27 us, 41 narrow).
+  const long long items = ((a.pairs + 63ll) / 64) * ((a.N + kRows - 1) / kRows);
+  if (a.pairs <= 64 || items <= dev.sm_count) return launch_narrow<64, kFp8Dense>(a, dev, s);
   return launch_wide<kFp8Dense>(a, nullptr, dev, s);
 }
 

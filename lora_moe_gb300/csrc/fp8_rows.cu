@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kActThreads, 8) act_fp8_kernel(const ActArgs p
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] = silu(a[i]) * b[i];
     const bool live = row[u] != 0xFFFFFFFFu;
+    if (p.act) store8<VEC>(p.act + (long long)row[u] * p.ld_act + grp[u] * kFp8Group + lane16 * 8, n[u], a);
     quantize8<VEC>(a, n[u], p.q + (long long)row[u] * p.ldq + grp[u] * kFp8Group + lane16 * 8,
                    p.scales + (size_t)row[u] * G.d + grp[u], live && lane16 == 0);
   }
@@ -271,7 +272,8 @@ int launch_norm_fp8(const NormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
 }
 
 int launch_act_fp8(const ActArgs &all, const DeviceInfo &dev, cudaStream_t s) {
-  const bool vec = all.I % 8 == 0 && aligned(all.x, 16) && all.ldx % 8 == 0 && aligned(all.q, 8) && all.ldq % 8 == 0;
+  const bool vec = all.I % 8 == 0 && aligned(all.x, 16) && all.ldx % 8 == 0 && aligned(all.q, 8) && all.ldq % 8 == 0 &&
+                   aligned(all.act, 16) && all.ld_act % 8 == 0;
   const int G = fp8_groups(all.I);
   const FastDiv div(G);
   // 31 bits of groups a launch
@@ -280,6 +282,7 @@ int launch_act_fp8(const ActArgs &all, const DeviceInfo &dev, cudaStream_t s) {
     ActArgs a = all;
     a.rows = (int)std::min<long long>(most, all.rows - r0);
     a.x += r0 * a.ldx;
+    if (a.act) a.act += r0 * a.ld_act;
     a.q += r0 * a.ldq;
     a.scales += r0 * G;
     const uint32_t items = (uint32_t)a.rows * G;

@@ -19,7 +19,7 @@ def _norm(**kw):
 
 
 def _act(**kw):
-    a = dict(x=P0, ldx=512, q=P0, ldq=256, scales=P0, rows=2, I=256, stream=None)
+    a = dict(x=P0, ldx=512, act=None, lda=0, q=P0, ldq=256, scales=P0, rows=2, I=256, stream=None)
     a.update(kw)
     return B.lib().moe_silu_mul_fp8(*a.values())
 
@@ -58,7 +58,8 @@ def test_norm(want, kw):
 @pytest.mark.parametrize("want,kw", [
     (INVALID, dict(rows=-1)), (INVALID, dict(I=0)), (INVALID, dict(ldx=511)), (INVALID, dict(ldq=255)),
     (INVALID, dict(x=None)), (INVALID, dict(q=None)), (INVALID, dict(scales=None)), (MISALIGNED, dict(x=P0 + 1)),
-    (MISALIGNED, dict(scales=P0 + 1)), (OK, dict(rows=0))])
+    (MISALIGNED, dict(scales=P0 + 1)), (INVALID, dict(act=P0, lda=255)), (MISALIGNED, dict(act=P0 + 1, lda=256)),
+    (OK, dict(rows=0))])
 def test_act(want, kw):
     assert _act(**kw) == want
 

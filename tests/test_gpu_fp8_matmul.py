@@ -44,14 +44,16 @@ def test_dense(M, N, K):
     _dense(M, N, K)
 
 
-@pytest.mark.parametrize("M,N,K", [(5, 264, 400), (40, 100, 77), (300, 700, 333), (130, 512, 4096)])
+@pytest.mark.parametrize("M,N,K", [(5, 264, 400), (40, 100, 77), (300, 700, 333), (130, 512, 4096), (2000, 700, 333),
+                                   (5000, 260, 129)])
 @pytest.mark.parametrize("pad,ypad", [(0, 1), (40, 8), (16, 5)])
 def test_dense_strided(M, N, K, pad, ypad):
     _dense(M, N, K, pad, ypad)
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 7168), (1, 64, 16384), (16, 128, 8192), (2048, 1100, 640),
-                                   (8192, 128, 256), (300, 20000, 128)])
+                                   (8192, 128, 256), (300, 20000, 128), (6000, 300, 1), (1500, 2049, 500), (20000, 1, 300),
+                                   (3, 9000, 9000), (16, 5000, 8192)])
 def test_dense_long(M, N, K):
     _dense(M, N, K)
 
@@ -63,7 +65,7 @@ def test_dense_empty():
                      torch.empty((0, 64), dtype=BF, device="cuda"))
 
 
-@pytest.mark.parametrize("M", [3, 300])
+@pytest.mark.parametrize("M", [3, 40, 300, 4000])
 def test_dense_nan_stays_in_its_row_and_column(M):
     g = _gen(M)
     x, xs = f8_rows(M, 256, g)
@@ -79,7 +81,7 @@ def test_dense_nan_stays_in_its_row_and_column(M):
     assert not bad.any() and err.item() == 0
 
 
-@pytest.mark.parametrize("M", [2, 300])
+@pytest.mark.parametrize("M", [2, 40, 300, 20000])
 def test_dense_infinite_and_zero_scales(M):
     g = _gen(M)
     x, xs = f8_rows(M, 384, g)

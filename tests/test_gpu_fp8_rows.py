@@ -147,12 +147,17 @@ def test_act(rows, I, pad):
     x = strided(rows, 2 * I, BF, pad)
     x.copy_(4 * torch.randn((rows, 2 * I), generator=g, device="cuda"))
     q, scales = strided(rows, I, F8, pad), torch.full((rows, groups(I)), float("nan"), device="cuda")
-    B.moe_silu_mul_fp8(x, q, scales)
+    act = strided(rows, I, BF, pad) if rows != 33 else None
+    B.moe_silu_mul_fp8(x, q, scales, act=act)
     gate, up = x[:, :I].double(), x[:, I:].double()
     v = gate / (1 + torch.exp(-gate)) * up
     assert_f8_close(q, scales, v, quantize64(v), ACT_REL, "act")
+    if act is not None:
+        assert_bf16_close(act, v, v.abs() * ACT_REL, "act")
     if pad:
         assert torch.isnan(q.as_strided((rows, I + pad), (I + pad, 1))[:, I:].float()).all()
+        if act is not None:
+            assert torch.isnan(act.as_strided((rows, I + pad), (I + pad, 1))[:, I:]).all()
 
 
 def test_act_extremes():
