@@ -9,6 +9,7 @@ so a missing library is an error.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -22,6 +23,7 @@ PATH_AUTO, PATH_CUDA_CORE, PATH_TCGEN05, PATH_CUDA_CORE_CLUSTER, PATH_CUDA_CORE_
 DEVERR_EXPERT_ID, DEVERR_LORA_ID, DEVERR_CAPACITY, DEVERR_PAIR_ID, DEVERR_TIMEOUT = 1, 2, 4, 8, 16
 
 _lib = None
+_fast = None     # fastcall.so's functions, or a stand-in
 _lock = threading.Lock()
 
 
@@ -363,6 +365,37 @@ def moe_lora_test_withheld_copy(x, lora_a, lora_b, y, topk_ids, token_lora_mappi
     _check(st, "moe_lora_test_withheld_copy")
 
 
+class _NoFast:
+    """Stands in for fastcall.so where it was not built: every call goes through ctypes."""
+
+    @staticmethod
+    def norm(*args):
+        return None
+
+    act = matmul = grouped = naive = norm
+
+
+def _load_fast():
+    """fastcall.so's functions: they take the common case of the 8-bit
+    operators' calls (ordinary tensors on the current device, its current
+    stream) and return None for any other, which the functions below treat."""
+    global _fast
+    L = lib()
+    with _lock:
+        if _fast is None:
+            if os.path.exists(_build.FASTCALL):
+                spec = importlib.util.spec_from_file_location("fastcall", _build.FASTCALL)
+                fast = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(fast)
+                fast.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+                    L.moe_add_rms_norm_fp8, L.moe_silu_mul_fp8, L.moe_fp8_matmul, L.moe_fp8_grouped_matmul,
+                    L.moe_fp8_grouped_matmul_naive, L.moe_fp8_grouped_workspace_bytes)])
+                _fast = fast
+            else:
+                _fast = _NoFast
+    return _fast
+
+
 FP8_GROUP = 128   # columns that share a scale
 
 _BF16, _F8, _F32, _I32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.int32
@@ -435,6 +468,10 @@ def moe_add_rms_norm_fp8(x, weight, q, scales, residual=None, residual_out=None,
     x: bf16 [M, H], or [M, parts, H] (a token's rows, summed).  residual,
     residual_out, normed: bf16 [M, H] or None.  q: float8_e4m3fn [M, H];
     scales: float32 [M, ceil(H / 128)].  Rows may be strided."""
+    if stream is None:
+        st = (_fast or _load_fast()).norm(x, weight, q, scales, residual, residual_out, normed, eps)
+        if st is not None:
+            return _check(st, "moe_add_rms_norm_fp8")
     shape = x.shape
     M, H = shape[0], shape[-1]
     parts, ld_part = 1, 0
@@ -467,6 +504,10 @@ def moe_silu_mul_fp8(x, q, scales, act=None, stream=None):
     x: bf16 [..., 2*I], gate then up.  q: float8_e4m3fn [..., I]; scales:
     float32 [..., ceil(I / 128)]; act: bf16 [..., I] or None.  Rows may be
     strided, evenly."""
+    if stream is None:
+        st = (_fast or _load_fast()).act(x, q, scales, act)
+        if st is not None:
+            return _check(st, "moe_silu_mul_fp8")
     I = q.shape[-1]
     rows = q.numel() // I if I else 0
     px, ldx = _rows(x, _BF16, "x", rows, 2 * I)
@@ -484,6 +525,10 @@ def moe_fp8_matmul(x, x_scales, w, w_scales, y, err_flag=None, stream=None):
     x: float8_e4m3fn [M, K], x_scales: float32 [M, ceil(K / 128)]; w:
     float8_e4m3fn [N, K], w_scales: float32 [ceil(N / 128), ceil(K / 128)]; y:
     bf16 [M, N].  Rows of x, w and y may be strided (x, w: by multiples of 16)."""
+    if stream is None:
+        st = (_fast or _load_fast()).matmul(x, x_scales, w, w_scales, y, err_flag)
+        if st is not None:
+            return _check(st, "moe_fp8_matmul")
     M, N = y.shape
     K = x.shape[-1]
     kb = -(-K // FP8_GROUP)
@@ -526,6 +571,11 @@ def moe_fp8_grouped_matmul(x, x_scales, w, w_scales, y, sorted_token_ids, expert
     [M, topk] or None.  workspace: a uint8 tensor of at least
     fp8_grouped_workspace_bytes(...) bytes; without one, calls that need one
     take it from torch's allocator."""
+    if stream is None:
+        st = (_fast or _load_fast()).grouped(x, x_scales, w, w_scales, y, topk_weights, bool(x_per_pair), err_flag,
+                                           sorted_token_ids, expert_ids, num_tokens_post_padded, block_size)
+        if st is not None:
+            return _check(st, "moe_fp8_grouped_matmul")
     M, topk, E, K, N, operands = _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair)
     L = _lib or lib()
     raw = _raw_stream(stream, y)
@@ -553,6 +603,10 @@ def moe_fp8_grouped_matmul_naive(x, x_scales, w, w_scales, y, topk_ids, topk_wei
                                  err_flag=None, stream=None):
     """moe_fp8_grouped_matmul without an align, one work item per (token,
     top-k) pair; topk_ids: int32 [M, topk]."""
+    if stream is None:
+        st = (_fast or _load_fast()).naive(x, x_scales, w, w_scales, y, topk_weights, bool(x_per_pair), err_flag, topk_ids)
+        if st is not None:
+            return _check(st, "moe_fp8_grouped_matmul_naive")
     M, topk, E, K, N, operands = _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair)
     _check((_lib or lib()).moe_fp8_grouped_matmul_naive(
         *operands, _dense(topk_ids, _I32, "topk_ids", M * topk), M, topk, E, K, N,

@@ -1,13 +1,17 @@
 """Build libmoe_lora.so (the CUDA library) in-tree with nvcc for sm_103a.
 
 Translation units are compiled in parallel, then linked into
-lora_moe_gb300/_build/libmoe_lora.so.  Usage: python -m lora_moe_gb300.build
+lora_moe_gb300/_build/libmoe_lora.so.  Beside it, where Python's headers are
+installed, fastcall.so: the 8-bit operators' calls from Python without ctypes
+(a C++ extension against torch's headers; without it they go through ctypes).
+Usage: python -m lora_moe_gb300.build
 """
 import concurrent.futures
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +21,7 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmoe_lora.so")
 SOURCES = ["api.cu", "align.cu", "fused_cuda_core.cu", "fused_tcgen05.cu", "stream_pipeline.cu",
            "fused_stream_cluster.cu", "align_static_workspace.cu", "api_fp8.cu", "fp8_rows.cu", "fp8_matmul.cu", "fp8_stream.cu"]
+FASTCALL = os.path.join(OUT_DIR, "fastcall.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -34,6 +39,28 @@ def _cuda_lib_dir(nvcc):
 def _inputs_mtime():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "moe_lora.h"), __file__]
     return max(os.path.getmtime(f) for f in files)
+
+
+def _has_python_headers():
+    return os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+
+
+def _build_fastcall():
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    include, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    tmp = FASTCALL + ".tmp.%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", include,
+           "-isystem", os.path.join(include, "torch", "csrc", "api", "include"), "-isystem", cuda,
+           os.path.join(CSRC, "fastcall.cpp"), "-o", tmp, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python", "-Wl,-rpath," + lib]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed for fastcall.cpp:\n%s\n%s" % (res.stdout, res.stderr))
+    os.replace(tmp, FASTCALL)
 
 
 def build(force=False, verbose=False, ptxas_info=False):
@@ -56,8 +83,11 @@ def build(force=False, verbose=False, ptxas_info=False):
             sys.stderr.write(res.stdout + res.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        fast = ex.submit(_build_fastcall) if _has_python_headers() else None
         objs = list(ex.map(compile_one, SOURCES))
+        if fast is not None:
+            fast.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs + [
         "-Xlinker", "-rpath," + _cuda_lib_dir(nvcc)]
