@@ -656,7 +656,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // lines an instruction: 4096 clk a tile).
       const float w = f < 0 ? 0.f : pair_weight<MODE>(p, f);
       const int n0 = nblk * kRows;
-      const bool vec = (p.ldy & 7) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
+      // 16 bytes at a time where rows are on 16 bytes and the 128 columns exist
+      const bool whole = (p.ldy & 7) == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0 && n0 + kRows <= p.N;
       uint8_t *out = smem + kWideStages * kWideStage + (warp - 4) * kWideOut;
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
@@ -674,20 +675,26 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         __syncwarp();
         const int chunk = lane & 7, n = n0 + part * 64 + chunk * 8;
+        uint4 o[8];
+        int fr[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int r = i * 4 + (lane >> 3);
-          const int fr = __shfl_sync(0xFFFFFFFFu, f, r);
-          const uint4 o = *reinterpret_cast<const uint4 *>(out + r * 128 + ((chunk ^ (r & 7)) << 4));
-          if (fr < 0 || n >= p.N) continue;
-          uint16_t *dst = p.y + (size_t)fr * p.ldy + n;
-          if (vec && n + 8 <= p.N) {
-            *reinterpret_cast<uint4 *>(dst) = o;
-          } else {
-            const uint32_t v[4] = {o.x, o.y, o.z, o.w};
+          fr[i] = __shfl_sync(0xFFFFFFFFu, f, r);
+          o[i] = *reinterpret_cast<const uint4 *>(out + r * 128 + ((chunk ^ (r & 7)) << 4));
+        }
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (fr[i] >= 0) *reinterpret_cast<uint4 *>(p.y + (size_t)fr[i] * p.ldy + n) = o[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t v[4] = {o[i].x, o[i].y, o[i].z, o[i].w};
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              if (n + j < p.N) dst[j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+              if (fr[i] >= 0 && n + j < p.N)
+                p.y[(size_t)fr[i] * p.ldy + n + j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
           }
         }
       }
