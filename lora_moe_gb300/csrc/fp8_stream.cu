@@ -55,11 +55,12 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // RG groups of 16 weight rows a CTA, K split over its other warps; NT tiles of 8 pairs.
+constexpr int ctas_per_sm(int mode) { return mode == kFp8Naive ? 3 : 2; }
 // Two groups of K in flight a warp, and registers for two CTAs an SM (three for
 // single pairs, whose items are many), measured best of 2 to 4 groups and 1 to
 // 3 CTAs.
 template <int NT, int RG, int MODE>
-__global__ void __launch_bounds__(kThreads, MODE == kFp8Naive ? 3 : 2) fp8_stream_kernel(const Fp8Args p, int tiles) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) fp8_stream_kernel(const Fp8Args p, int tiles) {
   constexpr int KS = kWarps / RG, kRowsCta = 16 * RG;
   constexpr int U = 2;
   __shared__ float red[kWarps][8 * NT][16 + 1];
@@ -195,13 +196,17 @@ int launch_rg(const Fp8Args &a, long long units, cudaStream_t stream) {
   return cudaLaunchKernelEx(&lc, fp8_stream_kernel<NT, RG, MODE>, a, tiles) == cudaSuccess ? 0 : MOE_LORA_ERR_LAUNCH;
 }
 
-// CTAs of 32 rows with K split in four while that leaves every SM eight CTAs'
-// worth of items (K of four groups or fewer: not split further than it has
-// groups for), else of 16 rows with K split in eight.
+// CTAs of 16, 32 or 64 rows, their eight warps splitting K in eight, four or
+// two: the fewest rows whose CTAs are all resident at once, as a second wave
+// costs more than a longer share of K (8 pairs of 2048 x 1536: 6.8 us with 384
+// CTAs of 32 rows, 7.9 with 768 of 16).  A short K is not split further than
+// it has groups for.
 template <int NT, int MODE>
 int launch_nt(const Fp8Args &a, long long units, const DeviceInfo &dev, cudaStream_t stream) {
-  if (a.KB <= 4 || units * ((a.N + 31) / 32) >= 8ll * dev.sm_count) return launch_rg<NT, 2, MODE>(a, units, stream);
-  return launch_rg<NT, 1, MODE>(a, units, stream);
+  auto fits = [&](int rg) { return units * ((a.N + 16 * rg - 1) / (16 * rg)) <= ctas_per_sm(MODE) * dev.sm_count; };
+  if (fits(1) && a.KB > 4) return launch_rg<NT, 1, MODE>(a, units, stream);
+  if (fits(2) && a.KB > 2) return launch_rg<NT, 2, MODE>(a, units, stream);
+  return launch_rg<NT, 4, MODE>(a, units, stream);
 }
 
 }  // namespace
