@@ -449,6 +449,14 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // the kernel was not launched as a dependent.
 __device__ __forceinline__ void wait_for_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// An ordinary load.  For what the preceding grid may have written, in a kernel
+// that starts before that grid has ended: __ldg() promises that the data do not
+// change while the kernel runs, and the compiler may move it above the wait.
+template <typename T>
+__device__ __forceinline__ T load_global(const T *p) {
+  return *p;
+}
+
 // True in one lane of a converged warp.  Around tcgen05 and bulk-copy
 // instructions inside a loop that the whole warp runs, it lets the compiler
 // keep their operands in uniform registers: an MMA issued under `lane == 0`

@@ -12,7 +12,7 @@ namespace moe_lora {
 
 // Blocks that the sorted arrays hold.
 __device__ __forceinline__ int num_blocks(const Fp8Args &p) {
-  const int n = __ldg(p.num_tokens_post_padded) / p.block;
+  const int n = load_global(p.num_tokens_post_padded) / p.block;
   return n < 0 ? 0 : (n > p.max_blocks ? p.max_blocks : n);
 }
 // The narrow kernel's units of bt positions: a block of the sorted arrays is
@@ -30,9 +30,9 @@ constexpr int kBadExpert = -1, kNoPairs = -2;
 template <int MODE>
 __device__ __forceinline__ int block_expert(const Fp8Args &p, int b, int bt) {
   if (MODE == kFp8Dense) return 0;
-  const int e = MODE == kFp8Sorted ? __ldg(p.expert_ids + b / (p.block / bt)) : __ldg(p.topk_ids + b);
+  const int e = MODE == kFp8Sorted ? load_global(p.expert_ids + b / (p.block / bt)) : load_global(p.topk_ids + b);
   if ((unsigned)e >= (unsigned)p.E) return kBadExpert;
-  if (MODE == kFp8Sorted && b % (p.block / bt) && __ldg(p.sorted_token_ids + (size_t)b * bt) == p.pairs) return kNoPairs;
+  if (MODE == kFp8Sorted && b % (p.block / bt) && load_global(p.sorted_token_ids + (size_t)b * bt) == p.pairs) return kNoPairs;
   return e;
 }
 // Pair at position t of block b, or -1.  `bt` positions a block.
@@ -41,7 +41,7 @@ __device__ __forceinline__ int block_pair(const Fp8Args &p, int b, int t, int bt
   if (MODE == kFp8Naive) return t == 0 ? b : -1;
   int f;
   if (MODE == kFp8Dense) f = b * bt + t;
-  else f = __ldg(p.sorted_token_ids + (size_t)b * bt + t);
+  else f = load_global(p.sorted_token_ids + (size_t)b * bt + t);
   return (unsigned)f < (unsigned)p.pairs ? f : -1;
 }
 template <int MODE>
@@ -58,14 +58,14 @@ __device__ __forceinline__ void flag_unit(const Fp8Args &p, int b, int bt, int e
   }
   if (MODE != kFp8Sorted) return;
   for (int t = lane; t < bt; t += 32) {
-    const int f = __ldg(p.sorted_token_ids + (size_t)b * bt + t);
+    const int f = load_global(p.sorted_token_ids + (size_t)b * bt + t);
     // neither a pair nor the sentinel, or (in a skipped unit) a pair after a sentinel
     if ((unsigned)f > (unsigned)p.pairs || (e == kNoPairs && f != p.pairs)) flag_error(p.err, MOE_LORA_DEVERR_PAIR_ID);
   }
 }
 template <int MODE>
 __device__ __forceinline__ float pair_weight(const Fp8Args &p, int f) {
-  return MODE != kFp8Dense && p.topk_weights ? __ldg(p.topk_weights + f) : 1.f;
+  return MODE != kFp8Dense && p.topk_weights ? load_global(p.topk_weights + f) : 1.f;
 }
 
 }  // namespace moe_lora

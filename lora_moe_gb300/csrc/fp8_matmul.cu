@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(kGatherThreads)
     const int per_tile = kTileRows / bs;
     for (int base = 0; base < nb; base += kGatherThreads) {
       const int b = base + tid;
-      const int e = b < nb ? __ldg(p.expert_ids + b) : -1;
-      const int before_e = b > 0 && b < nb ? __ldg(p.expert_ids + b - 1) : e, after_e = b + 1 < nb ? __ldg(p.expert_ids + b + 1) : e;
+      const int e = b < nb ? load_global(p.expert_ids + b) : -1;
+      const int before_e = b > 0 && b < nb ? load_global(p.expert_ids + b - 1) : e, after_e = b + 1 < nb ? load_global(p.expert_ids + b + 1) : e;
       int run = b < nb && (b == 0 || before_e != e) ? b : -1;   // first block of b's run: the last such at or before b
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kGatherThreads)
   // one warp a row
   const long long warps = (long long)gridDim.x * (kGatherThreads / 32);
   for (long long r = (long long)blockIdx.x * (kGatherThreads / 32) + warp; r < (long long)nb * bs; r += warps) {
-    const int f = __ldg(p.sorted_token_ids + r);
+    const int f = load_global(p.sorted_token_ids + r);
     if ((unsigned)f >= (unsigned)p.pairs) {
       if (f != p.pairs && lane == 0) flag_error(p.err, MOE_LORA_DEVERR_PAIR_ID);
       continue;
@@ -471,8 +471,8 @@ __global__ void __launch_bounds__(kGatherThreads)
     uint8_t *dst = xg + (size_t)r * ld;
     const int whole = p.K / 16;
     for (int c = lane; c < whole; c += 32)
-      *reinterpret_cast<uint4 *>(dst + c * 16) = __ldg(reinterpret_cast<const uint4 *>(src + c * 16));
-    for (int c = whole * 16 + lane; c < p.K; c += 32) dst[c] = __ldg(src + c);
+      *reinterpret_cast<uint4 *>(dst + c * 16) = load_global(reinterpret_cast<const uint4 *>(src + c * 16));
+    for (int c = whole * 16 + lane; c < p.K; c += 32) dst[c] = load_global(src + c);
   }
 }
 
@@ -529,12 +529,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   tc_fence_after();
   wait_for_prior_grid();
   const uint32_t tmem = ctl.tmem;
-  const int ntiles = MODE == kFp8Dense ? (p.pairs + kTileRows - 1) / kTileRows : __ldg(&g.tiles[0].row0);
+  const int ntiles = MODE == kFp8Dense ? (p.pairs + kTileRows - 1) / kTileRows : load_global(&g.tiles[0].row0);
   const int items = ntiles * cfg.nt;   // rows fastest: pairs at work share the weight's columns
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   auto tile = [&](int t) {
     if (MODE == kFp8Dense) return WideTile{t * kTileRows, min(kTileRows, p.pairs - t * kTileRows), 0, 0};
-    const int4 v = __ldg(reinterpret_cast<const int4 *>(g.tiles) + 1 + t);
+    const int4 v = load_global(reinterpret_cast<const int4 *>(g.tiles) + 1 + t);
     return WideTile{v.x, v.y, v.z, 0};
   };
 
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const WideTile t = tile(it - nt * ntiles);
       const int r = rank * kRows + quarter * 32 + lane;   // row of the tile
       int f = -1;
-      if (r < t.rows) f = MODE == kFp8Dense ? t.row0 + r : __ldg(p.sorted_token_ids + t.row0 + r);
+      if (r < t.rows) f = MODE == kFp8Dense ? t.row0 + r : load_global(p.sorted_token_ids + t.row0 + r);
       if ((unsigned)f >= (unsigned)p.pairs) f = -1;
       const int nblk = nt * 2 + half;
       const float *sx = f < 0 ? nullptr : p.x_scales + (size_t)pair_row<MODE>(p, f) * p.KB;
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
       for (int c = 0; c < 64; ++c) acc[c] = 0;
       // the scales of the next two groups are on their way
-      auto load = [](const float *s, int kb, int n) { return s && kb < n ? __ldg(s + kb) : 0.f; };
+      auto load = [](const float *s, int kb, int n) { return s && kb < n ? load_global(s + kb) : 0.f; };
       float sc0 = load(sx, 0, p.KB) * load(sw, 0, p.KB), sx1 = load(sx, 1, p.KB), sw1 = load(sw, 1, p.KB);
       for (int kb = 0; kb < p.KB; ++kb) {
         const f32x2 sc2 = f2_pack(sc0, sc0);
@@ -758,6 +758,7 @@ template <typename Kernel>
 int resident_clusters(Kernel kernel, const Fp8Cfg &cfg, int threads, const DeviceInfo &dev) {
   if (cfg.cluster == 1) return dev.sm_count;
   struct Entry {
+    const void *kernel;
     int device, cluster, smem, clusters;
   };
   static std::mutex mu;
@@ -765,7 +766,7 @@ int resident_clusters(Kernel kernel, const Fp8Cfg &cfg, int threads, const Devic
   static int n = 0;
   std::lock_guard<std::mutex> lock(mu);
   for (int i = 0; i < n; ++i)
-    if (known[i].device == dev.device && known[i].cluster == cfg.cluster && known[i].smem == cfg.smem_bytes)
+    if (known[i].kernel == (const void *)kernel && known[i].device == dev.device && known[i].cluster == cfg.cluster && known[i].smem == cfg.smem_bytes)
       return known[i].clusters;
   cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.smem_bytes);
   cudaLaunchConfig_t lc = {};
@@ -785,7 +786,7 @@ int resident_clusters(Kernel kernel, const Fp8Cfg &cfg, int threads, const Devic
     clusters = 0;
   }
   if (clusters < 1) clusters = std::max(1, dev.sm_count / cfg.cluster / 2);
-  if (n < 64) known[n++] = {dev.device, cfg.cluster, cfg.smem_bytes, clusters};
+  if (n < 64) known[n++] = {(const void *)kernel, dev.device, cfg.cluster, cfg.smem_bytes, clusters};
   return clusters;
 }
 

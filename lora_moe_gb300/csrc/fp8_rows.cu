@@ -29,11 +29,11 @@ template <bool VEC>
 __device__ __forceinline__ uint4 load8(const uint16_t *p, int n) {
   uint32_t w[4] = {0, 0, 0, 0};
   if constexpr (VEC) {
-    if (n > 0) return __ldg(reinterpret_cast<const uint4 *>(p));
+    if (n > 0) return load_global(reinterpret_cast<const uint4 *>(p));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) w[i >> 1] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
+      if (i < n) w[i >> 1] |= (uint32_t)load_global(p + i) << (16 * (i & 1));
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }

@@ -30,20 +30,21 @@ constexpr int kThreads = kWarps * 32;
 
 __device__ __forceinline__ uint4 load_weight(const uint8_t *p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");
   return r;
 }
 
 // 16 bytes of a row from column k on, zeros past the row's K columns; nothing
 // past them is read.
 __device__ __forceinline__ uint4 load_tail(const uint8_t *row, int k, int K) {
-  if (k + 16 <= K) return __ldg(reinterpret_cast<const uint4 *>(row + k));
+  if (k + 16 <= K) return load_global(reinterpret_cast<const uint4 *>(row + k));
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    if (k + i < K) w[i >> 2] |= (uint32_t)__ldg(row + k + i) << (8 * (i & 3));
+    if (k + i < K) w[i >> 2] |= (uint32_t)load_global(row + k + i) << (8 * (i & 3));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) fp8_stream_kernel
       for (int u = 0; u < U; ++u) {
         if (kb + u >= kb1) continue;
         const int k = (kb + u) * kFp8Group + 16 * t;
-        s[u] = __ldg(sw + kb + u);
+        s[u] = load_global(sw + kb + u);
         if (k - 16 * t + kFp8Group <= p.K) {
           a[u][0] = load_weight(w0 + k);
           a[u][1] = load_weight(w0 + k + 64);
@@ -129,15 +130,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) fp8_stream_kernel
           const int k = (kb + u) * kFp8Group + 16 * t;
           if (row[j] >= 0) {
             if (k - 16 * t + kFp8Group <= p.K) {
-              x[j][u][0] = __ldg(reinterpret_cast<const uint4 *>(xr + k));
-              x[j][u][1] = __ldg(reinterpret_cast<const uint4 *>(xr + k + 64));
+              x[j][u][0] = load_global(reinterpret_cast<const uint4 *>(xr + k));
+              x[j][u][1] = load_global(reinterpret_cast<const uint4 *>(xr + k + 64));
             } else {
               x[j][u][0] = load_tail(xr, k, p.K);
               x[j][u][1] = load_tail(xr, k + 64, p.K);
             }
           }
-          if (r0 >= 0) sx[j][u][0] = __ldg(s0 + kb + u);
-          if (r1 >= 0) sx[j][u][1] = __ldg(s1 + kb + u);
+          if (r0 >= 0) sx[j][u][0] = load_global(s0 + kb + u);
+          if (r1 >= 0) sx[j][u][1] = load_global(s1 + kb + u);
         }
       }
 #pragma unroll
