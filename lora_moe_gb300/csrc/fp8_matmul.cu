@@ -8,14 +8,20 @@
 // accumulation in tensor memory; the epilogue warps scale it into fp32
 // registers while the next groups are multiplied.
 //
-// Two kernels, both persistent, with a warp that loads (TMA), a warp that
-// issues the MMAs and epilogue warps:
+// Two kernels, both persistent, with warps that load (TMA), warps that issue
+// the MMAs and epilogue warps:
 //   narrow  the weight on the 128 rows of the MMA, 16 to 64 pairs on its
 //           columns: few pairs for each weight (decode), bound by the weight's
 //           bytes.  Where there are few items, clusters of CTAs split K, their
 //           partial sums exchanged through distributed shared memory and added
-//           in a fixed order.
-//   wide    128 pairs on the rows, 256 output columns: bound by the tensor cores.
+//           in a fixed order.  gpt-oss-shaped w2 decode (0.88 GB of weights):
+//           135 to 140 us, 6.3 to 6.6 TB/s.
+//   wide    pairs of CTAs (cta_group::2), 256 pairs by 256 output columns, on
+//           rows gathered into the blocks' order: bound by the tensor cores,
+//           the hand-shake with the epilogue and, over seconds, by power.
+//           8192 x 4096 x 4096 dense: 97 us (2.8 PFLOP/s; 110 us with the
+//           power limit reached); Mixtral-shaped w13 prefill: 1.49 ms (1.75).
+// Products of few rows and small weights are fp8_stream.cu's.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -32,12 +38,12 @@ namespace moe_lora {
 
 namespace {
 
-constexpr int kRows = 128;                     // M of every tcgen05.mma here
+constexpr int kRows = 128;                     // rows of an accumulator: lanes of tensor memory
 constexpr int kTileBytes = kRows * kFp8Group;  // 128 rows of one group: 16 KB, one swizzle row of 128 bytes each
 
 struct Fp8Maps {
-  CUtensorMap w;   // [E][N][K], box 1 x 128 x 128
-  CUtensorMap x;   // [rows][K], box BT x 128 (dense) or 1 x 128 (gathered)
+  CUtensorMap w;   // [E][N][K], box 1 x 128 (narrow) or 64 (wide) x 128
+  CUtensorMap x;   // [rows][K], box BT x 128 (dense), 1 x 128 (gathered by row) or 128 x 128 (wide)
 };
 
 // Launch shape of a call.
@@ -478,14 +484,24 @@ __global__ void __launch_bounds__(kGatherThreads)
 
 // The wide kernel: pairs of CTAs (cta_group::2), 256 rows by 256 output
 // columns.  Each CTA holds 128 of the rows and half of the weight's columns in
-// shared memory and 128 x 256 of the accumulators in tensor memory.
+// shared memory, 32 KB a group, and 128 x 256 of the accumulators in tensor
+// memory: four accumulators of 128 columns, two groups of two halves.
+// A group takes the tensor cores 512 clk, and about 750 in all (8192 x 4096 x
+// 4096 dense): the epilogue's reads and FMAs of an accumulator take 550 of the
+// 768 that pass before it is due again, the hand-shake over two CTAs the rest.
+// A single CTA with 128 x 256 tiles and two accumulators took 108 us, accumulators
+// handed back before their FMAs 104, sixteen epilogue warps 115, MMAs of 256
+// columns 99, against 97.
 constexpr int kWideThreads = 384;
 constexpr int kWideN = 256;
 constexpr int kHalf = kWideN / 2;
 constexpr int kWideStage = 2 * kTileBytes;       // 128 rows, and 128 columns of the weight
 constexpr int kWideStages = 6;
 constexpr int kWideOut = 32 * 128;               // an epilogue warp's rows on their way out: 32 rows of 64 bf16
-constexpr int kWideRegsIssue = 56, kWideRegsEpilogue = 216;   // registers a thread: loading and MMA warps, epilogue warps
+// Registers a thread: loading and MMA warps, epilogue warps.  A split by which
+// the compiler spills nothing: with 48 and 224, or 64 and 208, it spills 80 to
+// 136 bytes in the epilogue's loop (97 -> 145 us).
+constexpr int kWideRegsIssue = 56, kWideRegsEpilogue = 216;
 
 struct WideCtrl {
   uint64_t full[kWideStages], empty[kWideStages];
@@ -620,6 +636,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // the scales of the next two groups are on their way
       auto load = [](const float *s, int kb, int n) { return s && kb < n ? load_global(s + kb) : 0.f; };
       float sc0 = load(sx, 0, p.KB) * load(sw, 0, p.KB), sx1 = load(sx, 1, p.KB), sw1 = load(sw, 1, p.KB);
+#pragma unroll 1
       for (int kb = 0; kb < p.KB; ++kb) {
         const f32x2 sc2 = f2_pack(sc0, sc0);
         const float sx2 = load(sx, kb + 2, p.KB), sw2 = load(sw, kb + 2, p.KB);
@@ -675,26 +692,28 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
         __syncwarp();
         const int chunk = lane & 7, n = n0 + part * 64 + chunk * 8;
-        uint4 o[8];
-        int fr[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 4 + (lane >> 3);
-          fr[i] = __shfl_sync(0xFFFFFFFFu, f, r);
-          o[i] = *reinterpret_cast<const uint4 *>(out + r * 128 + ((chunk ^ (r & 7)) << 4));
-        }
-        if (whole) {
+        for (int i0 = 0; i0 < 8; i0 += 2) {
+          uint4 o[2];
+          int fr[2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (fr[i] >= 0) *reinterpret_cast<uint4 *>(p.y + (size_t)fr[i] * p.ldy + n) = o[i];
-        } else {
+          for (int i = 0; i < 2; ++i) {
+            const int r = (i0 + i) * 4 + (lane >> 3);
+            fr[i] = __shfl_sync(0xFFFFFFFFu, f, r);
+            o[i] = *reinterpret_cast<const uint4 *>(out + r * 128 + ((chunk ^ (r & 7)) << 4));
+          }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t v[4] = {o[i].x, o[i].y, o[i].z, o[i].w};
+          for (int i = 0; i < 2; ++i) {
+            if (fr[i] < 0) continue;
+            uint16_t *dst = p.y + (size_t)fr[i] * p.ldy + n;
+            if (whole) {
+              *reinterpret_cast<uint4 *>(dst) = o[i];
+            } else {
+              const uint32_t v[4] = {o[i].x, o[i].y, o[i].z, o[i].w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (fr[i] >= 0 && n + j < p.N)
-                p.y[(size_t)fr[i] * p.ldy + n + j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+              for (int j = 0; j < 8; ++j)
+                if (n + j < p.N) dst[j] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
+            }
           }
         }
       }
