@@ -27,6 +27,10 @@
  *       vLLM PR #32005, diff of vllm/lora/ops/triton_ops/fused_moe_lora_op.py
  *       (_adjust_kernel_inputs).
  *
+ * Beside the adapters, the 8-bit serving path of the same MoE layer (norm, base
+ * experts' products, activation): the moe_*_fp8 and moe_fp8_* entry points,
+ * below.
+ *
  * Conventions for every entry point:
  *   - Pointers marked [device] must be device pointers of the current CUDA
  *     device; [host] are host pointers.  bf16 tensors are passed as

@@ -319,7 +319,7 @@ static int naive_impl(const moe_lora_bf16 *x, int x_per_pair, const moe_lora_bf1
 
 extern "C" {
 
-int moe_lora_version(void) { return 100; }
+int moe_lora_version(void) { return 101; }
 
 const char *moe_lora_status_string(int status) {
   switch (status) {
