@@ -552,12 +552,12 @@ int moe_fp8_matmul(const moe_lora_fp8 *x, long long ldx, const float *x_scales, 
  *   sorted_token_ids, expert_ids, num_tokens_post_padded: as written by
  *     moe_align_block_size with the same M, topk, num_experts, block_size and
  *     capacities
- *   workspace: moe_fp8_grouped_workspace_bytes(M, topk, num_experts, K,
+ *   workspace: moe_fp8_grouped_workspace_bytes(M, topk, num_experts, K, N,
  *     block_size) bytes, [device], 16-byte aligned; may be NULL when that is 0.
  *     Its contents need no initialisation and are overwritten.
- * Calls with at least 24 pairs an expert on average gather x into the order
- * of the blocks (in the workspace) and run the kernel bound by the tensor
- * cores; others the one bound by the weight's bytes.  Sizes and limits as for
+ * Calls with at least 16 pairs an expert on average (and more than a round of
+ * work) gather x into the order of the blocks, in the workspace, and run the
+ * kernel bound by the tensor cores; others the one bound by the weight's bytes.  Sizes and limits as for
  * moe_align_block_size and moe_fp8_matmul.  An expert id out of range skips its
  * block (MOE_LORA_DEVERR_EXPERT_ID), a pair id that is neither a pair nor the
  * sentinel is skipped (MOE_LORA_DEVERR_PAIR_ID, as is a pair that follows 16 or
@@ -573,7 +573,7 @@ int moe_fp8_grouped_matmul(const moe_lora_fp8 *x, int x_per_pair, long long ldx,
 
 /* Bytes of workspace of a moe_fp8_grouped_matmul call with these sizes (0: none,
  * or invalid sizes).  Host only. */
-size_t moe_fp8_grouped_workspace_bytes(int M, int topk, int num_experts, int K, int block_size);
+size_t moe_fp8_grouped_workspace_bytes(int M, int topk, int num_experts, int K, int N, int block_size);
 
 /*
  * moe_fp8_grouped_matmul_naive -- the same without an align: each pair f is a

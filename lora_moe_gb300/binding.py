@@ -95,7 +95,7 @@ def lib() -> ctypes.CDLL:
             L.moe_fp8_grouped_matmul.restype = I
             L.moe_fp8_grouped_matmul.argtypes = [P, I, Q, P, P, Q, P, P, Q, P, P, P, P, I, I, I, I, I, I, I, I, P, S, P, P]
             L.moe_fp8_grouped_workspace_bytes.restype = S
-            L.moe_fp8_grouped_workspace_bytes.argtypes = [I, I, I, I, I]
+            L.moe_fp8_grouped_workspace_bytes.argtypes = [I, I, I, I, I, I]
             L.moe_fp8_grouped_matmul_naive.restype = I
             L.moe_fp8_grouped_matmul_naive.argtypes = [P, I, Q, P, P, Q, P, P, Q, P, P, I, I, I, I, I, P, P]
             _lib = L
@@ -554,9 +554,9 @@ def _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair):
                               _dense(topk_weights, _F32, "topk_weights", M * topk))
 
 
-def fp8_grouped_workspace_bytes(M, topk, num_experts, K, block_size) -> int:
+def fp8_grouped_workspace_bytes(M, topk, num_experts, K, N, block_size) -> int:
     """Bytes of workspace of a moe_fp8_grouped_matmul call with these sizes."""
-    return lib().moe_fp8_grouped_workspace_bytes(M, topk, num_experts, K, block_size)
+    return lib().moe_fp8_grouped_workspace_bytes(M, topk, num_experts, K, N, block_size)
 
 
 def moe_fp8_grouped_matmul(x, x_scales, w, w_scales, y, sorted_token_ids, expert_ids, num_tokens_post_padded,
@@ -571,7 +571,7 @@ def moe_fp8_grouped_matmul(x, x_scales, w, w_scales, y, sorted_token_ids, expert
     [M, topk] or None.  workspace: a uint8 tensor of at least
     fp8_grouped_workspace_bytes(...) bytes; without one, calls that need one
     take it from torch's allocator."""
-    if stream is None:
+    if stream is None and workspace is None:
         st = (_fast or _load_fast()).grouped(x, x_scales, w, w_scales, y, topk_weights, bool(x_per_pair), err_flag,
                                            sorted_token_ids, expert_ids, num_tokens_post_padded, block_size)
         if st is not None:
@@ -581,7 +581,7 @@ def moe_fp8_grouped_matmul(x, x_scales, w, w_scales, y, sorted_token_ids, expert
     raw = _raw_stream(stream, y)
     nbytes = 0
     if workspace is None:
-        nbytes = L.moe_fp8_grouped_workspace_bytes(M, topk, E, K, block_size)
+        nbytes = L.moe_fp8_grouped_workspace_bytes(M, topk, E, K, N, block_size)
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=y.device)
             if stream is not None:

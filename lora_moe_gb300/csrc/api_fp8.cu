@@ -157,9 +157,9 @@ int moe_fp8_matmul(const moe_lora_fp8 *x, long long ldx, const float *x_scales, 
   return launch_fp8_matmul(a, kFp8Dense, nullptr, dev, static_cast<cudaStream_t>(stream));
 }
 
-size_t moe_fp8_grouped_workspace_bytes(int M, int topk, int num_experts, int K, int block_size) {
+size_t moe_fp8_grouped_workspace_bytes(int M, int topk, int num_experts, int K, int N, int block_size) {
   if (M < 0 || topk < 1 || num_experts < 1 || num_experts > kMaxExperts || topk > num_experts || K < 1 ||
-      K > INT32_MAX - 128 || !valid_block(block_size))
+      K > INT32_MAX - 128 || N < 1 || N > INT32_MAX - 256 || !valid_block(block_size))
     return 0;
   const long long cap = (long long)M * topk + (long long)num_experts * (block_size - 1);
   if (cap > INT32_MAX / 2) return 0;
@@ -167,6 +167,7 @@ size_t moe_fp8_grouped_workspace_bytes(int M, int topk, int num_experts, int K, 
   a.pairs = M * topk;
   a.E = num_experts;
   a.K = K;
+  a.N = N;
   a.block = block_size;
   a.max_blocks = (int)(cap / block_size);
   return a.pairs == 0 ? 0 : fp8_sorted_workspace(a);

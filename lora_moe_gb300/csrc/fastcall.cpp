@@ -7,6 +7,7 @@
 // (another type, device or shape, uneven rows), for binding.py to treat or to
 // refuse with its message.  bind() gets the library's entry points.
 #include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
 #include <Python.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -200,7 +201,8 @@ PyObject *naive(PyObject *, PyObject *const *args, Py_ssize_t n) {
                                   (int)g.topk, (int)g.E, (int)g.K, (int)g.N, g.err, a.stream()));
 }
 
-// .., sorted_token_ids, expert_ids, num_tokens_post_padded, block_size; calls that need a workspace are binding.py's
+// .., sorted_token_ids, expert_ids, num_tokens_post_padded, block_size; the workspace, where the call needs one, from
+// torch's allocator (freed when the call has been enqueued: its next use is ordered behind it on this stream)
 PyObject *grouped(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (n != 12 || !PyLong_Check(args[11])) return none();
   Args a{args};
@@ -218,10 +220,12 @@ PyObject *grouped(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (!a.ready()) return none();
   const int64_t cap = THPVariable_Unpack(args[8]).numel(), capb = THPVariable_Unpack(args[9]).numel();
   if (cap > kIntMax || capb > kIntMax || THPVariable_Unpack(args[10]).numel() < 1) return none();
-  if (space_fn((int)g.M, (int)g.topk, (int)g.E, (int)g.K, (int)block)) return none();
+  const size_t need = space_fn((int)g.M, (int)g.topk, (int)g.E, (int)g.K, (int)g.N, (int)block);
+  at::Tensor space;
+  if (need) space = at::empty({(int64_t)need}, THPVariable_Unpack(args[4]).options().dtype(at::kByte));
   return PyLong_FromLong(grouped_fn(g.x, g.per_pair, g.ldx, g.xs, g.w, g.ldw, g.ws, g.y, g.ldy, g.weights, sorted,
                                     experts, padded, (int)g.M, (int)g.topk, (int)g.E, (int)g.K, (int)g.N, (int)block,
-                                    (int)cap, (int)capb, nullptr, 0, g.err, a.stream()));
+                                    (int)cap, (int)capb, need ? space.data_ptr() : nullptr, need, g.err, a.stream()));
 }
 
 // the entry points' addresses, in the order of the declarations above

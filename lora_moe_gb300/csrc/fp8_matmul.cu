@@ -10,8 +10,8 @@
 //
 // Two kernels, both persistent, with warps that load (TMA), warps that issue
 // the MMAs and epilogue warps:
-//   narrow  the weight on the 128 rows of the MMA, 16 to 64 pairs on its
-//           columns: few pairs for each weight (decode), bound by the weight's
+//   narrow  the weight on the 128 rows of the MMA, 16 pairs (dense: to 64) on
+//           its columns: few pairs for each weight (decode), bound by the weight's
 //           bytes.  Where there are few items, clusters of CTAs split K, their
 //           partial sums exchanged through distributed shared memory and added
 //           in a fixed order.  gpt-oss-shaped w2 decode (0.88 GB of weights):
@@ -887,20 +887,27 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
 
 }  // namespace
 
-// The wide kernel from 128 pairs an expert on (on average): below that a call
-// is bound by the weight's bytes, and tiles of 256 rows would be half empty.
 // Up to this many bytes of weights, calls of single pairs or of at most 16 rows
 // run the kernel that streams the weight through registers: it starts in half
 // the time (2048 x 2048 and one row: 2.5 us against 4.9), but has fewer bytes
 // in flight (8192 x 8192: 19 us against 16).
 constexpr double kStreamBytes = 32e6;
 
-// The wide kernel from 24 pairs an expert on (on average): below that a call is
-// bound by the weight's bytes, and mostly empty tiles of 256 rows and the
-// gather cost more than the narrow kernel's units of 16 to 64.  Measured, 128
-// experts of 2048 x 1536: 16 pairs an expert 87 us narrow, 93 wide; 32: 96 and
-// 95; 64: 177 and 102.
-bool fp8_sorted_is_wide(const Fp8Args &a) { return a.pairs >= 24ll * a.E; }
+// Sorted calls run the wide kernel from 16 pairs an expert on (on average), the
+// narrow one, in units of 16, below.  Below, a call is bound by the weight's
+// bytes, and tiles of 256 rows and the gather cost more than they give; above,
+// an expert's units read its weight again and again.  128 experts of 2048 x
+// 1536, us narrow / wide: 4 pairs an expert 66 / 86, 8 68 / 89, 16 76 / 92, 32
+// 123 / 95, 64 220 / 100; with a skewed router 4 70 / 74, 8 97 / 89, 16 113 / 96.
+// (Units of 32 and 64 were slower than of 16 wherever the narrow kernel wins:
+// 92 us at 16 pairs an expert, also over gathered rows.)
+// The narrow one also while a round of its items covers the output (16 experts
+// of 1024 x 1024 and 128 pairs: 10 us, 13 wide).
+constexpr long long kRoundItems = 152;
+bool fp8_sorted_is_wide(const Fp8Args &a) {
+  const long long units = a.pairs / 16 + std::min(a.E, a.pairs);
+  return a.pairs >= 16ll * a.E && units * ((a.N + kRows - 1) / kRows) > kRoundItems;
+}
 
 size_t fp8_sorted_workspace(const Fp8Args &a) {
   return fp8_sorted_is_wide(a) ? wide_space((long long)a.max_blocks * a.block, a.K).bytes : 0;
@@ -911,11 +918,7 @@ int launch_fp8_matmul(const Fp8Args &a, Fp8Mode mode, void *workspace, const Dev
   if (mode == kFp8Naive) return small ? launch_fp8_stream(a, mode, dev, s) : launch_narrow<16, kFp8Naive>(a, dev, s);
   if (mode == kFp8Sorted) {
     if (fp8_sorted_is_wide(a)) return launch_wide<kFp8Sorted>(a, workspace, dev, s);
-    // units of about twice an expert's average pairs, within the block
-    const int want = std::min<long long>(a.block, 2ll * a.pairs / a.E);
-    if (want <= 16) return launch_narrow<16, kFp8Sorted>(a, dev, s);
-    if (want <= 32) return launch_narrow<32, kFp8Sorted>(a, dev, s);
-    return launch_narrow<64, kFp8Sorted>(a, dev, s);
+    return launch_narrow<16, kFp8Sorted>(a, dev, s);
   }
   if (small && a.pairs <= 16) return launch_fp8_stream(a, mode, dev, s);
   if (a.pairs <= 16) return launch_narrow<16, kFp8Dense>(a, dev, s);

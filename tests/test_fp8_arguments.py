@@ -98,11 +98,14 @@ def test_grouped_sizes(call, want, kw):
 
 def test_grouped_workspace():
     need = B.fp8_grouped_workspace_bytes
-    assert need(64, 2, 8, 256, 16) == 0                    # few pairs an expert: none
-    n = need(8192, 2, 8, 4096, 128)
+    assert need(64, 2, 16, 256, 4096, 16) == 0                    # few pairs an expert: none
+    n = need(8192, 2, 8, 4096, 128, 128)
     rows = (8192 * 2 + 8 * 127) // 128 * 128
     assert rows * 4096 < n < rows * 4096 * 1.1
-    assert need(-1, 2, 8, 256, 16) == need(4, 9, 8, 256, 16) == need(4, 2, 8, 0, 16) == need(4, 2, 8, 256, 8) == 0
+    assert need(4096, 2, 8, 256, 128, 64) > 0 and need(64, 2, 8, 256, 128, 64) == 0
+    for bad in ((-1, 2, 8, 256, 128, 16), (4096, 9, 8, 256, 128, 16), (4096, 2, 8, 0, 128, 16), (4096, 2, 8, 256, 0, 16),
+                (4096, 2, 8, 256, 128, 8)):
+        assert need(*bad) == 0
     big = dict(M=8192, cap=1 << 20, capb=1 << 16, block=128, ldx=4096, ldw=4096, K=4096)
     assert _grouped(**big) == 4 and _grouped(ws_ptr=P0, ws_bytes=n - 1, **big) == 4
     assert _grouped(ws_ptr=P0 + 8, ws_bytes=n, **big) == MISALIGNED

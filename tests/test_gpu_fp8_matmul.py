@@ -177,18 +177,19 @@ def test_grouped_larger(M, topk, E, K, N, block):
 @pytest.mark.parametrize("block", [16, 32, 64, 128])
 @pytest.mark.parametrize("M,topk,E,K,N,kind", [(400, 1, 2, 256, 300, "even"), (130, 2, 2, 130, 520, "even"),
                                                (513, 1, 1, 400, 257, "one"), (2000, 2, 8, 512, 256, "skew"),
-                                               (700, 3, 16, 272, 128, "skew"), (3000, 4, 60, 128, 96, "even")])
+                                               (700, 3, 16, 272, 128, "skew"), (3000, 4, 60, 128, 96, "even"),
+                                               (400, 2, 2, 130, 777, "even"), (90, 1, 1, 64, 6000, "one")])
 def test_grouped_many_pairs_an_expert(block, M, topk, E, K, N, kind):
     _grouped(M, topk, E, K, N, block, kind, per_pair=block > 32, weighted=block == 64, pad=block // 4)
 
 
 def test_grouped_with_a_workspace():
     g = _gen(3)
-    M, topk, E, K, N, block = 600, 2, 4, 256, 320, 64
+    M, topk, E, K, N, block = 600, 2, 4, 256, 520, 64
     x, xs = f8_rows(M, K, g)
     w, ws = f8_weight(N, K, g, E)
     ids = _route(M, topk, E, g, "even")
-    n = B.fp8_grouped_workspace_bytes(M, topk, E, K, block)
+    n = B.fp8_grouped_workspace_bytes(M, topk, E, K, N, block)
     assert n > 0
     space = torch.full((n + 64,), 0x7f, dtype=torch.uint8, device="cuda")
     y, want = (torch.empty((M, topk, N), dtype=BF, device="cuda") for _ in range(2))
