@@ -555,7 +555,7 @@ int moe_fp8_matmul(const moe_lora_fp8 *x, long long ldx, const float *x_scales, 
  *   workspace: moe_fp8_grouped_workspace_bytes(M, topk, num_experts, K, N,
  *     block_size) bytes, [device], 16-byte aligned; may be NULL when that is 0.
  *     Its contents need no initialisation and are overwritten.
- * Calls with at least 16 pairs an expert on average (and more than a round of
+ * Calls with at least 20 pairs an expert on average (and more than a round of
  * work) gather x into the order of the blocks, in the workspace, and run the
  * kernel bound by the tensor cores; others the one bound by the weight's bytes.  Sizes and limits as for
  * moe_align_block_size and moe_fp8_matmul.  An expert id out of range skips its

@@ -51,7 +51,8 @@ struct Fp8Cfg {
   int stages;      // operand ring
   int nt;          // output tiles along N
   int cluster;     // CTAs that split K (narrow)
-  int off_scale, off_red, off_ctrl;
+  int off_scale, off_red, off_list, off_ctrl;
+  int list;        // units that the list of live ones holds (0: none is made)
   int smem_bytes;
 };
 
@@ -60,6 +61,7 @@ struct Fp8Cfg {
 constexpr int kNarrowThreads = 256;
 constexpr int kMaxRing = 12;
 constexpr int kScaleSlots = 16;   // ring of scale rows, one group each
+constexpr int kListUnits = 2048;
 
 template <int BT>
 struct Narrow {
@@ -80,7 +82,35 @@ struct NarrowCtrl {
   uint64_t red_full;
   uint32_t tmem;
   int abort;
+  int live;                                  // units in the list
+  int warp_live[kNarrowThreads / 32];
 };
+
+// The units of a sorted call that hold pairs, in order: where a block is
+// several units, most of a decode batch's hold none, and every CTA would look
+// each of them up for every tile of N (256 tokens, blocks of 64: 97 us against
+// 76 in blocks of 16, which need no list).  By the whole CTA.
+template <int BT>
+__device__ __forceinline__ void list_units(const Fp8Args &p, int units, int *list, NarrowCtrl &ctl, int tid) {
+  const int lane = tid & 31, warp = tid >> 5;
+  int n = 0;   // (the same in every thread)
+  for (int base = 0; base < units; base += kNarrowThreads) {
+    const int b = base + tid;
+    const int e = b < units ? block_expert<kFp8Sorted>(p, b, BT) : kNoPairs;
+    const uint32_t live = __ballot_sync(0xFFFFFFFFu, e >= 0);
+    if (lane == 0) ctl.warp_live[warp] = __popc(live);
+    __syncthreads();
+    int at = n;
+    for (int w = 0; w < kNarrowThreads / 32; ++w) {
+      if (w < warp) at += ctl.warp_live[w];
+      n += ctl.warp_live[w];
+    }
+    if (e >= 0) list[at + __popc(live & ((1u << lane) - 1))] = b;
+    __syncthreads();
+  }
+  if (tid == 0) ctl.live = n;
+  __syncthreads();
+}
 
 // The items of a CTA, in the order of its warps' loops: all of K, or (a cluster
 // of cs > 1 CTAs, which has one item at most) this CTA's share of it.
@@ -166,7 +196,17 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   if (cs > 1) cluster_arrive_release();   // this CTA's barriers are initialised; waited for before anything is sent
   wait_for_prior_grid();
   const uint32_t tmem = ctl.tmem;
-  const int items = num_units<MODE>(p, BT) * cfg.nt;
+  const int all_units = num_units<MODE>(p, BT);
+  int units = all_units;
+  const int *list = nullptr;
+  if (MODE == kFp8Sorted && cfg.list && units <= cfg.list) {
+    int *l = reinterpret_cast<int *>(smem + cfg.off_list);
+    list_units<BT>(p, units, l, ctl, tid);
+    list = l;
+    units = ctl.live;
+  }
+  const int items = units * cfg.nt;
+  auto unit = [&](int i) { return list ? list[i] : i; };
   NarrowWork wk(items, p.KB, cs);
   bool waited = false;   // for the cluster's barriers
 
@@ -175,7 +215,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     while (wk.advance()) {
-      const int b = wk.it / cfg.nt, nt = wk.it - b * cfg.nt, e = block_expert<MODE>(p, b, BT);
+      const int ui = wk.it / cfg.nt, nt = wk.it - ui * cfg.nt, b = unit(ui), e = block_expert<MODE>(p, b, BT);
       if (e < 0) continue;
       int row[4];
       bool mine = false;   // lane i gathers rows 4i .. 4i+3; groups without a pair are left as they are
@@ -220,7 +260,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     int s = 0, a = 0;
     uint32_t ph = 0, aph = 0;
     while (wk.advance()) {
-      if (block_expert<MODE>(p, wk.it / cfg.nt, BT) < 0) continue;
+      if (block_expert<MODE>(p, unit(wk.it / cfg.nt), BT) < 0) continue;
       for (int kb = wk.kb0; kb < wk.kb1; ++kb) {
         mbar_wait(&ctl.tempty[a], aph ^ 1, abort, p.err);
         const int i = (kb - wk.kb0) & 1;
@@ -246,8 +286,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     while (wk.advance()) {
-      const int b = wk.it / cfg.nt, nt = wk.it - b * cfg.nt, e = block_expert<MODE>(p, b, BT);
-      if (nt == 0 && wk.rank == 0) flag_unit<MODE>(p, b, BT, e, lane);
+      const int ui = wk.it / cfg.nt, nt = wk.it - ui * cfg.nt, b = unit(ui), e = block_expert<MODE>(p, b, BT);
       if (e < 0) continue;
       constexpr int kPer = (BT + 31) / 32;
       const float *src[kPer];
@@ -270,6 +309,11 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         if (++s == kScaleSlots) { s = 0; ph ^= 1; }
       }
     }
+  } else if (warp == 3) {
+    // ---------------- what is out of range, each unit once
+    if (MODE != kFp8Dense)
+      for (int b = blockIdx.x; b < all_units; b += gridDim.x)
+        flag_unit<MODE>(p, b, BT, block_expert<MODE>(p, b, BT), lane);
   } else if (warp >= 4) {
     // ---------------- epilogue: this thread's weight row, BT pairs
     const int row = (warp - 4) * 32 + lane;
@@ -277,7 +321,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     int s = 0, a = 0;
     uint32_t sph = 0, aph = 0;
     while (wk.advance()) {
-      const int b = wk.it / cfg.nt, nt = wk.it - b * cfg.nt;
+      const int ui = wk.it / cfg.nt, nt = wk.it - ui * cfg.nt, b = unit(ui);
       if (block_expert<MODE>(p, b, BT) < 0) continue;
       float acc[BT];
 #pragma unroll
@@ -824,6 +868,7 @@ int launch_narrow(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) 
   const long long items = block_bound(a, (Fp8Mode)MODE, BT) * cfg.nt;
   if (items <= 0) return 0;
   if (items > INT32_MAX) return MOE_LORA_ERR_UNSUPPORTED;
+  if (MODE == kFp8Sorted && a.block > BT) cfg.list = kListUnits;
   // Clusters that split K: while there are too few items for the SMs, as large
   // as leaves each CTA two groups and every item a cluster of its own.  A ring
   // no longer than a CTA's share lets more clusters fit (of 8 CTAs with 200 KB
@@ -831,12 +876,14 @@ int launch_narrow(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) 
   // they gave: gpt-oss-shaped w2 decode 146 us against 140.)
   auto shape = [&](int cs) {
     cfg.cluster = cs;
-    const int fixed = kScaleSlots * C::kScaleRow * 4 + (cs > 1 ? C::kRedBytes : 0) + (int)sizeof(NarrowCtrl) + 128;
+    const int list_bytes = cfg.list * 4;
+    const int fixed = kScaleSlots * C::kScaleRow * 4 + (cs > 1 ? C::kRedBytes : 0) + list_bytes + (int)sizeof(NarrowCtrl) + 128;
     const int share = items * cs <= dev.sm_count ? ((a.KB + cs - 1) / cs + 1) / 2 : kMaxRing;
     cfg.stages = std::max(2, std::min(share, std::min(kMaxRing, (200 * 1024 - fixed) / C::kStage)));
     cfg.off_scale = cfg.stages * C::kStage;
     cfg.off_red = cfg.off_scale + kScaleSlots * C::kScaleRow * 4;
-    cfg.off_ctrl = cfg.off_red + (cs > 1 ? C::kRedBytes : 0);
+    cfg.off_list = cfg.off_red + (cs > 1 ? C::kRedBytes : 0);
+    cfg.off_ctrl = cfg.off_list + list_bytes;
     cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(NarrowCtrl);
     return resident_clusters(fp8_narrow_kernel<BT, MODE>, cfg, kNarrowThreads, dev);
   };
@@ -893,12 +940,12 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
 // in flight (8192 x 8192: 19 us against 16).
 constexpr double kStreamBytes = 32e6;
 
-// Sorted calls run the wide kernel from 16 pairs an expert on (on average), the
+// Sorted calls run the wide kernel from 20 pairs an expert on (on average), the
 // narrow one, in units of 16, below.  Below, a call is bound by the weight's
 // bytes, and tiles of 256 rows and the gather cost more than they give; above,
 // an expert's units read its weight again and again.  128 experts of 2048 x
 // 1536, us narrow / wide: 4 pairs an expert 66 / 86, 8 68 / 89, 16 76 / 92, 32
-// 123 / 95, 64 220 / 100; with a skewed router 4 70 / 74, 8 97 / 89, 16 113 / 96.
+// 123 / 95, 64 220 / 100; with a skewed router 4 57 / 74, 8 71 / 89, 16 89 / 96.
 // (Units of 32 and 64 were slower than of 16 wherever the narrow kernel wins:
 // 92 us at 16 pairs an expert, also over gathered rows.)
 // The narrow one also while a round of its items covers the output (16 experts
@@ -906,7 +953,7 @@ constexpr double kStreamBytes = 32e6;
 constexpr long long kRoundItems = 152;
 bool fp8_sorted_is_wide(const Fp8Args &a) {
   const long long units = a.pairs / 16 + std::min(a.E, a.pairs);
-  return a.pairs >= 16ll * a.E && units * ((a.N + kRows - 1) / kRows) > kRoundItems;
+  return a.pairs >= 20ll * a.E && units * ((a.N + kRows - 1) / kRows) > kRoundItems;
 }
 
 size_t fp8_sorted_workspace(const Fp8Args &a) {
