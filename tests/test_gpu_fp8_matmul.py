@@ -53,7 +53,7 @@ def test_dense_strided(M, N, K, pad, ypad):
 
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 7168), (1, 64, 16384), (16, 128, 8192), (2048, 1100, 640),
                                    (8192, 128, 256), (300, 20000, 128), (6000, 300, 1), (1500, 2049, 500), (20000, 1, 300),
-                                   (3, 9000, 9000), (16, 5000, 8192)])
+                                   (3, 9000, 9000), (16, 5000, 8192), (16, 512, 65600), (9, 700, 49152), (70, 128, 16384)])
 def test_dense_long(M, N, K):
     _dense(M, N, K)
 
@@ -172,6 +172,14 @@ def test_grouped_strided(block, pad, ypad):
                                                 (700, 4, 16, 768, 1024, 64), (64, 4, 32, 2880, 2880, 32)])
 def test_grouped_larger(M, topk, E, K, N, block):
     _grouped(M, topk, E, K, N, block, "skew", seed=1)
+
+
+@pytest.mark.parametrize("block", [0, 16, 128])
+@pytest.mark.parametrize("M,topk,E,K,N,kind", [(5, 1, 1, 8192, 100, "one"), (3, 2, 3, 8200, 400, "even"),
+                                               (1, 1, 2, 8192, 4100, "even"), (2, 2, 4, 16384, 1030, "one")])
+def test_grouped_few_items_of_a_long_k(block, M, topk, E, K, N, kind):
+    """Clusters of 2, 4 and 8 CTAs that split K, with empty units beside the live ones."""
+    _grouped(M, topk, E, K, N, block, kind, weighted=True)
 
 
 @pytest.mark.parametrize("block", [16, 32, 64, 128])
