@@ -7,6 +7,7 @@ installed, fastcall.so: the 8-bit operators' calls from Python without ctypes
 Usage: python -m lora_moe_gb300.build
 """
 import concurrent.futures
+import fcntl
 import os
 import shutil
 import subprocess
@@ -64,10 +65,24 @@ def _build_fastcall():
 
 
 def build(force=False, verbose=False, ptxas_info=False):
-    if not force and not ptxas_info and os.path.exists(LIB) and os.path.getmtime(LIB) >= _inputs_mtime():
+    always = force or ptxas_info
+    if not always and _is_current():
         return LIB
-    nvcc = _nvcc()
     os.makedirs(OUT_DIR, exist_ok=True)
+    # One process at a time: the object files are shared. One that waited finds the other's result.
+    with open(os.path.join(OUT_DIR, "lock"), "w") as lock:
+        fcntl.flock(lock, fcntl.LOCK_EX)
+        if always or not _is_current():
+            _build(verbose, ptxas_info)
+    return LIB
+
+
+def _is_current():
+    return os.path.exists(LIB) and os.path.getmtime(LIB) >= _inputs_mtime()
+
+
+def _build(verbose, ptxas_info):
+    nvcc = _nvcc()
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
                      "-Xcompiler", "-Wall", "--expt-relaxed-constexpr"]
     if ptxas_info:
@@ -95,7 +110,6 @@ def build(force=False, verbose=False, ptxas_info=False):
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (res.stdout, res.stderr))
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
