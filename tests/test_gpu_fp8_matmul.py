@@ -351,6 +351,21 @@ def test_grouped_in_a_cuda_graph():
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("M,N,ld", [(12, 200, 1 << 29), (40, 200, 1 << 27), (5200, 260, 1 << 20)])
+def test_dense_offsets_past_32_bits(M, N, ld):
+    """Rows of x and y far apart, the last past 2^32 bytes, on each kernel."""
+    g = _gen(M)
+    K = 272
+    w, ws = f8_weight(N, K, g)
+    small, xs = f8_rows(M, K, g)
+    x = torch.empty(M * ld, dtype=torch.uint8, device="cuda").view(F8).view(M, ld)[:, :K]
+    x.copy_(small)
+    y = torch.empty(M * ld, dtype=BF, device="cuda").view(M, ld)[:, :N]
+    B.moe_fp8_matmul(x, xs, w, ws, y)
+    ref, bound = product64(small, xs, w, ws)
+    assert_bf16_close(y, ref, bound)
+
+
 def test_grouped_offsets_past_32_bits():
     """A weight of more than 2^32 elements and rows of x and y past 2^31 elements: the last expert and the last rows."""
     g = _gen(8)

@@ -204,3 +204,20 @@ def test_rows_on_another_stream_and_twice_the_same():
         outs.append((q.view(torch.uint8), s, n.view(torch.uint8), r))
     for a, b in zip(*outs):
         assert torch.equal(a, b)
+
+
+def test_rows_offsets_past_32_bits():
+    """Rows 2^30 elements apart: the last one starts past 2^32."""
+    M, H, ld = 6, 400, 1 << 30
+    g = _gen(4)
+    x = torch.empty(M * ld, dtype=BF, device="cuda").view(M, ld)[:, :2 * H]
+    q8 = torch.empty(M * ld, dtype=torch.uint8, device="cuda").view(F8).view(M, ld)
+    x.copy_(torch.randn((M, 2 * H), generator=g, device="cuda"))
+    q, scales = q8[:, :H], torch.empty((M, groups(H)), device="cuda")
+    weight = torch.ones(H, dtype=BF, device="cuda")
+    B.moe_add_rms_norm_fp8(x[:, :H], weight, q, scales)
+    _check_norm(x[:, :H], None, weight, 1e-6, None, None, q, scales)
+    B.moe_silu_mul_fp8(x, q, scales)
+    v = x[:, :H].double()
+    v = v / (1 + torch.exp(-v)) * x[:, H:].double()
+    assert_f8_close(q, scales, v, quantize64(v), ACT_REL)
