@@ -483,7 +483,10 @@ typedef uint8_t moe_lora_fp8;
  *   scales[m][g] = max(max |n| over group g / 448, 2^-126)
  *   q[m][c] = e4m3(n[c] / scales[m][g])
  * The norm and the 8 bits come from the fp32 h and n, not from their bf16
- * roundings.  A NaN in a row makes that row's n, scales and q NaN.
+ * roundings.  Both quotients are products with a reciprocal, 1 / 448 or
+ * 1 / scales[m][g], each within 2^-23 of the quotient: where n / scale lies that
+ * close to half way between two 8-bit values, q may be either of them.  A NaN in
+ * a row makes that row's n, scales and q NaN.
  *
  *   x            [device] bf16, part p of row m at x + m*ldx + p*ld_part;
  *                parts = 1 is the plain residual addition, parts = topk sums a
@@ -508,7 +511,9 @@ int moe_add_rms_norm_fp8(const moe_lora_bf16 *x, long long ldx, long long ld_par
  * moe_silu_mul_fp8 -- the gated activation with an 8-bit output:
  *   a = x[r][c] / (1 + exp(-x[r][c])) * x[r][I + c]     (fp32, c < I)
  *   act[r][c] = bf16(a)
- * and scales and q of the fp32 a as above.  The gate is in columns [0, I) of a
+ * and scales and q of the fp32 a as above.  The exponential and the quotient are
+ * the fast ones: a is within 2^-16 of its value for gates down to -87, below
+ * which exp(-|gate|) loses bits and a tends to zero.  The gate is in columns [0, I) of a
  * row of x, the up projection in [I, 2I), as two slices of one w13 product.
  * act is what w2's adapters read.
  *   x  [device] bf16 [rows, ldx], ldx >= 2*I
