@@ -101,6 +101,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
   }
 }
 
+// Bounded wait used before a CTA exits: ignores the abort flag.
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
+  const unsigned long long t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > kWaitTimeoutNs) return;
+}
+// The same for a ring of which `uses` uses of consecutive slots were begun:
+// waits until each slot's last use has completed its phase (the n-th use of a
+// slot completes phase n).  What completes phases asynchronously (copies,
+// commits) writes to this CTA's shared memory, so the CTA must not exit before.
+__device__ __forceinline__ void drain_ring(uint64_t *bars, uint32_t slots, uint32_t uses) {
+  const unsigned long long t0 = global_timer_ns();
+  for (uint32_t s = 0; s < slots && s < uses; ++s)
+    while (!mbar_try_wait(&bars[s], ((uses - 1 - s) / slots) & 1))
+      if (global_timer_ns() - t0 > kWaitTimeoutNs) return;
+}
+
 // mbar_wait in few registers, for loops that hold most of them: the clock in 32
 // bits of nanoseconds (which kWaitTimeoutNs fits).
 static_assert(kWaitTimeoutNs < 0xFFFFFFFFull - kSuspendHintNs, "a 32-bit clock must show the limit");
@@ -401,6 +418,7 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Make this thread's generic-proxy shared-memory writes visible to the async
 // proxy (bulk copies, TMA, tcgen05.mma operand reads).

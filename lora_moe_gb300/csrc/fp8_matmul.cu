@@ -80,6 +80,7 @@ struct NarrowCtrl {
   uint64_t sfull[kScaleSlots], sempty[kScaleSlots];
   uint64_t tfull[4], tempty[4];
   uint64_t red_full;
+  uint64_t done;                             // every MMA of this CTA
   uint32_t tmem;
   int abort;
   int live;                                  // units in the list
@@ -181,6 +182,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       mbar_init(&ctl.tempty[s], 4);
     }
     mbar_init(&ctl.red_full, 1);
+    mbar_init(&ctl.done, 1);
     ctl.abort = 0;
     fence_barrier_init();
     prefetch_tensor_map(&maps.w);
@@ -213,8 +215,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   if (warp == 0) {
     // ---------------- operands: the weight's tile, and the pairs' rows
     int s = 0;
-    uint32_t ph = 0;
-    while (wk.advance()) {
+    uint32_t ph = 0, fills = 0;
+    bool go = true;   // falls with a wait that gave up: nothing more is requested
+    while (go && wk.advance()) {
       const int ui = wk.it / cfg.nt, nt = wk.it - ui * cfg.nt, b = unit(ui), e = block_expert<MODE>(p, b, BT);
       if (e < 0) continue;
       int row[4];
@@ -234,7 +237,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       }
       const int groups = MODE == kFp8Dense ? BT / 4 : __popc(__ballot_sync(0xFFFFFFFFu, mine));
       for (int kb = wk.kb0; kb < wk.kb1; kb += 2) {
-        mbar_wait(&ctl.empty[s], ph ^ 1, abort, p.err);
+        go = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.empty[s], ph ^ 1, abort, p.err));
+        if (!go) break;
+        ++fills;
         uint8_t *st = smem + (size_t)s * C::kStage;
         const int n = min(2, wk.kb1 - kb);
         if (elect_one()) {
@@ -253,6 +258,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         if (++s == cfg.stages) { s = 0; ph ^= 1; }
       }
     }
+    // the copies have landed, the stages' hand-backs arrived and the MMAs completed before this CTA exits
+    __syncwarp();
+    if (lane == 0) {
+      drain_ring(ctl.full, cfg.stages, fills);
+      drain_ring(ctl.empty, cfg.stages, fills);
+      drain_wait(&ctl.done, 0);
+    }
+    __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA: each group of 128 columns into an accumulator of its own
     constexpr uint32_t idesc = make_idesc_e4m3(kRows, BT);
@@ -279,6 +292,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         if (++a == C::kBufs) { a = 0; aph ^= 1; }
       }
     }
+    if (elect_one()) tc_commit(&ctl.done);
+    __syncwarp();
   } else if (warp == 2) {
     // ---------------- scales: a row of BT + 1 for each group
     // (clusters have an item each for all blocks that an align writes)
@@ -309,6 +324,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         if (++s == kScaleSlots) { s = 0; ph ^= 1; }
       }
     }
+    cp_async_wait_all();
   } else if (warp == 3) {
     // ---------------- what is out of range, each unit once
     if (MODE != kFp8Dense)
@@ -550,6 +566,7 @@ constexpr int kWideRegsIssue = 56, kWideRegsEpilogue = 216;
 struct WideCtrl {
   uint64_t full[kWideStages], empty[kWideStages];
   uint64_t tfull[4], tempty[4];
+  uint64_t done;   // every MMA of the pair
   uint32_t tmem;
   int abort;
 };
@@ -576,6 +593,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mbar_init(&ctl.tfull[s], 1);
       mbar_init(&ctl.tempty[s], 8);   // four epilogue warps of each CTA
     }
+    mbar_init(&ctl.done, 2);          // a commit of each MMA warp
     ctl.abort = 0;
     fence_barrier_init();
     prefetch_tensor_map(&maps.w);
@@ -604,14 +622,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // ---------------- operands: this CTA's rows, and its 64 of each 128 columns
       const uint32_t full0 = cluster_map(smem_addr(&ctl.full[0]), 0);   // rank 0's
       int s = 0;
-      uint32_t ph = 0;
-      for (int it = first; it < items; it += step) {
+      uint32_t ph = 0, fills = 0;
+      bool go = true;   // falls with a wait that gave up: nothing more is requested
+      for (int it = first; go && it < items; it += step) {
         const int nt = it / ntiles;
         const WideTile t = tile(it - nt * ntiles);
         const bool have = t.rows > rank * kRows;
         const uint32_t bytes = 2 * kTileBytes + (t.rows > kRows ? 2 : 1) * kTileBytes;
         for (int kb = 0; kb < p.KB; ++kb) {
-          mbar_wait(&ctl.empty[s], ph ^ 1, abort, p.err);
+          go = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.empty[s], ph ^ 1, abort, p.err));
+          if (!go) break;
+          ++fills;
           uint8_t *st = smem + (size_t)s * kWideStage;
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
@@ -624,6 +645,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           __syncwarp();
           if (++s == kWideStages) { s = 0; ph ^= 1; }
         }
+      }
+      // The pair's copies have landed (rank 0's barriers count both CTAs'), the
+      // hand-backs of the last stages have arrived here and the MMAs have
+      // completed before the pair exits: the epilogue waits for neither.
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) drain_ring(ctl.full, kWideStages, fills);
+        drain_ring(ctl.empty, kWideStages, fills);
+        drain_wait(&ctl.done, 0);
       }
     } else if (warp <= 2 && rank == 0) {
       // ---------------- MMA, for both CTAs: a warp for each half of the
@@ -653,6 +683,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (a == 0) aph ^= 1;
         }
       }
+      if (elect_one()) tc_commit_pair(&ctl.done);
     }
     __syncwarp();
   } else {
@@ -765,7 +796,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_arrive_release();   // the pair's accumulators are read, and no barrier of the peer is used any more
+  // The pair's accumulators are read, and nothing is on its way to either CTA's shared memory: copies and commits were
+  // waited for above, and the release orders the epilogue's remote arrivals.
+  cluster_arrive_release();
   cluster_wait();
   if (warp == 1) {
     tc_fence_after();

@@ -119,13 +119,6 @@ struct CsMeta {
   int abort;
 };
 
-// Bounded wait used when draining: ignores the abort flag.
-__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
-  const unsigned long long t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity))
-    if (global_timer_ns() - t0 > kWaitTimeoutNs) return;
-}
-
 // Row sums over a group of G consecutive lanes (G a power of two up to 32),
 // each lane holding partial sums of the same V rows.  While a lane holds more
 // than one row, a step with lane distance d hands half of its rows to the
