@@ -137,6 +137,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_commit(&meta.shrink_done);
       }
+      // copies have landed and the last hand-backs arrived before the CTA exits (the epilogue waits for neither)
+      drain_ring(meta.full_sh, cfg.s_sh, sh_iter);
+      drain_ring(meta.empty_sh, cfg.s_sh, sh_iter);
     }
     __syncwarp();
   } else if (warp == 0) {
@@ -172,6 +175,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_commit(&meta.t_empty[tb]);
       }
+      drain_ring(meta.full_ex, cfg.s_ex, ex_iter);
+      drain_ring(meta.empty_ex, cfg.s_ex, ex_iter);
+      drain_ring(meta.t_empty, cfg.t_bufs, kk);
     }
     __syncwarp();
   } else {
