@@ -543,11 +543,7 @@ __global__ void __launch_bounds__(kClusterAlignThreads, 1) align_cluster_kernel(
 }
 
 int set_smem_limit(const void *fn, size_t bytes) {
-  if (bytes <= 48 * 1024) return 0;
-  return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
-                 cudaSuccess
-             ? 0
-             : MOE_LORA_ERR_LAUNCH;
+  return bytes <= 48 * 1024 ? 0 : allow_dynamic_smem(fn);   // (48 KB need no permission)
 }
 
 }  // namespace
@@ -602,9 +598,7 @@ bool align_cluster_fits(int E) {
 int launch_align_cluster(const AlignArgs &a, cudaStream_t stream) {
   const int CA = align_cluster_size(a.M, a.topk);
   const size_t bytes = ((size_t)kClusterAlignWarps * a.num_experts + 4 * (size_t)a.num_experts + 1 + 32) * sizeof(int);
-  if (cudaFuncSetAttribute((const void *)align_cluster_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)bytes) != cudaSuccess)
-    return MOE_LORA_ERR_LAUNCH;
+  if (int st = allow_dynamic_smem((const void *)align_cluster_kernel)) return st;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(a.num_active_loras * CA), 1, 1);
   lc.blockDim = dim3(kClusterAlignThreads, 1, 1);

@@ -35,6 +35,15 @@ int current_device_info(DeviceInfo *out) {
   return 0;
 }
 
+int allow_dynamic_smem(const void *kernel) {
+  DeviceInfo dev;
+  if (int st = current_device_info(&dev)) return st;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dev.max_smem_optin) ==
+                 cudaSuccess
+             ? 0
+             : MOE_LORA_ERR_LAUNCH;
+}
+
 }  // namespace moe_lora
 
 using namespace moe_lora;

@@ -826,10 +826,8 @@ bool register_shares_fit(Kernel kernel) {
 template <typename... Params, typename... Args>
 int launch(void (*kernel)(Params...), const Fp8Cfg &cfg, unsigned grid, int threads, cudaStream_t stream,
            const Args &...args) {
-  if (cfg.smem_bytes > 0 &&
-      cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.smem_bytes) !=
-          cudaSuccess)
-    return MOE_LORA_ERR_LAUNCH;
+  if (cfg.smem_bytes > 0)
+    if (int st = allow_dynamic_smem((const void *)kernel)) return st;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(grid, 1, 1);
   lc.blockDim = dim3(threads, 1, 1);
@@ -864,7 +862,7 @@ int resident_clusters(Kernel kernel, const Fp8Cfg &cfg, int threads, const Devic
   for (int i = 0; i < n; ++i)
     if (known[i].kernel == (const void *)kernel && known[i].device == dev.device && known[i].cluster == cfg.cluster && known[i].smem == cfg.smem_bytes)
       return known[i].clusters;
-  cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.smem_bytes);
+  if (allow_dynamic_smem((const void *)kernel)) return std::max(1, dev.sm_count / cfg.cluster / 2);
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)cfg.cluster, 1, 1);
   lc.blockDim = dim3(threads, 1, 1);

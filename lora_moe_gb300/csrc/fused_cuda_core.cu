@@ -547,8 +547,7 @@ int pick_cfg(const FusedArgs &f, const DeviceInfo &dev, int pg, bool per_block, 
 template <int RV, bool NAIVE, int NPG>
 int launch_one(const FusedArgs &f, const CcCfg &cfg, unsigned gy, unsigned gz, cudaStream_t stream) {
   const void *fn = (const void *)fused_cuda_core_kernel<RV, NAIVE, NPG>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.smem_bytes) != cudaSuccess)
-    return MOE_LORA_ERR_LAUNCH;
+  if (int st = allow_dynamic_smem(fn)) return st;
   if (cfg.C > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     return MOE_LORA_ERR_LAUNCH;
   cudaLaunchConfig_t lc = {};
@@ -596,7 +595,7 @@ int resident_clusters_of(const CcCfg &cfg, const DeviceInfo &dev) {
       return cache[i].clusters;
   const void *fn = (const void *)fused_cuda_core_kernel<RV, NAIVE, NPG>;
   int clusters = 0;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.smem_bytes) == cudaSuccess &&
+  if (allow_dynamic_smem(fn) == 0 &&
       (cfg.C <= 8 || cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess)) {
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(cfg.C, 1, 1);

@@ -882,7 +882,7 @@ int resident_clusters(const CsCfg &cfg, const DeviceInfo &dev) {
       return cache[i].clusters;
   const void *fn = (const void *)fused_cluster_stream_kernel<NAIVE, LG_VR, NPG>;
   int clusters = 0;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.smem_bytes) == cudaSuccess) {
+  if (allow_dynamic_smem(fn) == 0) {
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(cfg.C, 1, 1);
     lc.blockDim = dim3(kThreads, 1, 1);
@@ -949,8 +949,7 @@ int launch_with(const FusedArgs &f, const CsCfg &cfg, long long G, cudaStream_t 
       return st;
   }
   const void *fn = (const void *)fused_cluster_stream_kernel<NAIVE, LG_VR, NPG>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.smem_bytes) != cudaSuccess)
-    return MOE_LORA_ERR_LAUNCH;
+  if (int st = allow_dynamic_smem(fn)) return st;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(G * cfg.C), 1, 1);
   lc.blockDim = dim3(kThreads, 1, 1);

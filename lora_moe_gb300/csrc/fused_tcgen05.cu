@@ -346,8 +346,7 @@ template <int BS>
 int launch_bs(const FusedArgs &f, const stream::Cfg &cfg, const stream::TmapSet &maps, int G,
               cudaStream_t stream) {
   const void *fn = (const void *)fused_tcgen05_kernel<BS>;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, cfg.smem_bytes) != cudaSuccess)
-    return MOE_LORA_ERR_LAUNCH;
+  if (int st = allow_dynamic_smem(fn)) return st;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(G, 1, 1);
   lc.blockDim = dim3(kThreads, 1, 1);

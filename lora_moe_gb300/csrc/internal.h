@@ -121,6 +121,12 @@ struct DeviceInfo {
   size_t max_smem_optin;
 };
 int current_device_info(DeviceInfo *out);
+// Lets `kernel` (which has no static shared memory) be launched with any dynamic
+// shared memory that the current device gives a block.  The limit belongs to the
+// function, not to a launch, so it is the same for every call: one of the call's
+// own size would be lowered by another host thread before the launch.  Set each
+// time, as a new context starts without it.
+int allow_dynamic_smem(const void *kernel);
 
 // The launch plan of a fused call (host arithmetic only).
 struct FusedPlan {
