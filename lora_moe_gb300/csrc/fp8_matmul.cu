@@ -826,8 +826,6 @@ bool register_shares_fit(Kernel kernel) {
 template <typename... Params, typename... Args>
 int launch(void (*kernel)(Params...), const Fp8Cfg &cfg, unsigned grid, int threads, cudaStream_t stream,
            const Args &...args) {
-  if (cfg.smem_bytes > 0)
-    if (int st = allow_dynamic_smem((const void *)kernel)) return st;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(grid, 1, 1);
   lc.blockDim = dim3(threads, 1, 1);
@@ -862,7 +860,6 @@ int resident_clusters(Kernel kernel, const Fp8Cfg &cfg, int threads, const Devic
   for (int i = 0; i < n; ++i)
     if (known[i].kernel == (const void *)kernel && known[i].device == dev.device && known[i].cluster == cfg.cluster && known[i].smem == cfg.smem_bytes)
       return known[i].clusters;
-  if (allow_dynamic_smem((const void *)kernel)) return std::max(1, dev.sm_count / cfg.cluster / 2);
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)cfg.cluster, 1, 1);
   lc.blockDim = dim3(threads, 1, 1);
@@ -899,6 +896,7 @@ int launch_narrow(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) 
   const long long items = block_bound(a, (Fp8Mode)MODE, BT) * cfg.nt;
   if (items <= 0) return 0;
   if (items > INT32_MAX) return MOE_LORA_ERR_UNSUPPORTED;
+  if (int st = allow_dynamic_smem((const void *)fp8_narrow_kernel<BT, MODE>)) return st;
   if (MODE == kFp8Sorted && a.block > BT) cfg.list = kListUnits;
   // Clusters that split K: while there are too few items for the SMs, as large
   // as leaves each CTA two groups and every item a cluster of its own.  A ring
@@ -942,6 +940,7 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
   cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(WideCtrl);
   static const bool fits = register_shares_fit(fp8_wide_kernel<MODE>);
   if (!fits) return MOE_LORA_ERR_LAUNCH;
+  if (int st = allow_dynamic_smem((const void *)fp8_wide_kernel<MODE>)) return st;
   Fp8Maps maps;
   WideArgs g = {};
   if (MODE == kFp8Dense) {

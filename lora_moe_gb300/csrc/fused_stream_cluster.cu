@@ -940,6 +940,8 @@ int choose(const FusedArgs &f, const DeviceInfo &dev, bool naive, ResidentFn res
 
 template <bool NAIVE, int LG_VR, int NPG>
 int launch_with(const FusedArgs &f, const CsCfg &cfg, long long G, cudaStream_t stream) {
+  const void *fn = (const void *)fused_cluster_stream_kernel<NAIVE, LG_VR, NPG>;
+  if (int st = allow_dynamic_smem(fn)) return st;
   CsMaps maps;
   const uint64_t LE = (uint64_t)f.max_loras * f.num_experts;
   for (int s = 0; s < kMaxSlices; ++s) {
@@ -948,8 +950,6 @@ int launch_with(const FusedArgs &f, const CsCfg &cfg, long long G, cudaStream_t 
                                    (uint32_t)f.rank, CU_TENSOR_MAP_SWIZZLE_NONE))
       return st;
   }
-  const void *fn = (const void *)fused_cluster_stream_kernel<NAIVE, LG_VR, NPG>;
-  if (int st = allow_dynamic_smem(fn)) return st;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3((unsigned)(G * cfg.C), 1, 1);
   lc.blockDim = dim3(kThreads, 1, 1);

@@ -343,10 +343,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int BS>
-int launch_bs(const FusedArgs &f, const stream::Cfg &cfg, const stream::TmapSet &maps, int G,
-              cudaStream_t stream) {
-  const void *fn = (const void *)fused_tcgen05_kernel<BS>;
-  if (int st = allow_dynamic_smem(fn)) return st;
+int launch_bs(const FusedArgs &f, const stream::Cfg &cfg, int G, cudaStream_t stream) {
+  if (int st = allow_dynamic_smem((const void *)fused_tcgen05_kernel<BS>)) return st;
+  stream::TmapSet maps;
+  if (int st = stream::make_tensor_maps(f, cfg, &maps)) return st;
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(G, 1, 1);
   lc.blockDim = dim3(kThreads, 1, 1);
@@ -426,13 +426,11 @@ int launch_fused_tcgen05(const FusedArgs &f, cudaStream_t stream_) {
   long long G = 0;
   if (int st = configure(f, dev, &cfg, &G)) return st;
   if (G <= 0) return 0;
-  stream::TmapSet maps;
-  if (int st = stream::make_tensor_maps(f, cfg, &maps)) return st;
   switch (f.block_size) {
-    case 16: return launch_bs<16>(f, cfg, maps, (int)G, stream_);
-    case 32: return launch_bs<32>(f, cfg, maps, (int)G, stream_);
-    case 64: return launch_bs<64>(f, cfg, maps, (int)G, stream_);
-    case 128: return launch_bs<128>(f, cfg, maps, (int)G, stream_);
+    case 16: return launch_bs<16>(f, cfg, (int)G, stream_);
+    case 32: return launch_bs<32>(f, cfg, (int)G, stream_);
+    case 64: return launch_bs<64>(f, cfg, (int)G, stream_);
+    case 128: return launch_bs<128>(f, cfg, (int)G, stream_);
     default: return MOE_LORA_ERR_UNSUPPORTED;
   }
 }

@@ -125,7 +125,9 @@ int current_device_info(DeviceInfo *out);
 // shared memory that the current device gives a block.  The limit belongs to the
 // function, not to a launch, so it is the same for every call: one of the call's
 // own size would be lowered by another host thread before the launch.  Set each
-// time, as a new context starts without it.
+// time, as a new context starts without it.  Launchers call this before they
+// encode tensor maps, a driver call that needs the context which this one makes
+// current in a host thread that has made no CUDA call yet.
 int allow_dynamic_smem(const void *kernel);
 
 // The launch plan of a fused call (host arithmetic only).

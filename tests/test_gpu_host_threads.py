@@ -40,6 +40,49 @@ def _in_threads(jobs):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("which", ["dense, narrow", "dense, wide", "dense, few rows", "norm", "align", "adapters, tensor cores", "adapters, streaming"])
+def test_first_call_of_a_thread(which):
+    """A thread whose first CUDA call this is: no context is current in it yet."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    M, N, K = {"dense, narrow": (40, 300, 256), "dense, wide": (5000, 300, 256)}.get(which, (4, 300, 256))
+    x, w = (torch.randint(-2, 3, (n, K), generator=g, device="cuda").to(F8) for n in (M, N))
+    xs, ws = torch.ones((M, 2), device="cuda"), torch.ones((3, 2), device="cuda")
+    y, q = torch.zeros((M, N), dtype=BF, device="cuda"), torch.zeros((M, K), dtype=F8, device="cuda")
+    rows, gain = torch.ones((M, K), dtype=BF, device="cuda"), torch.ones(K, dtype=BF, device="cuda")
+    w_ = gen.Workload("thread", M=64, K=256, N=512, E=4, topk=2, max_loras=2, num_active_loras=2, rank=16,
+                      block_size=32, mapping="uniform", experts="uniform")
+    d = DeviceInputs(gen.make_inputs(w_))
+    align = lambda s: B.moe_lora_align(  # noqa: E731
+        d.topk_ids, d.mapping, d.lora_ids, w_.E, w_.max_loras, w_.block_size, d.buf.sorted_token_ids, d.buf.expert_ids,
+        d.buf.num_tokens_post_padded, workspace=d.buf.workspace, stream=s)
+    align(None)
+    stream = torch.cuda.current_stream()
+    torch.cuda.synchronize()
+
+    def call():
+        if which == "norm":
+            B.moe_add_rms_norm_fp8(rows, gain, q, xs, stream=stream)
+        elif which == "align":
+            align(stream)
+        elif which.startswith("adapters"):
+            B.moe_lora_fused_shrink_expand(d.x, d.a, d.b, d.y_in, d.buf.sorted_token_ids, d.buf.expert_ids,
+                                           d.buf.num_tokens_post_padded, d.lora_ids, w_.topk, w_.block_size,
+                                           path=B.PATH_TCGEN05 if "tensor" in which else B.PATH_CUDA_CORE_STREAM,
+                                           stream=stream)
+        else:
+            B.moe_fp8_matmul(x, xs, w, ws, y, stream=stream)
+    call()       # (whatever is done once a process is done in this thread)
+    torch.cuda.synchronize()
+    y.zero_()
+    torch.cuda.synchronize()
+    with concurrent.futures.ThreadPoolExecutor(1) as ex:
+        ex.submit(call).result()
+    torch.cuda.synchronize()
+    if which.startswith("dense"):
+        assert torch.equal(y, (x.double() @ w.double().t()).to(BF))
+
+
 def test_fp8_products():
     g = torch.Generator(device="cuda")
     g.manual_seed(0)
