@@ -461,6 +461,17 @@ def _raw_stream(stream, t):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _check_device(stream, *tensors):
+    """The library works on the current device, and the stream is taken from a tensor's: all of a call's tensors, and a
+    stream that the caller names, must be there."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError("a tensor on cuda:%d, with cuda:%d as the current device" % (t.get_device(), here))
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != here:
+        raise ValueError("a stream of cuda:%d, with cuda:%d as the current device" % (stream.device.index, here))
+
+
 def moe_add_rms_norm_fp8(x, weight, q, scales, residual=None, residual_out=None, normed=None, eps=1e-6, stream=None):
     """Residual addition and root-mean-square norm with an 8-bit output; see
     include/moe_lora.h.
@@ -493,9 +504,10 @@ def moe_add_rms_norm_fp8(x, weight, q, scales, residual=None, residual_out=None,
     po, ldo = (None, 0) if residual_out is None else _rows(residual_out, _BF16, "residual_out", M, H)
     pn, ldn = (None, 0) if normed is None else _rows(normed, _BF16, "normed", M, H)
     pq, ldq = _rows(q, _F8, "q", M, H)
-    _check((_lib or lib()).moe_add_rms_norm_fp8(
-        px, ldx, ld_part, parts, pr, ldr, _dense(weight, _BF16, "weight", H), eps, po, ldo, pn, ldn, pq, ldq,
-        _dense(scales, _F32, "scales", M * -(-H // FP8_GROUP)), M, H, _raw_stream(stream, q)), "moe_add_rms_norm_fp8")
+    pw, ps = _dense(weight, _BF16, "weight", H), _dense(scales, _F32, "scales", M * -(-H // FP8_GROUP))
+    _check_device(stream, x, weight, q, scales, residual, residual_out, normed)
+    _check((_lib or lib()).moe_add_rms_norm_fp8(px, ldx, ld_part, parts, pr, ldr, pw, eps, po, ldo, pn, ldn, pq, ldq, ps,
+                                                M, H, _raw_stream(stream, q)), "moe_add_rms_norm_fp8")
 
 
 def moe_silu_mul_fp8(x, q, scales, act=None, stream=None):
@@ -513,9 +525,10 @@ def moe_silu_mul_fp8(x, q, scales, act=None, stream=None):
     px, ldx = _rows(x, _BF16, "x", rows, 2 * I)
     pa, lda = (None, 0) if act is None else _rows(act, _BF16, "act", rows, I)
     pq, ldq = _rows(q, _F8, "q", rows, I)
-    _check((_lib or lib()).moe_silu_mul_fp8(px, ldx, pa, lda, pq, ldq,
-                                            _dense(scales, _F32, "scales", rows * -(-I // FP8_GROUP)), rows, I,
-                                            _raw_stream(stream, q)), "moe_silu_mul_fp8")
+    ps = _dense(scales, _F32, "scales", rows * -(-I // FP8_GROUP))
+    _check_device(stream, x, q, scales, act)
+    _check((_lib or lib()).moe_silu_mul_fp8(px, ldx, pa, lda, pq, ldq, ps, rows, I, _raw_stream(stream, q)),
+           "moe_silu_mul_fp8")
 
 
 def moe_fp8_matmul(x, x_scales, w, w_scales, y, err_flag=None, stream=None):
@@ -535,10 +548,11 @@ def moe_fp8_matmul(x, x_scales, w, w_scales, y, err_flag=None, stream=None):
     px, ldx = _rows(x, _F8, "x", M, K)
     pw, ldw = _rows(w, _F8, "w", N, K)
     py, ldy = _rows(y, _BF16, "y", M, N)
-    _check((_lib or lib()).moe_fp8_matmul(
-        px, ldx, _dense(x_scales, _F32, "x_scales", M * kb), pw, ldw,
-        _dense(w_scales, _F32, "w_scales", -(-N // FP8_GROUP) * kb), py, ldy, M, N, K,
-        _dense(err_flag, _I32, "err_flag"), _raw_stream(stream, y)), "moe_fp8_matmul")
+    pxs, pws = _dense(x_scales, _F32, "x_scales", M * kb), _dense(w_scales, _F32, "w_scales", -(-N // FP8_GROUP) * kb)
+    perr = _dense(err_flag, _I32, "err_flag")
+    _check_device(stream, x, x_scales, w, w_scales, y, err_flag)
+    _check((_lib or lib()).moe_fp8_matmul(px, ldx, pxs, pw, ldw, pws, py, ldy, M, N, K, perr, _raw_stream(stream, y)),
+           "moe_fp8_matmul")
 
 
 def _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair):
@@ -577,6 +591,12 @@ def moe_fp8_grouped_matmul(x, x_scales, w, w_scales, y, sorted_token_ids, expert
         if st is not None:
             return _check(st, "moe_fp8_grouped_matmul")
     M, topk, E, K, N, operands = _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair)
+    blocks = [_dense(t, _I32, name) for t, name in (
+        (sorted_token_ids, "sorted_token_ids"), (expert_ids, "expert_ids"),
+        (num_tokens_post_padded, "num_tokens_post_padded"))]
+    perr = _dense(err_flag, _I32, "err_flag")
+    _check_device(stream, x, x_scales, w, w_scales, y, topk_weights, sorted_token_ids, expert_ids,
+                  num_tokens_post_padded, workspace, err_flag)
     L = _lib or lib()
     raw = _raw_stream(stream, y)
     nbytes = 0
@@ -592,11 +612,9 @@ def moe_fp8_grouped_matmul(x, x_scales, w, w_scales, y, sorted_token_ids, expert
     else:
         nbytes = workspace.numel() * workspace.element_size()
     _check(L.moe_fp8_grouped_matmul(
-        *operands, _dense(sorted_token_ids, _I32, "sorted_token_ids"), _dense(expert_ids, _I32, "expert_ids"),
-        _dense(num_tokens_post_padded, _I32, "num_tokens_post_padded"), M, topk, E, K, N, block_size,
-        sorted_token_ids.numel(), expert_ids.numel(),
-        None if workspace is None else _dense(workspace, workspace.dtype, "workspace"), nbytes,
-        _dense(err_flag, _I32, "err_flag"), raw), "moe_fp8_grouped_matmul")
+        *operands, *blocks, M, topk, E, K, N, block_size, sorted_token_ids.numel(), expert_ids.numel(),
+        None if workspace is None else _dense(workspace, workspace.dtype, "workspace"), nbytes, perr, raw),
+        "moe_fp8_grouped_matmul")
 
 
 def moe_fp8_grouped_matmul_naive(x, x_scales, w, w_scales, y, topk_ids, topk_weights=None, x_per_pair=False,
@@ -608,9 +626,10 @@ def moe_fp8_grouped_matmul_naive(x, x_scales, w, w_scales, y, topk_ids, topk_wei
         if st is not None:
             return _check(st, "moe_fp8_grouped_matmul_naive")
     M, topk, E, K, N, operands = _grouped_operands(x, x_scales, w, w_scales, y, topk_weights, x_per_pair)
-    _check((_lib or lib()).moe_fp8_grouped_matmul_naive(
-        *operands, _dense(topk_ids, _I32, "topk_ids", M * topk), M, topk, E, K, N,
-        _dense(err_flag, _I32, "err_flag"), _raw_stream(stream, y)), "moe_fp8_grouped_matmul_naive")
+    pids, perr = _dense(topk_ids, _I32, "topk_ids", M * topk), _dense(err_flag, _I32, "err_flag")
+    _check_device(stream, x, x_scales, w, w_scales, y, topk_weights, topk_ids, err_flag)
+    _check((_lib or lib()).moe_fp8_grouped_matmul_naive(*operands, pids, M, topk, E, K, N, perr, _raw_stream(stream, y)),
+           "moe_fp8_grouped_matmul_naive")
 
 
 class AlignBuffers:
