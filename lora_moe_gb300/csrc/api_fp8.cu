@@ -50,6 +50,7 @@ int grouped(Fp8Args a, Fp8Mode mode, int M, void *workspace, size_t workspace_by
     if (!ids[i] && (i == 3) == (mode == kFp8Naive)) return MOE_LORA_ERR_INVALID_ARG;
     if (!on(ids[i], 4)) return MOE_LORA_ERR_MISALIGNED;
   }
+  if (!fp8_items_fit(a, mode)) return MOE_LORA_ERR_UNSUPPORTED;
   if (mode == kFp8Sorted) {
     const size_t need = fp8_sorted_workspace(a);
     if (need && (!workspace || workspace_bytes < need)) return MOE_LORA_ERR_WORKSPACE;
@@ -152,6 +153,7 @@ int moe_fp8_matmul(const moe_lora_fp8 *x, long long ldx, const float *x_scales, 
   if (empty) return MOE_LORA_OK;
   a.KB = fp8_groups(K);
   a.NB = fp8_groups(N);
+  if (!fp8_items_fit(a, kFp8Dense)) return MOE_LORA_ERR_UNSUPPORTED;
   DeviceInfo dev;
   if (int st = current_device_info(&dev)) return st;
   return launch_fp8_matmul(a, kFp8Dense, nullptr, dev, static_cast<cudaStream_t>(stream));

@@ -65,6 +65,9 @@ int launch_fp8_stream(const Fp8Args &a, Fp8Mode mode, const DeviceInfo &dev, cud
 // Sorted calls with many pairs an expert gather x into the workspace (the
 // bytes it needs; 0: none).
 size_t fp8_sorted_workspace(const Fp8Args &a);
+// Whether the kernels' work items of a call can be counted in an int; asked
+// before anything is enqueued.
+bool fp8_items_fit(const Fp8Args &a, Fp8Mode mode);
 int launch_fp8_matmul(const Fp8Args &a, Fp8Mode mode, void *workspace, const DeviceInfo &dev, cudaStream_t stream);
 
 }  // namespace moe_lora

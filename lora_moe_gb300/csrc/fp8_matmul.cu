@@ -888,6 +888,11 @@ long long block_bound(const Fp8Args &a, Fp8Mode mode, int bt) {
   return std::min<long long>(a.max_blocks, fused_block_bound(a.pairs, 1, a.E, 1, a.block)) * (a.block / bt);
 }
 
+// Upper bound of the wide kernel's tiles of rows.
+long long tile_bound(const Fp8Args &a, bool sorted) {
+  return sorted ? a.pairs / kTileRows + std::min(a.E, a.pairs) : ((long long)a.pairs + kTileRows - 1) / kTileRows;
+}
+
 template <int BT, int MODE>
 int launch_narrow(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) {
   using C = Narrow<BT>;
@@ -895,7 +900,6 @@ int launch_narrow(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) 
   cfg.nt = (a.N + kRows - 1) / kRows;
   const long long items = block_bound(a, (Fp8Mode)MODE, BT) * cfg.nt;
   if (items <= 0) return 0;
-  if (items > INT32_MAX) return MOE_LORA_ERR_UNSUPPORTED;
   if (int st = allow_dynamic_smem((const void *)fp8_narrow_kernel<BT, MODE>)) return st;
   if (MODE == kFp8Sorted && a.block > BT) cfg.list = kListUnits;
   // Clusters that split K: while there are too few items for the SMs, as large
@@ -931,8 +935,7 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
   Fp8Cfg cfg = {};
   cfg.nt = (a.N + kWideN - 1) / kWideN;
   const long long rows = (long long)a.max_blocks * a.block;
-  const long long tiles = MODE == kFp8Dense ? ((long long)a.pairs + kTileRows - 1) / kTileRows
-                                            : a.pairs / kTileRows + std::min(a.E, a.pairs);
+  const long long tiles = tile_bound(a, MODE == kFp8Sorted);
   if (tiles <= 0) return 0;
   cfg.cluster = 2;
   cfg.stages = kWideStages;
@@ -957,7 +960,6 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
       return st;
   }
   const long long items = tiles * cfg.nt;   // (the sorted arrays' own tiles are no more, but for entries that no align writes)
-  if (items > INT32_MAX / 16) return MOE_LORA_ERR_UNSUPPORTED;
   const unsigned grid = 2 * (unsigned)std::min<long long>(items, dev.sm_count / 2);
   return launch(fp8_wide_kernel<MODE>, cfg, grid, kWideThreads, stream, maps, a, g, cfg);
 }
@@ -988,6 +990,14 @@ bool fp8_sorted_is_wide(const Fp8Args &a) {
 
 size_t fp8_sorted_workspace(const Fp8Args &a) {
   return fp8_sorted_is_wide(a) ? wide_space((long long)a.max_blocks * a.block, a.K).bytes : 0;
+}
+
+bool fp8_items_fit(const Fp8Args &a, Fp8Mode mode) {
+  if (mode == kFp8Dense ? a.pairs > 64 : mode == kFp8Sorted && fp8_sorted_is_wide(a))
+    return tile_bound(a, mode == kFp8Sorted) * ((a.N + kWideN - 1) / kWideN) <= INT32_MAX / 16;
+  // every unit that the sorted arrays can hold, whatever they hold
+  const long long units = mode == kFp8Sorted ? (long long)a.max_blocks * (a.block / 16) : block_bound(a, mode, 16);
+  return units * ((a.N + kRows - 1) / kRows) <= INT32_MAX;
 }
 
 int launch_fp8_matmul(const Fp8Args &a, Fp8Mode mode, void *workspace, const DeviceInfo &dev, cudaStream_t s) {
