@@ -12,6 +12,7 @@ import ctypes
 import importlib.util
 import os
 import threading
+import warnings
 
 import torch
 
@@ -23,7 +24,7 @@ PATH_AUTO, PATH_CUDA_CORE, PATH_TCGEN05, PATH_CUDA_CORE_CLUSTER, PATH_CUDA_CORE_
 DEVERR_EXPERT_ID, DEVERR_LORA_ID, DEVERR_CAPACITY, DEVERR_PAIR_ID, DEVERR_TIMEOUT = 1, 2, 4, 8, 16
 
 _lib = None
-_fast = None     # fastcall.so's functions, or a stand-in
+_fast = None     # fastcall's functions, or a stand-in
 _lock = threading.Lock()
 
 
@@ -366,7 +367,7 @@ def moe_lora_test_withheld_copy(x, lora_a, lora_b, y, topk_ids, token_lora_mappi
 
 
 class _NoFast:
-    """Stands in for fastcall.so where it was not built: every call goes through ctypes."""
+    """Stands in for fastcall where it was not built or does not load: every call goes through ctypes."""
 
     @staticmethod
     def norm(*args):
@@ -376,17 +377,23 @@ class _NoFast:
 
 
 def _load_fast():
-    """fastcall.so's functions: they take the common case of the 8-bit
+    """fastcall's functions (a compiled module): they take the common case of the 8-bit
     operators' calls (ordinary tensors on the current device, its current
     stream) and return None for any other, which the functions below treat."""
     global _fast
     L = lib()
     with _lock:
         if _fast is None:
+            fast = None
             if os.path.exists(_build.FASTCALL):
-                spec = importlib.util.spec_from_file_location("fastcall", _build.FASTCALL)
-                fast = importlib.util.module_from_spec(spec)
-                spec.loader.exec_module(fast)
+                try:
+                    spec = importlib.util.spec_from_file_location("fastcall", _build.FASTCALL)
+                    fast = importlib.util.module_from_spec(spec)
+                    spec.loader.exec_module(fast)
+                except ImportError as e:
+                    warnings.warn("the 8-bit operators' calls go through ctypes: %s" % e)
+                    fast = None
+            if fast is not None:
                 fast.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
                     L.moe_add_rms_norm_fp8, L.moe_silu_mul_fp8, L.moe_fp8_matmul, L.moe_fp8_grouped_matmul,
                     L.moe_fp8_grouped_matmul_naive, L.moe_fp8_grouped_workspace_bytes)])

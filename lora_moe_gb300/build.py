@@ -1,18 +1,22 @@
 """Build libmoe_lora.so (the CUDA library) in-tree with nvcc for sm_103a.
 
 Translation units are compiled in parallel, then linked into
-lora_moe_gb300/_build/libmoe_lora.so.  Beside it, where Python's headers are
-installed, fastcall.so: the 8-bit operators' calls from Python without ctypes
-(a C++ extension against torch's headers; without it they go through ctypes).
+lora_moe_gb300/_build/libmoe_lora.so.  Beside it, where Python's headers and
+torch are installed, fastcall.*.so: the 8-bit operators' calls from Python
+without ctypes (a C++ extension, named by the Python and the torch that it was
+built against).  Where it does not build, a warning says so and the calls go
+through ctypes.
 Usage: python -m lora_moe_gb300.build
 """
 import concurrent.futures
 import fcntl
+import importlib.metadata
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,7 +26,17 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmoe_lora.so")
 SOURCES = ["api.cu", "align.cu", "fused_cuda_core.cu", "fused_tcgen05.cu", "stream_pipeline.cu",
            "fused_stream_cluster.cu", "align_static_workspace.cu", "api_fp8.cu", "fp8_rows.cu", "fp8_matmul.cu", "fp8_stream.cu"]
-FASTCALL = os.path.join(OUT_DIR, "fastcall.so")
+
+
+def _torch_version():
+    """torch's version without importing it, or None where it is not installed."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+FASTCALL = os.path.join(OUT_DIR, "fastcall.%s.torch-%s.so" % (sysconfig.get_config_var("SOABI"), _torch_version()))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -64,9 +78,28 @@ def _build_fastcall():
     os.replace(tmp, FASTCALL)
 
 
+def _try_fastcall():
+    """Build fastcall, or note why it does not build: not tried again until its inputs change."""
+    try:
+        _build_fastcall()
+    except Exception as e:
+        with open(FASTCALL + ".failed", "w") as f:
+            f.write(str(e))
+        warnings.warn("the 8-bit operators' calls go through ctypes: %s" % e)
+
+
+def _fastcall_settled():
+    """Built for this Python and torch from the present sources, known not to build, or not to be built here."""
+    if not _has_python_headers() or _torch_version() is None:
+        return True
+    inputs = max(os.path.getmtime(f) for f in (os.path.join(CSRC, "fastcall.cpp"),
+                                               os.path.join(INCLUDE, "moe_lora.h"), __file__))
+    return any(os.path.exists(f) and os.path.getmtime(f) >= inputs for f in (FASTCALL, FASTCALL + ".failed"))
+
+
 def build(force=False, verbose=False, ptxas_info=False):
     always = force or ptxas_info
-    if not always and _is_current():
+    if not always and _is_current() and _fastcall_settled():
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     # One process at a time: the object files are shared. One that waited finds the other's result.
@@ -74,6 +107,8 @@ def build(force=False, verbose=False, ptxas_info=False):
         fcntl.flock(lock, fcntl.LOCK_EX)
         if always or not _is_current():
             _build(verbose, ptxas_info)
+        if not _fastcall_settled():     # (the library was current)
+            _try_fastcall()
     return LIB
 
 
@@ -99,7 +134,7 @@ def _build(verbose, ptxas_info):
         return obj
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        fast = ex.submit(_build_fastcall) if _has_python_headers() else None
+        fast = ex.submit(_try_fastcall) if _has_python_headers() and _torch_version() is not None else None
         objs = list(ex.map(compile_one, SOURCES))
         if fast is not None:
             fast.result()
