@@ -32,6 +32,7 @@
 #include "device_utils.cuh"
 #include "fp8.h"
 #include "fp8_blocks.cuh"
+#include "launch.cuh"
 #include "stream_pipeline.cuh"
 
 namespace moe_lora {
@@ -823,28 +824,6 @@ bool register_shares_fit(Kernel kernel) {
   return attr.numRegs * kWideThreads >= 128 * kWideRegsIssue + 256 * kWideRegsEpilogue;
 }
 
-template <typename... Params, typename... Args>
-int launch(void (*kernel)(Params...), const Fp8Cfg &cfg, unsigned grid, int threads, cudaStream_t stream,
-           const Args &...args) {
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(grid, 1, 1);
-  lc.blockDim = dim3(threads, 1, 1);
-  lc.dynamicSmemBytes = cfg.smem_bytes;
-  lc.stream = stream;
-  // May start while the kernel before it is finishing: barriers, tensor memory
-  // and tensor maps are set up before it waits for that kernel.
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cfg.cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = cfg.cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? 0 : MOE_LORA_ERR_LAUNCH;
-}
-
 // Clusters of this shape that are resident at once; asked once for each shape.
 template <typename Kernel>
 int resident_clusters(Kernel kernel, const Fp8Cfg &cfg, int threads, const DeviceInfo &dev) {
@@ -927,7 +906,8 @@ int launch_narrow(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) 
   const unsigned clusters = (unsigned)std::min<long long>(items, std::min(fit, dev.sm_count / cs));
   Fp8Maps maps;
   if (int st = make_maps(a, a.x, a.rows, a.ldx, kRows, MODE == kFp8Dense ? BT : 1, &maps)) return st;
-  return launch(fp8_narrow_kernel<BT, MODE>, cfg, clusters * cs, kNarrowThreads, stream, maps, a, cfg);
+  return launch_dependent(fp8_narrow_kernel<BT, MODE>, clusters * cs, kNarrowThreads, cs, cfg.smem_bytes, stream, maps, a,
+                          cfg);
 }
 
 template <int MODE>
@@ -937,7 +917,6 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
   const long long rows = (long long)a.max_blocks * a.block;
   const long long tiles = tile_bound(a, MODE == kFp8Sorted);
   if (tiles <= 0) return 0;
-  cfg.cluster = 2;
   cfg.stages = kWideStages;
   cfg.off_ctrl = kWideStages * kWideStage + 8 * kWideOut;
   cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(WideCtrl);
@@ -953,15 +932,14 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
     uint8_t *base = static_cast<uint8_t *>(workspace);
     g.tiles = reinterpret_cast<WideTile *>(base + w.tiles);
     if (int st = make_maps(a, base + w.x, rows, w.ld, kHalf / 2, kRows, &maps)) return st;
-    Fp8Cfg gather = {};
-    gather.cluster = 1;
-    if (int st = launch(fp8_gather_kernel, gather, (unsigned)std::min<long long>((rows + 7) / 8, dev.sm_count * 8ll),
-                        kGatherThreads, stream, a, reinterpret_cast<WideTile *>(base + w.tiles), base + w.x, w.ld))
+    if (int st = launch_dependent(fp8_gather_kernel, (unsigned)std::min<long long>((rows + 7) / 8, dev.sm_count * 8ll),
+                                  kGatherThreads, 1, 0, stream, a, reinterpret_cast<WideTile *>(base + w.tiles),
+                                  base + w.x, w.ld))
       return st;
   }
   const long long items = tiles * cfg.nt;   // (the sorted arrays' own tiles are no more, but for entries that no align writes)
   const unsigned grid = 2 * (unsigned)std::min<long long>(items, dev.sm_count / 2);
-  return launch(fp8_wide_kernel<MODE>, cfg, grid, kWideThreads, stream, maps, a, g, cfg);
+  return launch_dependent(fp8_wide_kernel<MODE>, grid, kWideThreads, 2, cfg.smem_bytes, stream, maps, a, g, cfg);
 }
 
 }  // namespace

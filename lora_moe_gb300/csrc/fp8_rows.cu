@@ -19,6 +19,7 @@
 
 #include "device_utils.cuh"
 #include "fp8.h"
+#include "launch.cuh"
 
 namespace moe_lora {
 
@@ -174,7 +175,9 @@ __global__ void __launch_bounds__(512) norm_fp8_kernel(const NormArgs p) {
   }
 }
 
-// Exact quotients of 31-bit numbers by a divisor, with one multiplication.
+// Exact quotients of 31-bit numbers by a divisor, with one multiplication
+// (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994).
 struct FastDiv {
   uint32_t d, mul, shift;
   explicit FastDiv(uint32_t div) : d(div), shift(0) {
@@ -228,22 +231,6 @@ __global__ void __launch_bounds__(kActThreads, 8) act_fp8_kernel(const ActArgs p
   }
 }
 
-// May start while the kernel before it is finishing: every kernel here waits
-// for it before it touches memory.
-template <typename... Params, typename... Args>
-int launch(void (*kernel)(Params...), unsigned grid, unsigned threads, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(grid, 1, 1);
-  lc.blockDim = dim3(threads, 1, 1);
-  lc.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, kernel, args...) == cudaSuccess ? 0 : MOE_LORA_ERR_LAUNCH;
-}
-
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 template <bool VEC>
@@ -255,10 +242,10 @@ int launch_norm(const NormArgs &a, const DeviceInfo &dev, cudaStream_t s) {
   const int nv = vecs > 1024 ? 4 : (vecs > 512 || (!few && vecs >= 128) ? 2 : 1);
   const int threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
   if (nv == 1)
-    return a.parts > 2 ? launch(norm_fp8_kernel<1, 4, VEC>, a.M, threads, s, a)
-                       : launch(norm_fp8_kernel<1, 2, VEC>, a.M, threads, s, a);
-  if (nv == 2) return launch(norm_fp8_kernel<2, 2, VEC>, a.M, threads, s, a);
-  return launch(norm_fp8_kernel<4, 1, VEC>, a.M, threads, s, a);
+    return a.parts > 2 ? launch_dependent(norm_fp8_kernel<1, 4, VEC>, a.M, threads, 1, 0, s, a)
+                       : launch_dependent(norm_fp8_kernel<1, 2, VEC>, a.M, threads, 1, 0, s, a);
+  if (nv == 2) return launch_dependent(norm_fp8_kernel<2, 2, VEC>, a.M, threads, 1, 0, s, a);
+  return launch_dependent(norm_fp8_kernel<4, 1, VEC>, a.M, threads, 1, 0, s, a);
 }
 
 }  // namespace
@@ -292,9 +279,9 @@ int launch_act_fp8(const ActArgs &all, const DeviceInfo &dev, cudaStream_t s) {
     // two groups a thread once that leaves every SM's eight CTAs work, else one (latency)
     const bool many = items >= (uint32_t)dev.sm_count * 8 * 32;
     const uint32_t per_cta = kActThreads / 16 * (many ? 2 : 1), grid = (items + per_cta - 1) / per_cta;
-    const int st = many ? launch(vec ? act_fp8_kernel<2, true> : act_fp8_kernel<2, false>, grid, kActThreads, s, a, items, div)
-                        : launch(vec ? act_fp8_kernel<1, true> : act_fp8_kernel<1, false>, grid, kActThreads, s, a, items, div);
-    if (st) return st;
+    const auto kernel = many ? (vec ? act_fp8_kernel<2, true> : act_fp8_kernel<2, false>)
+                             : (vec ? act_fp8_kernel<1, true> : act_fp8_kernel<1, false>);
+    if (int st = launch_dependent(kernel, grid, kActThreads, 1, 0, s, a, items, div)) return st;
   }
   return 0;
 }

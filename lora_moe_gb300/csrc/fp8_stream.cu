@@ -23,6 +23,7 @@
 #include "device_utils.cuh"
 #include "fp8.h"
 #include "fp8_blocks.cuh"
+#include "launch.cuh"
 
 namespace moe_lora {
 
@@ -187,17 +188,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) fp8_stream_kernel
 template <int NT, int RG, int MODE>
 int launch_rg(const Fp8Args &a, long long units, cudaStream_t stream) {
   const int tiles = (a.N + 16 * RG - 1) / (16 * RG);
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)std::min<long long>(units * tiles, 1ll << 30), 1, 1);
-  lc.blockDim = dim3(kThreads, 1, 1);
-  lc.stream = stream;
-  // may start while the kernel before it is finishing (it waits for it before it reads anything)
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, fp8_stream_kernel<NT, RG, MODE>, a, tiles) == cudaSuccess ? 0 : MOE_LORA_ERR_LAUNCH;
+  return launch_dependent(fp8_stream_kernel<NT, RG, MODE>, (unsigned)std::min<long long>(units * tiles, 1ll << 30), kThreads,
+                          1, 0, stream, a, tiles);
 }
 
 // CTAs of 16, 32 or 64 rows, their eight warps splitting K in eight, four or
