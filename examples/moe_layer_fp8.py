@@ -76,6 +76,7 @@ class MoELayer:
         B.moe_add_rms_norm_fp8(rows, self.norm, x8, xs, residual=residual, residual_out=residual, normed=x)
         ids, weights = self.route(x)
 
+        # every id is one of this layer's experts, so every row is written (a rank that holds some of them zeroes these)
         y13, y2 = new(M, topk, 2 * I), new(M, topk, H)
         act, act8 = new(M * topk, I), new(M * topk, I, dtype=F8)
         act_s = new(M * topk, B.fp8_groups(I), dtype=torch.float32)

@@ -460,6 +460,11 @@ int moe_lora_align_static_workspace(const int32_t *topk_ids, const int32_t *toke
  *   moe_lora_fused_*          y2 += adapters (reads act)
  *   moe_add_rms_norm_fp8      the next norm sums each token's top-k rows of y2
  *
+ * The products write the rows of the pairs that they are given and no others.
+ * Where some pairs are given to none (a rank that holds some of the experts, and
+ * whose router's other ids the align drops), y13 and y2 are zeroed before the
+ * products: the activation and the next norm read every pair's row.
+ *
  * 8-bit values are e4m3 (finite: 448 is the largest, 0x7f and 0xff are NaN).
  * A group is 128 consecutive columns; the last one of a row may be shorter.
  * Row operands have one fp32 scale a group ([rows, ceil(n / 128)], dense);
@@ -562,8 +567,8 @@ int moe_fp8_matmul(const moe_lora_fp8 *x, long long ldx, const float *x_scales, 
  *     Its contents need no initialisation and are overwritten.
  * Calls with at least 20 pairs an expert on average (and more than a round of
  * work) gather x into the order of the blocks, in the workspace, and run the
- * kernel bound by the tensor cores; others the one bound by the weight's bytes.  Sizes and limits as for
- * moe_align_block_size and moe_fp8_matmul.  An expert id out of range skips its
+ * kernel bound by the tensor cores; others the one bound by the weight's bytes.
+ * Sizes and limits as for moe_align_block_size and moe_fp8_matmul.  An expert id out of range skips its
  * block (MOE_LORA_DEVERR_EXPERT_ID), a pair id that is neither a pair nor the
  * sentinel is skipped (MOE_LORA_DEVERR_PAIR_ID, as is a pair that follows 16 or
  * more sentinels of its block).

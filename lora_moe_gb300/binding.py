@@ -588,7 +588,8 @@ def moe_fp8_grouped_matmul(x, x_scales, w, w_scales, y, sorted_token_ids, expert
 
     x: float8_e4m3fn [M, K] ([M*topk, K] with x_per_pair); w: float8_e4m3fn [E,
     N, K], w_scales: float32 [E, ceil(N / 128), ceil(K / 128)]; y: bf16 [M,
-    topk, N], written in place for every pair of a block; topk_weights: float32
+    topk, N], written in place for every pair of a block and no other (zero it
+    first where the align drops pairs and all rows are read); topk_weights: float32
     [M, topk] or None.  workspace: a uint8 tensor of at least
     fp8_grouped_workspace_bytes(...) bytes; without one, calls that need one
     take it from torch's allocator."""

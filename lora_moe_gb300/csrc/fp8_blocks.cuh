@@ -56,12 +56,12 @@ __device__ __forceinline__ void flag_unit(const Fp8Args &p, int b, int bt, int e
     if (lane == 0) flag_error(p.err, MOE_LORA_DEVERR_EXPERT_ID);
     return;
   }
-  if (MODE != kFp8Sorted) return;
-  for (int t = lane; t < bt; t += 32) {
-    const int f = load_global(p.sorted_token_ids + (size_t)b * bt + t);
-    // neither a pair nor the sentinel, or (in a skipped unit) a pair after a sentinel
-    if ((unsigned)f > (unsigned)p.pairs || (e == kNoPairs && f != p.pairs)) flag_error(p.err, MOE_LORA_DEVERR_PAIR_ID);
-  }
+  if constexpr (MODE == kFp8Sorted)
+    for (int t = lane; t < bt; t += 32) {
+      const int f = load_global(p.sorted_token_ids + (size_t)b * bt + t);
+      // neither a pair nor the sentinel, or (in a skipped unit) a pair after a sentinel
+      if ((unsigned)f > (unsigned)p.pairs || (e == kNoPairs && f != p.pairs)) flag_error(p.err, MOE_LORA_DEVERR_PAIR_ID);
+    }
 }
 template <int MODE>
 __device__ __forceinline__ float pair_weight(const Fp8Args &p, int f) {

@@ -19,8 +19,9 @@
 //   wide    pairs of CTAs (cta_group::2), 256 pairs by 256 output columns, on
 //           rows gathered into the blocks' order: bound by the tensor cores,
 //           the hand-shake with the epilogue and, over seconds, by power.
-//           8192 x 4096 x 4096 dense: 97 us (2.8 PFLOP/s; 110 us with the
-//           power limit reached); Mixtral-shaped w13 prefill: 1.49 ms (1.75).
+//           8192 x 4096 x 4096 dense: 111 us (2.5 PFLOP/s) in calls that go on
+//           for seconds, with the power limit reached, 97 us in short runs;
+//           Mixtral-shaped w13 prefill: 1.79 ms (2.15 PFLOP/s), and 1.5.
 // Products of few rows and small weights are fp8_stream.cu's.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -958,8 +959,11 @@ constexpr double kStreamBytes = 32e6;
 // 123 / 95, 64 220 / 100; with a skewed router 4 57 / 74, 8 71 / 89, 16 89 / 96.
 // (Units of 32 and 64 were slower than of 16 wherever the narrow kernel wins:
 // 92 us at 16 pairs an expert, also over gathered rows.)
+// That is one weight's shape: K and N are not in the rule, though the bytes that
+// a unit reads again and the cost of a tile grow with them.
 // The narrow one also while a round of its items covers the output (16 experts
-// of 1024 x 1024 and 128 pairs: 10 us, 13 wide).
+// of 1024 x 1024 and 128 pairs: 10 us, 13 wide).  A round is a GB300's 152 SMs,
+// not the current device's: the workspace's size is asked for on hosts without one.
 constexpr long long kRoundItems = 152;
 bool fp8_sorted_is_wide(const Fp8Args &a) {
   const long long units = a.pairs / 16 + std::min(a.E, a.pairs);
