@@ -33,7 +33,7 @@ int check_product(const Fp8Args &a, bool *empty) {
   return 0;
 }
 
-int grouped(Fp8Args a, Fp8Mode mode, int M, void *workspace, size_t workspace_bytes, void *stream) {
+int grouped(Fp8Args a, ProductMode mode, int M, void *workspace, size_t workspace_bytes, void *stream) {
   if (M < 0 || a.topk < 1 || a.E < 1) return MOE_LORA_ERR_INVALID_ARG;
   if (a.E > kMaxExperts || a.topk > a.E) return MOE_LORA_ERR_UNSUPPORTED;
   const long long pairs = (long long)M * a.topk;
@@ -47,11 +47,11 @@ int grouped(Fp8Args a, Fp8Mode mode, int M, void *workspace, size_t workspace_by
   if (empty) return MOE_LORA_OK;
   const void *ids[4] = {a.sorted_token_ids, a.expert_ids, a.num_tokens_post_padded, a.topk_ids};
   for (int i = 0; i < 4; ++i) {
-    if (!ids[i] && (i == 3) == (mode == kFp8Naive)) return MOE_LORA_ERR_INVALID_ARG;
+    if (!ids[i] && (i == 3) == (mode == kNaive)) return MOE_LORA_ERR_INVALID_ARG;
     if (!on(ids[i], 4)) return MOE_LORA_ERR_MISALIGNED;
   }
   if (!fp8_items_fit(a, mode)) return MOE_LORA_ERR_UNSUPPORTED;
-  if (mode == kFp8Sorted) {
+  if (mode == kSorted) {
     const size_t need = fp8_sorted_workspace(a);
     if (need && (!workspace || workspace_bytes < need)) return MOE_LORA_ERR_WORKSPACE;
     if (need && !on(workspace, 16)) return MOE_LORA_ERR_MISALIGNED;
@@ -153,10 +153,10 @@ int moe_fp8_matmul(const moe_lora_fp8 *x, long long ldx, const float *x_scales, 
   if (empty) return MOE_LORA_OK;
   a.KB = fp8_groups(K);
   a.NB = fp8_groups(N);
-  if (!fp8_items_fit(a, kFp8Dense)) return MOE_LORA_ERR_UNSUPPORTED;
+  if (!fp8_items_fit(a, kDense)) return MOE_LORA_ERR_UNSUPPORTED;
   DeviceInfo dev;
   if (int st = current_device_info(&dev)) return st;
-  return launch_fp8_matmul(a, kFp8Dense, nullptr, dev, static_cast<cudaStream_t>(stream));
+  return launch_fp8_matmul(a, kDense, nullptr, dev, static_cast<cudaStream_t>(stream));
 }
 
 size_t moe_fp8_grouped_workspace_bytes(int M, int topk, int num_experts, int K, int N, int block_size) {
@@ -208,7 +208,7 @@ int moe_fp8_grouped_matmul(const moe_lora_fp8 *x, int x_per_pair, long long ldx,
   a.block = block_size;
   a.max_blocks = (int)(cap / block_size);   // an align's blocks are whole ones
   a.err = err_flag;
-  return grouped(a, kFp8Sorted, M, workspace, workspace_bytes, stream);
+  return grouped(a, kSorted, M, workspace, workspace_bytes, stream);
 }
 
 int moe_fp8_grouped_matmul_naive(const moe_lora_fp8 *x, int x_per_pair, long long ldx, const float *x_scales,
@@ -233,7 +233,7 @@ int moe_fp8_grouped_matmul_naive(const moe_lora_fp8 *x, int x_per_pair, long lon
   a.N = N;
   a.block = 16;
   a.err = err_flag;
-  return grouped(a, kFp8Naive, M, nullptr, 0, stream);
+  return grouped(a, kNaive, M, nullptr, 0, stream);
 }
 
 }  // extern "C"

@@ -475,6 +475,27 @@ __device__ __forceinline__ T load_global(const T *p) {
   return *p;
 }
 
+// 16 bytes that are read once: not kept in L1.
+__device__ __forceinline__ uint4 load_streamed(const uint8_t *p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
+// 16 bytes of a row from byte k on, zeros past the row's K bytes; nothing past
+// them is read.
+__device__ __forceinline__ uint4 load_tail(const uint8_t *row, int k, int K) {
+  if (k + 16 <= K) return load_global(reinterpret_cast<const uint4 *>(row + k));
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (k + i < K) w[i >> 2] |= (uint32_t)load_global(row + k + i) << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // True in one lane of a converged warp.  Around tcgen05 and bulk-copy
 // instructions inside a loop that the whole warp runs, it lets the compiler
 // keep their operands in uniform registers: four 8-bit MMAs of 128 columns
@@ -534,6 +555,18 @@ __device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
+// The same over a pair of CTAs: A and D's rows are split between them (each
+// holds 128 of 256 at the same offsets), B's rows too (half of N each).
+__device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // D[tmem] (+)= A[smem] * B[smem]^T, 8-bit floating-point inputs (K = 32 a
 // call), fp32 accumulate.
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
@@ -546,8 +579,7 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
-// The same over a pair of CTAs: A and D's rows are split between them (each
-// holds 128 of 256 at the same offsets), B's rows too (half of N each).
+// The same over a pair of CTAs, as above.
 __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(

@@ -7,6 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "blocks.cuh"
 #include "internal.h"
 
 namespace moe_lora {
@@ -42,32 +43,24 @@ struct ActArgs {
 };
 int launch_act_fp8(const ActArgs &a, const DeviceInfo &dev, cudaStream_t stream);
 
-// 8-bit products.  Dense: one expert, one block per `block` rows, pair f is row f.
-enum Fp8Mode { kFp8Dense = 0, kFp8Sorted = 1, kFp8Naive = 2 };
-struct Fp8Args {
+// 8-bit products.
+struct Fp8Args : PairBlocks {
   const uint8_t *x;           // e4m3 [rows, ldx]
   const float *x_scales;      // fp32 [rows, KB]
   const uint8_t *w;           // e4m3 [E, N, ldw]
   const float *w_scales;      // fp32 [E, NB, KB]
   uint16_t *y;                // bf16 [pairs, ldy]
-  const float *topk_weights;  // fp32 [pairs] or null
-  const int32_t *sorted_token_ids, *expert_ids, *num_tokens_post_padded;   // sorted
-  const int32_t *topk_ids;                                                 // naive
-  int32_t *err;               // may be null
   long long ldx, ldw, ldy;
-  int rows, pairs, topk, E, K, N, KB, NB;
-  int block;                  // pairs per block (sorted)
-  int max_blocks;             // blocks that the sorted arrays hold
-  int x_per_pair;             // row of pair f is f, else f / topk
+  int rows, K, N, KB, NB;
 };
 // Naive calls, and dense ones of at most 16 rows, whose weights are small.
-int launch_fp8_stream(const Fp8Args &a, Fp8Mode mode, const DeviceInfo &dev, cudaStream_t stream);
+int launch_fp8_stream(const Fp8Args &a, ProductMode mode, const DeviceInfo &dev, cudaStream_t stream);
 // Sorted calls with many pairs an expert gather x into the workspace (the
 // bytes it needs; 0: none).
 size_t fp8_sorted_workspace(const Fp8Args &a);
 // Whether the kernels' work items of a call can be counted in an int; asked
 // before anything is enqueued.
-bool fp8_items_fit(const Fp8Args &a, Fp8Mode mode);
-int launch_fp8_matmul(const Fp8Args &a, Fp8Mode mode, void *workspace, const DeviceInfo &dev, cudaStream_t stream);
+bool fp8_items_fit(const Fp8Args &a, ProductMode mode);
+int launch_fp8_matmul(const Fp8Args &a, ProductMode mode, void *workspace, const DeviceInfo &dev, cudaStream_t stream);
 
 }  // namespace moe_lora

@@ -27,20 +27,19 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <mutex>
-#include <type_traits>
 
+#include "blocks.cuh"
 #include "device_utils.cuh"
 #include "fp8.h"
-#include "fp8_blocks.cuh"
+#include "gather.h"
 #include "launch.cuh"
+#include "narrow.cuh"
 #include "stream_pipeline.cuh"
 
 namespace moe_lora {
 
 namespace {
 
-constexpr int kRows = 128;                     // rows of an accumulator: lanes of tensor memory
 constexpr int kTileBytes = kRows * kFp8Group;  // 128 rows of one group: 16 KB, one swizzle row of 128 bytes each
 
 struct Fp8Maps {
@@ -60,10 +59,8 @@ struct Fp8Cfg {
 
 // ------------------------------------------------------------------ narrow
 
-constexpr int kNarrowThreads = 256;
 constexpr int kMaxRing = 12;
 constexpr int kScaleSlots = 16;   // ring of scale rows, one group each
-constexpr int kListUnits = 2048;
 
 template <int BT>
 struct Narrow {
@@ -88,76 +85,6 @@ struct NarrowCtrl {
   int live;                                  // units in the list
   int warp_live[kNarrowThreads / 32];
 };
-
-// The units of a sorted call that hold pairs, in order: where a block is
-// several units, most of a decode batch's hold none, and every CTA would look
-// each of them up for every tile of N (256 tokens, blocks of 64: 97 us against
-// 76 in blocks of 16, which need no list).  By the whole CTA.
-template <int BT>
-__device__ __forceinline__ void list_units(const Fp8Args &p, int units, int *list, NarrowCtrl &ctl, int tid) {
-  const int lane = tid & 31, warp = tid >> 5;
-  int n = 0;   // (the same in every thread)
-  for (int base = 0; base < units; base += kNarrowThreads) {
-    const int b = base + tid;
-    const int e = b < units ? block_expert<kFp8Sorted>(p, b, BT) : kNoPairs;
-    const uint32_t live = __ballot_sync(0xFFFFFFFFu, e >= 0);
-    if (lane == 0) ctl.warp_live[warp] = __popc(live);
-    __syncthreads();
-    int at = n;
-    for (int w = 0; w < kNarrowThreads / 32; ++w) {
-      if (w < warp) at += ctl.warp_live[w];
-      n += ctl.warp_live[w];
-    }
-    if (e >= 0) list[at + __popc(live & ((1u << lane) - 1))] = b;
-    __syncthreads();
-  }
-  if (tid == 0) ctl.live = n;
-  __syncthreads();
-}
-
-// The items of a CTA, in the order of its warps' loops: all of K, or (a cluster
-// of cs > 1 CTAs, which has one item at most) this CTA's share of it.
-struct NarrowWork {
-  int items, next, step, it, kb0, kb1, rank;
-  __device__ __forceinline__ NarrowWork(int n, int KB, int cs) : items(n) {
-    rank = blockIdx.x % cs;   // (a cluster is cs consecutive CTAs)
-    next = blockIdx.x / cs;
-    step = cs > 1 ? items : gridDim.x;
-    kb0 = (int)((long long)KB * rank / cs);
-    kb1 = (int)((long long)KB * (rank + 1) / cs);
-  }
-  __device__ __forceinline__ bool advance() {
-    if (next >= items) return false;
-    it = next;
-    next += step;   // (cs > 1: past the last)
-    return true;
-  }
-};
-
-// The sums of one CTA's positions over CS ranks, in rank order; Q of 4
-// positions (or 2) at a time.
-template <int CS, int W>
-__device__ __forceinline__ void sum_ranks(const float *buf, int per_rank, int at, int row, float (&v)[W]) {
-#pragma unroll
-  for (int i = 0; i < W; ++i) v[i] = 0.f;
-#pragma unroll
-  for (int q = 0; q < CS; ++q) {
-    const float *src = buf + ((q * per_rank + at) * kRows + row) * W;
-    if constexpr (W == 4) {
-      const float4 u = *reinterpret_cast<const float4 *>(src);
-      v[0] += u.x;
-      v[1] += u.y;
-      v[2] += u.z;
-      v[3] += u.w;
-    } else if constexpr (W == 2) {
-      const float2 u = *reinterpret_cast<const float2 *>(src);
-      v[0] += u.x;
-      v[1] += u.y;
-    } else {
-      v[0] += *src;
-    }
-  }
-}
 
 template <int BT, int MODE>
 __global__ void __launch_bounds__(kNarrowThreads, 1)
@@ -203,9 +130,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   const int all_units = num_units<MODE>(p, BT);
   int units = all_units;
   const int *list = nullptr;
-  if (MODE == kFp8Sorted && cfg.list && units <= cfg.list) {
+  if (MODE == kSorted && cfg.list && units <= cfg.list) {
     int *l = reinterpret_cast<int *>(smem + cfg.off_list);
-    list_units<BT>(p, units, l, ctl, tid);
+    list_units<BT>(p, units, l, ctl.warp_live, &ctl.live, tid);
     list = l;
     units = ctl.live;
   }
@@ -224,7 +151,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       if (e < 0) continue;
       int row[4];
       bool mine = false;   // lane i gathers rows 4i .. 4i+3; groups without a pair are left as they are
-      if (MODE != kFp8Dense && lane < BT / 4) {
+      if (MODE != kDense && lane < BT / 4) {
         int some = -1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -237,7 +164,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         for (int i = 0; i < 4; ++i)
           if (row[i] < 0) row[i] = some;
       }
-      const int groups = MODE == kFp8Dense ? BT / 4 : __popc(__ballot_sync(0xFFFFFFFFu, mine));
+      const int groups = MODE == kDense ? BT / 4 : __popc(__ballot_sync(0xFFFFFFFFu, mine));
       for (int kb = wk.kb0; kb < wk.kb1; kb += 2) {
         go = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.empty[s], ph ^ 1, abort, p.err));
         if (!go) break;
@@ -248,12 +175,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
           mbar_arrive_expect_tx(&ctl.full[s], n * (kTileBytes + groups * 4 * kFp8Group));
           for (int i = 0; i < n; ++i)
             tma_load_3d(st + i * C::kGroup, &maps.w, (kb + i) * kFp8Group, nt * kRows, e, &ctl.full[s]);
-          if (MODE == kFp8Dense)
+          if (MODE == kDense)
             for (int i = 0; i < n; ++i)
               tma_load_2d(st + i * C::kGroup + kTileBytes, &maps.x, (kb + i) * kFp8Group, b * BT, &ctl.full[s]);
         }
         __syncwarp();
-        if (MODE != kFp8Dense && mine)
+        if (MODE != kDense && mine)
           for (int i = 0; i < n; ++i)
             tma_gather4(st + i * C::kGroup + kTileBytes + lane * 4 * kFp8Group, &maps.x, (kb + i) * kFp8Group, row,
                         &ctl.full[s]);
@@ -329,7 +256,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     cp_async_wait_all();
   } else if (warp == 3) {
     // ---------------- what is out of range, each unit once
-    if (MODE != kFp8Dense)
+    if (MODE != kDense)
       for (int b = blockIdx.x; b < all_units; b += gridDim.x)
         flag_unit<MODE>(p, b, BT, block_expert<MODE>(p, b, BT), lane);
   } else if (warp >= 4) {
@@ -378,64 +305,19 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       auto store = [&](int f, float v) {
         if (f >= 0 && n < p.N) p.y[(size_t)f * p.ldy + n] = float_to_bf16_bits(v * pair_weight<MODE>(p, f));
       };
-      constexpr int kLive = MODE == kFp8Naive ? 1 : BT;   // positions that can hold a pair
+      constexpr int kLive = MODE == kNaive ? 1 : BT;   // positions that can hold a pair
       if (cs == 1) {
 #pragma unroll
         for (int c = 0; c < kLive; ++c) store(block_pair<MODE>(p, b, c, BT), acc[c]);
         continue;
       }
-      // Rank q sums the positions [q * tc, (q + 1) * tc) of every rank's
-      // partial sums, in rank order (one position: rank 0 does).  There is one
-      // item at most, so that the buffer is used once, and every CTA waits for
-      // all that is sent to it: nothing reaches a CTA that has left.
-      const int tc = MODE == kFp8Naive ? 1 : BT / cs, lg = __ffs(tc) - 1;
-      const uint32_t red_base = smem_addr(smem + cfg.off_red), red_bar = smem_addr(&ctl.red_full);
-      const bool receives = MODE != kFp8Naive || wk.rank == 0;
-      if (row == 0 && receives) mbar_arrive_expect_tx(&ctl.red_full, (MODE == kFp8Naive ? cs : BT) * kRows * 4);
-      cluster_wait();
+      join_ranks<BT, MODE == kNaive>(acc, cs, wk.rank, row, smem + cfg.off_red, &ctl.red_full, abort, p.err,
+                                     [&](int t, const auto &v) {
+#pragma unroll
+                                       for (int i = 0; i < (int)(sizeof(v) / sizeof(float)); ++i)
+                                         store(block_pair<MODE>(p, b, t + i, BT), v[i]);
+                                     });
       waited = true;
-      if constexpr (MODE == kFp8Naive) {
-        st_async_f1(cluster_map(red_base + (wk.rank * kRows + row) * 4, 0), acc[0], cluster_map(red_bar, 0));
-      } else if (tc >= 4) {
-#pragma unroll
-        for (int c = 0; c < BT; c += 4) {
-          const int q = c >> lg, quad = (c - (q << lg)) >> 2;
-          st_async_v4(cluster_map(red_base + (((wk.rank * tc) >> 2) + quad) * kRows * 16 + row * 16, q),
-                      make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]), cluster_map(red_bar, q));
-        }
-      } else {   // two positions a rank
-#pragma unroll
-        for (int c = 0; c < BT; c += 2)
-          st_async_f2(cluster_map(red_base + (wk.rank * kRows + row) * 8, c >> 1), acc[c], acc[c + 1],
-                      cluster_map(red_bar, c >> 1));
-      }
-      if (!receives) continue;
-      mbar_wait_cluster(&ctl.red_full, 0, abort, p.err);
-      const float *buf = reinterpret_cast<const float *>(smem + cfg.off_red);
-      auto finish = [&](auto ranks) {
-        constexpr int CS = decltype(ranks)::value;
-        if constexpr (MODE == kFp8Naive) {
-          float v[1];
-          sum_ranks<CS>(buf, 1, 0, row, v);
-          store(b, v[0]);
-        } else if constexpr (BT / CS >= 4) {
-#pragma unroll 4
-          for (int quad = 0; quad < BT / CS / 4; ++quad) {
-            float v[4];
-            sum_ranks<CS>(buf, BT / CS / 4, quad, row, v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) store(block_pair<MODE>(p, b, wk.rank * (BT / CS) + quad * 4 + i, BT), v[i]);
-          }
-        } else {
-          float v[2];
-          sum_ranks<CS>(buf, 1, 0, row, v);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) store(block_pair<MODE>(p, b, wk.rank * 2 + i, BT), v[i]);
-        }
-      };
-      if (cs == 2) finish(std::integral_constant<int, 2>());
-      else if (cs == 4) finish(std::integral_constant<int, 4>());
-      else finish(std::integral_constant<int, 8>());
     }
   }
   if (cs > 1 && !waited) cluster_wait();
@@ -448,101 +330,6 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
 }
 
 // ------------------------------------------------------------------ wide
-
-// The rows of the sorted pairs, gathered once into the order of
-// sorted_token_ids: the wide kernel reads each of them N / 256 times, and TMA
-// fetches gathered rows four at a time at 80 clk each, cp.async by the
-// kernel's own warps at 40 % of the tensor cores' time.  CTA 0 also lists the
-// tiles of at most 256 rows of one expert.
-struct WideTile {
-  int row0, rows, expert, pad;
-};
-constexpr int kGatherThreads = 256;
-constexpr int kTileRows = 256;
-
-struct WideSpace {   // offsets into the workspace
-  size_t tiles, x, bytes;
-  long long rows, ld;   // capacity of the sorted arrays in whole blocks; bytes from row to row
-};
-WideSpace wide_space(long long rows, int K) {
-  WideSpace w;
-  w.rows = rows;
-  w.ld = (long long)fp8_groups(K) * kFp8Group;
-  w.tiles = 0;
-  // at most a tile for each of the sorted arrays' smallest blocks, and the count
-  w.x = ((size_t)(rows / 16 + 1) * sizeof(WideTile) + sizeof(WideTile) + 127) / 128 * 128;
-  w.bytes = w.x + (size_t)rows * w.ld;
-  return w;
-}
-
-__global__ void __launch_bounds__(kGatherThreads)
-    fp8_gather_kernel(const Fp8Args p, WideTile *tiles, uint8_t *xg, long long ld) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int bs = p.block;
-  wait_for_prior_grid();
-  const int nb = num_blocks(p);
-  if (blockIdx.x == 0) {
-    // Tile list.  Blocks of one expert are neighbours: a run.  A block heads a
-    // tile when the blocks before it in its run are a multiple of 256 rows; the
-    // last block of a tile writes it down.
-    __shared__ int warp_last[kGatherThreads / 32], warp_heads[kGatherThreads / 32], carry_first, carry_heads;
-    if (tid == 0) carry_first = carry_heads = 0;
-    __syncthreads();
-    const int per_tile = kTileRows / bs;
-    for (int base = 0; base < nb; base += kGatherThreads) {
-      const int b = base + tid;
-      const int e = b < nb ? load_global(p.expert_ids + b) : -1;
-      const int before_e = b > 0 && b < nb ? load_global(p.expert_ids + b - 1) : e, after_e = b + 1 < nb ? load_global(p.expert_ids + b + 1) : e;
-      int run = b < nb && (b == 0 || before_e != e) ? b : -1;   // first block of b's run: the last such at or before b
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, run, d);
-        if (lane >= d) run = max(run, o);
-      }
-      if (lane == 31) warp_last[warp] = run;
-      __syncthreads();
-      int before = carry_first;
-      for (int w = 0; w < warp; ++w) before = max(before, warp_last[w]);
-      run = max(run, before);
-      const bool good = (unsigned)e < (unsigned)p.E;
-      if (b < nb && !good) flag_error(p.err, MOE_LORA_DEVERR_EXPERT_ID);
-      const int at = (b - run) % per_tile;   // place in the tile
-      const uint32_t heads = __ballot_sync(0xFFFFFFFFu, b < nb && good && at == 0);
-      if (lane == 31) warp_heads[warp] = __popc(heads);
-      __syncthreads();
-      int index = carry_heads + __popc(heads & (0xFFFFFFFFu >> (31 - lane)));   // heads up to b, b among them
-      for (int w = 0; w < warp; ++w) index += warp_heads[w];
-      // (tiles[0] is the count: tile i is tiles[1 + i])
-      if (b < nb && good && (at == per_tile - 1 || b + 1 == nb || after_e != e))
-        tiles[index] = {(b - at) * bs, (at + 1) * bs, e, 0};
-      __syncthreads();
-      if (tid == 0) {
-        for (int w = 0; w < kGatherThreads / 32; ++w) {
-          carry_first = max(carry_first, warp_last[w]);
-          carry_heads += warp_heads[w];
-        }
-      }
-      __syncthreads();
-    }
-    if (tid == 0) tiles[0] = {carry_heads, 0, 0, 0};
-  }
-  // one warp a row
-  const long long warps = (long long)gridDim.x * (kGatherThreads / 32);
-  for (long long r = (long long)blockIdx.x * (kGatherThreads / 32) + warp; r < (long long)nb * bs; r += warps) {
-    const int f = load_global(p.sorted_token_ids + r);
-    if ((unsigned)f >= (unsigned)p.pairs) {
-      if (f != p.pairs && lane == 0) flag_error(p.err, MOE_LORA_DEVERR_PAIR_ID);
-      continue;
-    }
-    const int xr = pair_row<kFp8Sorted>(p, f);
-    const uint8_t *src = p.x + (size_t)xr * p.ldx;
-    uint8_t *dst = xg + (size_t)r * ld;
-    const int whole = p.K / 16;
-    for (int c = lane; c < whole; c += 32)
-      *reinterpret_cast<uint4 *>(dst + c * 16) = load_global(reinterpret_cast<const uint4 *>(src + c * 16));
-    for (int c = whole * 16 + lane; c < p.K; c += 32) dst[c] = load_global(src + c);
-  }
-}
 
 // The wide kernel: pairs of CTAs (cta_group::2), 256 rows by 256 output
 // columns.  Each CTA holds 128 of the rows and half of the weight's columns in
@@ -609,11 +396,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   tc_fence_after();
   wait_for_prior_grid();
   const uint32_t tmem = ctl.tmem;
-  const int ntiles = MODE == kFp8Dense ? (p.pairs + kTileRows - 1) / kTileRows : load_global(&g.tiles[0].row0);
+  const int ntiles = MODE == kDense ? (p.pairs + kTileRows - 1) / kTileRows : load_global(&g.tiles[0].row0);
   const int items = ntiles * cfg.nt;   // rows fastest: pairs at work share the weight's columns
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   auto tile = [&](int t) {
-    if (MODE == kFp8Dense) return WideTile{t * kTileRows, min(kTileRows, p.pairs - t * kTileRows), 0, 0};
+    if (MODE == kDense) return WideTile{t * kTileRows, min(kTileRows, p.pairs - t * kTileRows), 0, 0};
     const int4 v = load_global(reinterpret_cast<const int4 *>(g.tiles) + 1 + t);
     return WideTile{v.x, v.y, v.z, 0};
   };
@@ -702,7 +489,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const WideTile t = tile(it - nt * ntiles);
       const int r = rank * kRows + quarter * 32 + lane;   // row of the tile
       int f = -1;
-      if (r < t.rows) f = MODE == kFp8Dense ? t.row0 + r : load_global(p.sorted_token_ids + t.row0 + r);
+      if (r < t.rows) f = MODE == kDense ? t.row0 + r : load_global(p.sorted_token_ids + t.row0 + r);
       if ((unsigned)f >= (unsigned)p.pairs) f = -1;
       const int nblk = nt * 2 + half;
       const float *sx = f < 0 ? nullptr : p.x_scales + (size_t)pair_row<MODE>(p, f) * p.KB;
@@ -825,63 +612,15 @@ bool register_shares_fit(Kernel kernel) {
   return attr.numRegs * kWideThreads >= 128 * kWideRegsIssue + 256 * kWideRegsEpilogue;
 }
 
-// Clusters of this shape that are resident at once; asked once for each shape.
-template <typename Kernel>
-int resident_clusters(Kernel kernel, const Fp8Cfg &cfg, int threads, const DeviceInfo &dev) {
-  if (cfg.cluster == 1) return dev.sm_count;
-  struct Entry {
-    const void *kernel;
-    int device, cluster, smem, clusters;
-  };
-  static std::mutex mu;
-  static Entry known[64];
-  static int n = 0;
-  std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < n; ++i)
-    if (known[i].kernel == (const void *)kernel && known[i].device == dev.device && known[i].cluster == cfg.cluster && known[i].smem == cfg.smem_bytes)
-      return known[i].clusters;
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)cfg.cluster, 1, 1);
-  lc.blockDim = dim3(threads, 1, 1);
-  lc.dynamicSmemBytes = cfg.smem_bytes;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cfg.cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  int clusters = 0;
-  if (cudaOccupancyMaxActiveClusters(&clusters, (const void *)kernel, &lc) != cudaSuccess) {
-    cudaGetLastError();   // a failed query leaves no sticky error
-    clusters = 0;
-  }
-  if (clusters < 1) clusters = std::max(1, dev.sm_count / cfg.cluster / 2);
-  if (n < 64) known[n++] = {(const void *)kernel, dev.device, cfg.cluster, cfg.smem_bytes, clusters};
-  return clusters;
-}
-
-// Upper bound of the call's units (skipped ones included).
-long long block_bound(const Fp8Args &a, Fp8Mode mode, int bt) {
-  if (mode == kFp8Dense) return ((long long)a.pairs + bt - 1) / bt;
-  if (mode == kFp8Naive) return a.pairs;
-  return std::min<long long>(a.max_blocks, fused_block_bound(a.pairs, 1, a.E, 1, a.block)) * (a.block / bt);
-}
-
-// Upper bound of the wide kernel's tiles of rows.
-long long tile_bound(const Fp8Args &a, bool sorted) {
-  return sorted ? a.pairs / kTileRows + std::min(a.E, a.pairs) : ((long long)a.pairs + kTileRows - 1) / kTileRows;
-}
-
 template <int BT, int MODE>
 int launch_narrow(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) {
   using C = Narrow<BT>;
   Fp8Cfg cfg = {};
   cfg.nt = (a.N + kRows - 1) / kRows;
-  const long long items = block_bound(a, (Fp8Mode)MODE, BT) * cfg.nt;
+  const long long items = unit_bound(a, (ProductMode)MODE, BT) * cfg.nt;
   if (items <= 0) return 0;
   if (int st = allow_dynamic_smem((const void *)fp8_narrow_kernel<BT, MODE>)) return st;
-  if (MODE == kFp8Sorted && a.block > BT) cfg.list = kListUnits;
+  if (MODE == kSorted && a.block > BT) cfg.list = kListUnits;
   // Clusters that split K: while there are too few items for the SMs, as large
   // as leaves each CTA two groups and every item a cluster of its own.  A ring
   // no longer than a CTA's share lets more clusters fit (of 8 CTAs with 200 KB
@@ -898,7 +637,7 @@ int launch_narrow(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) 
     cfg.off_list = cfg.off_red + (cs > 1 ? C::kRedBytes : 0);
     cfg.off_ctrl = cfg.off_list + list_bytes;
     cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(NarrowCtrl);
-    return resident_clusters(fp8_narrow_kernel<BT, MODE>, cfg, kNarrowThreads, dev);
+    return resident_clusters(fp8_narrow_kernel<BT, MODE>, cfg.cluster, cfg.smem_bytes, kNarrowThreads, dev);
   };
   int cs = 1;
   while (cs < 8 && items * cs * 2 <= dev.sm_count && a.KB >= cs * 4) cs *= 2;
@@ -906,7 +645,7 @@ int launch_narrow(const Fp8Args &a, const DeviceInfo &dev, cudaStream_t stream) 
   while (cs > 1 && fit < items) fit = shape(cs /= 2);
   const unsigned clusters = (unsigned)std::min<long long>(items, std::min(fit, dev.sm_count / cs));
   Fp8Maps maps;
-  if (int st = make_maps(a, a.x, a.rows, a.ldx, kRows, MODE == kFp8Dense ? BT : 1, &maps)) return st;
+  if (int st = make_maps(a, a.x, a.rows, a.ldx, kRows, MODE == kDense ? BT : 1, &maps)) return st;
   return launch_dependent(fp8_narrow_kernel<BT, MODE>, clusters * cs, kNarrowThreads, cs, cfg.smem_bytes, stream, maps, a,
                           cfg);
 }
@@ -916,7 +655,7 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
   Fp8Cfg cfg = {};
   cfg.nt = (a.N + kWideN - 1) / kWideN;
   const long long rows = (long long)a.max_blocks * a.block;
-  const long long tiles = tile_bound(a, MODE == kFp8Sorted);
+  const long long tiles = tile_bound(a, MODE == kSorted);
   if (tiles <= 0) return 0;
   cfg.stages = kWideStages;
   cfg.off_ctrl = kWideStages * kWideStage + 8 * kWideOut;
@@ -926,17 +665,14 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
   if (int st = allow_dynamic_smem((const void *)fp8_wide_kernel<MODE>)) return st;
   Fp8Maps maps;
   WideArgs g = {};
-  if (MODE == kFp8Dense) {
+  if (MODE == kDense) {
     if (int st = make_maps(a, a.x, a.rows, a.ldx, kHalf / 2, kRows, &maps)) return st;
   } else {
-    const WideSpace w = wide_space(rows, a.K);
+    const GatherSpace w = gather_space(rows, a.K);
     uint8_t *base = static_cast<uint8_t *>(workspace);
-    g.tiles = reinterpret_cast<WideTile *>(base + w.tiles);
+    g.tiles = reinterpret_cast<WideTile *>(base);
     if (int st = make_maps(a, base + w.x, rows, w.ld, kHalf / 2, kRows, &maps)) return st;
-    if (int st = launch_dependent(fp8_gather_kernel, (unsigned)std::min<long long>((rows + 7) / 8, dev.sm_count * 8ll),
-                                  kGatherThreads, 1, 0, stream, a, reinterpret_cast<WideTile *>(base + w.tiles),
-                                  base + w.x, w.ld))
-      return st;
+    if (int st = launch_gather(a, a.x, a.ldx, a.K, workspace, dev, stream)) return st;
   }
   const long long items = tiles * cfg.nt;   // (the sorted arrays' own tiles are no more, but for entries that no align writes)
   const unsigned grid = 2 * (unsigned)std::min<long long>(items, dev.sm_count / 2);
@@ -971,33 +707,33 @@ bool fp8_sorted_is_wide(const Fp8Args &a) {
 }
 
 size_t fp8_sorted_workspace(const Fp8Args &a) {
-  return fp8_sorted_is_wide(a) ? wide_space((long long)a.max_blocks * a.block, a.K).bytes : 0;
+  return fp8_sorted_is_wide(a) ? gather_space((long long)a.max_blocks * a.block, a.K).bytes : 0;
 }
 
-bool fp8_items_fit(const Fp8Args &a, Fp8Mode mode) {
-  if (mode == kFp8Dense ? a.pairs > 64 : mode == kFp8Sorted && fp8_sorted_is_wide(a))
-    return tile_bound(a, mode == kFp8Sorted) * ((a.N + kWideN - 1) / kWideN) <= INT32_MAX / 16;
+bool fp8_items_fit(const Fp8Args &a, ProductMode mode) {
+  if (mode == kDense ? a.pairs > 64 : mode == kSorted && fp8_sorted_is_wide(a))
+    return tile_bound(a, mode == kSorted) * ((a.N + kWideN - 1) / kWideN) <= INT32_MAX / 16;
   // every unit that the sorted arrays can hold, whatever they hold
-  const long long units = mode == kFp8Sorted ? (long long)a.max_blocks * (a.block / 16) : block_bound(a, mode, 16);
+  const long long units = mode == kSorted ? (long long)a.max_blocks * (a.block / 16) : unit_bound(a, mode, 16);
   return units * ((a.N + kRows - 1) / kRows) <= INT32_MAX;
 }
 
-int launch_fp8_matmul(const Fp8Args &a, Fp8Mode mode, void *workspace, const DeviceInfo &dev, cudaStream_t s) {
-  const bool small = (mode == kFp8Naive ? (double)a.pairs : 1.0) * a.N * a.K <= kStreamBytes;
-  if (mode == kFp8Naive) return small ? launch_fp8_stream(a, mode, dev, s) : launch_narrow<16, kFp8Naive>(a, dev, s);
-  if (mode == kFp8Sorted) {
-    if (fp8_sorted_is_wide(a)) return launch_wide<kFp8Sorted>(a, workspace, dev, s);
-    return launch_narrow<16, kFp8Sorted>(a, dev, s);
+int launch_fp8_matmul(const Fp8Args &a, ProductMode mode, void *workspace, const DeviceInfo &dev, cudaStream_t s) {
+  const bool small = (mode == kNaive ? (double)a.pairs : 1.0) * a.N * a.K <= kStreamBytes;
+  if (mode == kNaive) return small ? launch_fp8_stream(a, mode, dev, s) : launch_narrow<16, kNaive>(a, dev, s);
+  if (mode == kSorted) {
+    if (fp8_sorted_is_wide(a)) return launch_wide<kSorted>(a, workspace, dev, s);
+    return launch_narrow<16, kSorted>(a, dev, s);
   }
   if (small && a.pairs <= 16) return launch_fp8_stream(a, mode, dev, s);
-  if (a.pairs <= 16) return launch_narrow<16, kFp8Dense>(a, dev, s);
-  if (a.pairs <= 32) return launch_narrow<32, kFp8Dense>(a, dev, s);
+  if (a.pairs <= 16) return launch_narrow<16, kDense>(a, dev, s);
+  if (a.pairs <= 32) return launch_narrow<32, kDense>(a, dev, s);
   // The narrow kernel while one round of its 64 x 128 items covers the output
   // (192 x 4096 x 4096: 14.2 us, 16.2 wide), else the wide one (192 x 8192 x
   // 8192: 27 us, 41 narrow).
   const long long items = ((a.pairs + 63ll) / 64) * ((a.N + kRows - 1) / kRows);
-  if (a.pairs <= 64 || items <= dev.sm_count) return launch_narrow<64, kFp8Dense>(a, dev, s);
-  return launch_wide<kFp8Dense>(a, nullptr, dev, s);
+  if (a.pairs <= 64 || items <= dev.sm_count) return launch_narrow<64, kDense>(a, dev, s);
+  return launch_wide<kDense>(a, nullptr, dev, s);
 }
 
 }  // namespace moe_lora

@@ -22,7 +22,7 @@
 
 #include "device_utils.cuh"
 #include "fp8.h"
-#include "fp8_blocks.cuh"
+#include "blocks.cuh"
 #include "launch.cuh"
 
 namespace moe_lora {
@@ -32,26 +32,6 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 
-__device__ __forceinline__ uint4 load_weight(const uint8_t *p) {
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p)
-               : "memory");
-  return r;
-}
-
-// 16 bytes of a row from column k on, zeros past the row's K columns; nothing
-// past them is read.
-__device__ __forceinline__ uint4 load_tail(const uint8_t *row, int k, int K) {
-  if (k + 16 <= K) return load_global(reinterpret_cast<const uint4 *>(row + k));
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (k + i < K) w[i >> 2] |= (uint32_t)load_global(row + k + i) << (8 * (i & 3));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -60,7 +40,7 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // RG groups of 16 weight rows a CTA, K split over its other warps; NT tiles of 8 pairs.
-constexpr int ctas_per_sm(int mode) { return mode == kFp8Naive ? 3 : 2; }
+constexpr int ctas_per_sm(int mode) { return mode == kNaive ? 3 : 2; }
 // Two groups of K in flight a warp, and registers for two CTAs an SM (three for
 // single pairs, whose items are many), measured best of 2 to 4 groups and 1 to
 // 3 CTAs.
@@ -108,10 +88,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) fp8_stream_kernel
         const int k = (kb + u) * kFp8Group + 16 * t;
         s[u] = load_global(sw + kb + u);
         if (k - 16 * t + kFp8Group <= p.K) {
-          a[u][0] = load_weight(w0 + k);
-          a[u][1] = load_weight(w0 + k + 64);
-          a[u][2] = load_weight(w1 + k);
-          a[u][3] = load_weight(w1 + k + 64);
+          a[u][0] = load_streamed(w0 + k);
+          a[u][1] = load_streamed(w0 + k + 64);
+          a[u][2] = load_streamed(w1 + k);
+          a[u][3] = load_streamed(w1 + k + 64);
         } else {
           a[u][0] = load_tail(w0, k, p.K);
           a[u][1] = load_tail(w0, k + 64, p.K);
@@ -172,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) fp8_stream_kernel
 #pragma unroll
       for (int i = 0; i < 4; ++i) red[warp][j * 8 + 2 * t + (i & 1)][g + (i >> 1) * 8] = acc[j][i];
     __syncthreads();
-    constexpr int kLive = MODE == kFp8Naive ? 1 : kUnit;
+    constexpr int kLive = MODE == kNaive ? 1 : kUnit;
     for (int o = tid; o < kRowsCta * kLive; o += kThreads) {
       const int r = o % kRowsCta, c = o / kRowsCta, n = tile * kRowsCta + r;
       float v = 0.f;
@@ -207,9 +187,9 @@ int launch_nt(const Fp8Args &a, long long units, const DeviceInfo &dev, cudaStre
 
 }  // namespace
 
-int launch_fp8_stream(const Fp8Args &a, Fp8Mode mode, const DeviceInfo &dev, cudaStream_t stream) {
-  if (mode == kFp8Naive) return launch_nt<1, kFp8Naive>(a, a.pairs, dev, stream);
-  return a.pairs <= 8 ? launch_nt<1, kFp8Dense>(a, 1, dev, stream) : launch_nt<2, kFp8Dense>(a, 1, dev, stream);
+int launch_fp8_stream(const Fp8Args &a, ProductMode mode, const DeviceInfo &dev, cudaStream_t stream) {
+  if (mode == kNaive) return launch_nt<1, kNaive>(a, a.pairs, dev, stream);
+  return a.pairs <= 8 ? launch_nt<1, kDense>(a, 1, dev, stream) : launch_nt<2, kDense>(a, 1, dev, stream);
 }
 
 }  // namespace moe_lora
