@@ -596,6 +596,113 @@ int moe_fp8_grouped_matmul_naive(const moe_lora_fp8 *x, int x_per_pair, long lon
                                  long long ldy, const float *topk_weights, const int32_t *topk_ids, int M, int topk,
                                  int num_experts, int K, int N, int32_t *err_flag, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The same layer with base weights in bf16, and its router:
+ *
+ *   moe_bf16_matmul           router's projection: logits (fp32) = x . gate^T + bias
+ *   moe_route                 logits -> topk_ids, topk_weights
+ *   moe_align_block_size      topk_ids -> blocks
+ *   moe_bf16_grouped_matmul   w13, w2: as the 8-bit products above
+ *
+ * All products here compute
+ *   y[f][n] = weight[f] * act( sum_k x[r][k] * w[e][n][k] + bias[e][n] ) + residual[f][n]
+ * from bf16 x and w, in fp32, rounded once to y's type.  The tensor cores add
+ * exact products of two bf16 in fp32, over runs of at most 256 columns where y is fp32 or
+ * the kernel is one of those for few rows, else over all of K (each addition
+ * there may truncate); runs are added in ascending order, where K is split
+ * over a cluster's CTAs or a CTA's warps ascending within each share and then
+ * over the shares.  The same call gives the same bits.
+ * ------------------------------------------------------------------------ */
+
+/* Activations (act above).  SILU: v / (1 + exp(-v)); GELU: v * Phi(v), by erfc;
+ * GELU_TANH: 0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))). */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_SILU 2
+#define MOE_ACT_GELU 3
+#define MOE_ACT_GELU_TANH 4
+
+/*
+ * moe_bf16_matmul -- y = act(x . w^T + bias) + residual.
+ *   x [device] bf16 [M, ldx];  w [device] bf16 [N, ldw]
+ *   bias [device] bf16 or (bias_f32) fp32 [N], or NULL
+ *   residual [device] of y's type [M, ld_residual], or NULL; may be y (with its
+ *            leading dimension), and must not overlap y otherwise
+ *   y [device] bf16 or (y_f32) fp32 [M, ldy]
+ * Sizes: M >= 0, N >= 1, K >= 1; x and w on 16 bytes with ldx, ldw multiples of
+ * 8 (columns from K on are not used); bias, residual, y and their leading
+ * dimensions are not restricted beyond their type's alignment (rows on 16
+ * bytes are read and written 16 bytes at a time).
+ */
+int moe_bf16_matmul(const moe_lora_bf16 *x, long long ldx, const moe_lora_bf16 *w, long long ldw, const void *bias,
+                    int bias_f32, const void *residual, long long ld_residual, void *y, long long ldy, int y_f32,
+                    int activation, int M, int N, int K, int32_t *err_flag, void *stream);
+
+/*
+ * moe_bf16_grouped_matmul -- the product over a MoE layer's experts, on the
+ * blocks of moe_align_block_size: as moe_fp8_grouped_matmul, with bf16 rows and
+ * weights, a bias for each expert and an activation (y is bf16, no residual):
+ *   y[f][n] = bf16( (topk_weights ? topk_weights[f] : 1) * act( sum_k x[r][k] * w[e][n][k] + bias[e][n] ) )
+ *   x [device] bf16 [M, ldx] ([M*topk, ldx] when x_per_pair)
+ *   w [device] bf16 [num_experts, N, ldw];  bias [device] bf16 or fp32 [num_experts, N], or NULL
+ *   the rest, the workspace (moe_bf16_grouped_workspace_bytes) and the errors as
+ *   for moe_fp8_grouped_matmul, alignments as for moe_bf16_matmul.
+ */
+int moe_bf16_grouped_matmul(const moe_lora_bf16 *x, int x_per_pair, long long ldx, const moe_lora_bf16 *w,
+                            long long ldw, const void *bias, int bias_f32, moe_lora_bf16 *y, long long ldy,
+                            int activation, const float *topk_weights, const int32_t *sorted_token_ids,
+                            const int32_t *expert_ids, const int32_t *num_tokens_post_padded, int M, int topk,
+                            int num_experts, int K, int N, int block_size, int max_num_tokens_padded,
+                            int max_num_m_blocks, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                            void *stream);
+
+/* Bytes of workspace of a moe_bf16_grouped_matmul call with these sizes (0:
+ * none, or invalid sizes).  Host only. */
+size_t moe_bf16_grouped_workspace_bytes(int M, int topk, int num_experts, int K, int N, int block_size);
+
+/* moe_bf16_grouped_matmul_naive -- the same without an align, as
+ * moe_fp8_grouped_matmul_naive. */
+int moe_bf16_grouped_matmul_naive(const moe_lora_bf16 *x, int x_per_pair, long long ldx, const moe_lora_bf16 *w,
+                                  long long ldw, const void *bias, int bias_f32, moe_lora_bf16 *y, long long ldy,
+                                  int activation, const float *topk_weights, const int32_t *topk_ids, int M, int topk,
+                                  int num_experts, int K, int N, int32_t *err_flag, void *stream);
+
+/* Scorings and limits of moe_route. */
+#define MOE_ROUTE_SOFTMAX 0
+#define MOE_ROUTE_SIGMOID 1
+#define MOE_ROUTE_MAX_TOPK 32
+#define MOE_ROUTE_MAX_GROUPS 32
+
+/*
+ * moe_route -- each token's top-k experts and their weights, from its logits:
+ *   s[e] = softmax over the experts of logits[m], or (SIGMOID) 1 / (1 + exp(-logits[m][e]))
+ *   c[e] = s[e] + bias[e]          the choice; without a bias the logits decide, in whose order s is
+ *   topk_ids[m]     = the topk experts with the largest c, in descending order, the lowest index first among equals
+ *   topk_weights[m] = s[id] of each, divided by their sum when `renormalize` (and the sum is not zero), times scale
+ * With num_groups > topk_groups, only the experts of topk_groups of num_groups
+ * equal groups of neighbours are candidates: those groups whose group_best (1 or 2)
+ * largest c have the largest sum, the lowest index first among equals.
+ * The order is that of c in 64-bit arithmetic; the weights are computed in fp32
+ * (within 2^-19 of their value) or better.
+ * An expert whose logit (or c) is -inf or NaN is no candidate: it comes after
+ * all candidates, as those of the other groups do, by index, with a weight of
+ * zero; a row of nothing else has weights of zero.  A row with a NaN logit, or a
+ * NaN bias, or (SOFTMAX) a logit of +inf, has NaN weights.  The ids of a row are always
+ * distinct and in [0, num_experts).
+ *
+ *   logits       [device] bf16 or (logits_f32) fp32 [M, ld_logits]
+ *   bias         [device] fp32 [num_experts], or NULL
+ *   topk_ids     [device] int32 [M, topk], written: moe_lora_align's and the products' input
+ *   topk_weights [device] fp32 [M, topk], written
+ * Sizes: M >= 0; num_experts <= 1024; topk <= MOE_ROUTE_MAX_TOPK and no more
+ * than the chosen groups' experts; num_groups divides num_experts and is at most
+ * MOE_ROUTE_MAX_GROUPS; topk_groups <= num_groups; ld_logits >= num_experts.  Any alignment of the
+ * elements; rows on 16 bytes are read faster.
+ */
+int moe_route(const void *logits, int logits_f32, long long ld_logits, const float *bias, int scoring, int renormalize,
+              float scale, int num_groups, int topk_groups, int group_best, int32_t *topk_ids, float *topk_weights, int M,
+              int num_experts, int topk, void *stream);
+
 /* Human-readable name of a moe_lora_status value (static string). */
 const char *moe_lora_status_string(int status);
 

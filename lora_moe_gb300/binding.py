@@ -20,6 +20,8 @@ from . import build as _build
 
 MOE_LORA_OK = 0
 ALIGN_AUTO, ALIGN_SMEM, ALIGN_GLOBAL, ALIGN_CLUSTER = 0, 1, 2, 3
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
 PATH_AUTO, PATH_CUDA_CORE, PATH_TCGEN05, PATH_CUDA_CORE_CLUSTER, PATH_CUDA_CORE_STREAM = 0, 1, 2, 3, 4
 DEVERR_EXPERT_ID, DEVERR_LORA_ID, DEVERR_CAPACITY, DEVERR_PAIR_ID, DEVERR_TIMEOUT = 1, 2, 4, 8, 16
 
@@ -99,6 +101,17 @@ def lib() -> ctypes.CDLL:
             L.moe_fp8_grouped_workspace_bytes.argtypes = [I, I, I, I, I, I]
             L.moe_fp8_grouped_matmul_naive.restype = I
             L.moe_fp8_grouped_matmul_naive.argtypes = [P, I, Q, P, P, Q, P, P, Q, P, P, I, I, I, I, I, P, P]
+            L.moe_route.restype = I
+            L.moe_route.argtypes = [P, I, Q, P, I, I, F, I, I, I, P, P, I, I, I, P]
+            L.moe_bf16_matmul.restype = I
+            L.moe_bf16_matmul.argtypes = [P, Q, P, Q, P, I, P, Q, P, Q, I, I, I, I, I, P, P]
+            L.moe_bf16_grouped_matmul.restype = I
+            L.moe_bf16_grouped_matmul.argtypes = [P, I, Q, P, Q, P, I, P, Q, I, P, P, P, P, I, I, I, I, I, I, I, I, P, S,
+                                                  P, P]
+            L.moe_bf16_grouped_workspace_bytes.restype = S
+            L.moe_bf16_grouped_workspace_bytes.argtypes = [I, I, I, I, I, I]
+            L.moe_bf16_grouped_matmul_naive.restype = I
+            L.moe_bf16_grouped_matmul_naive.argtypes = [P, I, Q, P, Q, P, I, P, Q, I, P, P, I, I, I, I, I, P, P]
             _lib = L
     return _lib
 
@@ -373,12 +386,12 @@ class _NoFast:
     def norm(*args):
         return None
 
-    act = matmul = grouped = naive = norm
+    act = matmul = grouped = naive = route = matmul16 = grouped16 = naive16 = norm
 
 
 def _load_fast():
-    """fastcall's functions (a compiled module): they take the common case of the 8-bit
-    operators' calls (ordinary tensors on the current device, its current
+    """fastcall's functions (a compiled module): they take the common case of the
+    serving operators' calls (ordinary tensors on the current device, its current
     stream) and return None for any other, which the functions below treat."""
     global _fast
     L = lib()
@@ -391,12 +404,15 @@ def _load_fast():
                     fast = importlib.util.module_from_spec(spec)
                     spec.loader.exec_module(fast)
                 except ImportError as e:
-                    warnings.warn("the 8-bit operators' calls go through ctypes: %s" % e)
+                    warnings.warn("the serving operators' calls go through ctypes: %s" % e)
                     fast = None
             if fast is not None:
                 fast.bind(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
                     L.moe_add_rms_norm_fp8, L.moe_silu_mul_fp8, L.moe_fp8_matmul, L.moe_fp8_grouped_matmul,
                     L.moe_fp8_grouped_matmul_naive, L.moe_fp8_grouped_workspace_bytes)])
+                fast.bind16(*[ctypes.cast(f, ctypes.c_void_p).value for f in (
+                    L.moe_route, L.moe_bf16_matmul, L.moe_bf16_grouped_matmul, L.moe_bf16_grouped_matmul_naive,
+                    L.moe_bf16_grouped_workspace_bytes)])
                 _fast = fast
             else:
                 _fast = _NoFast
@@ -580,6 +596,19 @@ def fp8_grouped_workspace_bytes(M, topk, num_experts, K, N, block_size) -> int:
     return lib().moe_fp8_grouped_workspace_bytes(M, topk, num_experts, K, N, block_size)
 
 
+def _take_workspace(nbytes, y, stream, raw):
+    """nbytes of torch's allocator for a call on `stream` (raw: its handle)."""
+    if not nbytes:
+        return None
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=y.device)
+    if stream is not None:
+        # the allocator's earlier work on this memory is ordered on the current stream, its next on either
+        side = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, y.device)
+        side.wait_stream(torch.cuda.current_stream(y.device))
+        workspace.record_stream(side)
+    return workspace
+
+
 def moe_fp8_grouped_matmul(x, x_scales, w, w_scales, y, sorted_token_ids, expert_ids, num_tokens_post_padded,
                            block_size, topk_weights=None, x_per_pair=False, workspace=None, err_flag=None,
                            stream=None):
@@ -610,13 +639,7 @@ def moe_fp8_grouped_matmul(x, x_scales, w, w_scales, y, sorted_token_ids, expert
     nbytes = 0
     if workspace is None:
         nbytes = L.moe_fp8_grouped_workspace_bytes(M, topk, E, K, N, block_size)
-        if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=y.device)
-            if stream is not None:
-                # the allocator's earlier work on this memory is ordered on the current stream, its next on either
-                side = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, y.device)
-                side.wait_stream(torch.cuda.current_stream(y.device))
-                workspace.record_stream(side)
+        workspace = _take_workspace(nbytes, y, stream, raw)
     else:
         nbytes = workspace.numel() * workspace.element_size()
     _check(L.moe_fp8_grouped_matmul(
@@ -638,6 +661,135 @@ def moe_fp8_grouped_matmul_naive(x, x_scales, w, w_scales, y, topk_ids, topk_wei
     _check_device(stream, x, x_scales, w, w_scales, y, topk_weights, topk_ids, err_flag)
     _check((_lib or lib()).moe_fp8_grouped_matmul_naive(*operands, pids, M, topk, E, K, N, perr, _raw_stream(stream, y)),
            "moe_fp8_grouped_matmul_naive")
+
+
+def _either(t, name, numel):
+    """Address of a contiguous bf16 or fp32 CUDA tensor, and whether it is fp32 (None: none)."""
+    if t is None:
+        return None, 0
+    if t.dtype is not _BF16 and t.dtype is not _F32:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
+    return _dense(t, t.dtype, name, numel), int(t.dtype is _F32)
+
+
+def moe_route(logits, topk_ids, topk_weights, bias=None, scoring=ROUTE_SOFTMAX, renormalize=True, scale=1.0,
+              num_groups=1, topk_groups=1, group_best=1, stream=None):
+    """Each token's top-k experts and their weights; see include/moe_lora.h.
+
+    logits: bf16 or float32 [M, E], rows may be strided.  topk_ids: int32 [M,
+    topk] and topk_weights: float32 [M, topk], written.  bias: float32 [E] or
+    None, added to the scores for the choice alone.  scoring: ROUTE_SOFTMAX or
+    ROUTE_SIGMOID."""
+    if stream is None:
+        st = (_fast or _load_fast()).route(logits, topk_ids, topk_weights, bias, scoring, renormalize, scale, num_groups,
+                                           topk_groups, group_best)
+        if st is not None:
+            return _check(st, "moe_route")
+    M, E = logits.shape
+    topk = topk_ids.shape[-1]
+    if logits.dtype is not _BF16 and logits.dtype is not _F32:
+        raise TypeError("logits must be bfloat16 or float32, got %s" % logits.dtype)
+    pl, ld = _rows(logits, logits.dtype, "logits", M, E)
+    pi, pw = _dense(topk_ids, _I32, "topk_ids", M * topk), _dense(topk_weights, _F32, "topk_weights", M * topk)
+    pb = _dense(bias, _F32, "bias", E)
+    _check_device(stream, logits, topk_ids, topk_weights, bias)
+    _check((_lib or lib()).moe_route(pl, int(logits.dtype is _F32), max(ld, E), pb, scoring, int(bool(renormalize)), scale,
+                                     num_groups, topk_groups, group_best, pi, pw, M, E, topk,
+                                     _raw_stream(stream, topk_ids)), "moe_route")
+
+
+def moe_bf16_matmul(x, w, y, bias=None, residual=None, activation=ACT_NONE, err_flag=None, stream=None):
+    """y = activation(x @ w.T + bias) + residual; see include/moe_lora.h.
+
+    x: bf16 [M, K]; w: bf16 [N, K]; y: bf16 or float32 [M, N]; bias: bf16 or
+    float32 [N] or None; residual: of y's type, [M, N], or None (may be y).
+    Rows of x, w, residual and y may be strided (x, w: by multiples of 8).
+    activation: ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU or ACT_GELU_TANH."""
+    if stream is None:
+        st = (_fast or _load_fast()).matmul16(x, w, y, bias, residual, activation, err_flag)
+        if st is not None:
+            return _check(st, "moe_bf16_matmul")
+    M, N = y.shape
+    K = x.shape[-1]
+    if y.dtype is not _BF16 and y.dtype is not _F32:
+        raise TypeError("y must be bfloat16 or float32, got %s" % y.dtype)
+    px, ldx = _rows(x, _BF16, "x", M, K)
+    pw, ldw = _rows(w, _BF16, "w", N, K)
+    py, ldy = _rows(y, y.dtype, "y", M, N)
+    pr, ldr = (None, 0) if residual is None else _rows(residual, y.dtype, "residual", M, N)
+    pb, bias_f32 = _either(bias, "bias", N)
+    perr = _dense(err_flag, _I32, "err_flag")
+    _check_device(stream, x, w, y, bias, residual, err_flag)
+    _check((_lib or lib()).moe_bf16_matmul(px, ldx, pw, ldw, pb, bias_f32, pr, ldr, py, ldy, int(y.dtype is _F32),
+                                           activation, M, N, K, perr, _raw_stream(stream, y)), "moe_bf16_matmul")
+
+
+def _grouped16_operands(x, w, y, bias, activation, topk_weights, x_per_pair):
+    M, topk, N = y.shape
+    E, _, K = w.shape
+    px, ldx = _rows(x, _BF16, "x", M * topk if x_per_pair else M, K)
+    pw, ldw = _rows(w, _BF16, "w", E * N, K)
+    py, ldy = _rows(y, _BF16, "y", M * topk, N)
+    pb, bias_f32 = _either(bias, "bias", E * N)
+    return M, topk, E, K, N, (px, 1 if x_per_pair else 0, ldx, pw, ldw, pb, bias_f32, py, ldy, activation,
+                              _dense(topk_weights, _F32, "topk_weights", M * topk))
+
+
+def bf16_grouped_workspace_bytes(M, topk, num_experts, K, N, block_size) -> int:
+    """Bytes of workspace of a moe_bf16_grouped_matmul call with these sizes."""
+    return lib().moe_bf16_grouped_workspace_bytes(M, topk, num_experts, K, N, block_size)
+
+
+def moe_bf16_grouped_matmul(x, w, y, sorted_token_ids, expert_ids, num_tokens_post_padded, block_size, bias=None,
+                            activation=ACT_NONE, topk_weights=None, x_per_pair=False, workspace=None, err_flag=None,
+                            stream=None):
+    """activation(x @ w[e].T + bias[e]) over a MoE layer's experts, on
+    moe_align_block_size's blocks; see include/moe_lora.h.
+
+    x: bf16 [M, K] ([M*topk, K] with x_per_pair); w: bf16 [E, N, K]; bias: bf16
+    or float32 [E, N] or None; y: bf16 [M, topk, N], written in place for every
+    pair of a block and no other (zero it first where the align drops pairs and
+    all rows are read); topk_weights: float32 [M, topk] or None.  workspace: a
+    uint8 tensor of at least bf16_grouped_workspace_bytes(...) bytes; without
+    one, calls that need one take it from torch's allocator."""
+    if stream is None and workspace is None:
+        st = (_fast or _load_fast()).grouped16(x, w, y, bias, activation, topk_weights, bool(x_per_pair), err_flag,
+                                               sorted_token_ids, expert_ids, num_tokens_post_padded, block_size)
+        if st is not None:
+            return _check(st, "moe_bf16_grouped_matmul")
+    M, topk, E, K, N, operands = _grouped16_operands(x, w, y, bias, activation, topk_weights, x_per_pair)
+    blocks = [_dense(t, _I32, name) for t, name in (
+        (sorted_token_ids, "sorted_token_ids"), (expert_ids, "expert_ids"),
+        (num_tokens_post_padded, "num_tokens_post_padded"))]
+    perr = _dense(err_flag, _I32, "err_flag")
+    _check_device(stream, x, w, y, bias, topk_weights, sorted_token_ids, expert_ids, num_tokens_post_padded, workspace,
+                  err_flag)
+    L = _lib or lib()
+    raw = _raw_stream(stream, y)
+    if workspace is None:
+        nbytes = L.moe_bf16_grouped_workspace_bytes(M, topk, E, K, N, block_size)
+        workspace = _take_workspace(nbytes, y, stream, raw)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _check(L.moe_bf16_grouped_matmul(
+        *operands, *blocks, M, topk, E, K, N, block_size, sorted_token_ids.numel(), expert_ids.numel(),
+        None if workspace is None else _dense(workspace, workspace.dtype, "workspace"), nbytes, perr, raw),
+        "moe_bf16_grouped_matmul")
+
+
+def moe_bf16_grouped_matmul_naive(x, w, y, topk_ids, bias=None, activation=ACT_NONE, topk_weights=None,
+                                  x_per_pair=False, err_flag=None, stream=None):
+    """moe_bf16_grouped_matmul without an align, one work item per (token,
+    top-k) pair; topk_ids: int32 [M, topk]."""
+    if stream is None:
+        st = (_fast or _load_fast()).naive16(x, w, y, bias, activation, topk_weights, bool(x_per_pair), err_flag, topk_ids)
+        if st is not None:
+            return _check(st, "moe_bf16_grouped_matmul_naive")
+    M, topk, E, K, N, operands = _grouped16_operands(x, w, y, bias, activation, topk_weights, x_per_pair)
+    pids, perr = _dense(topk_ids, _I32, "topk_ids", M * topk), _dense(err_flag, _I32, "err_flag")
+    _check_device(stream, x, w, y, bias, topk_weights, topk_ids, err_flag)
+    _check((_lib or lib()).moe_bf16_grouped_matmul_naive(*operands, pids, M, topk, E, K, N, perr, _raw_stream(stream, y)),
+           "moe_bf16_grouped_matmul_naive")
 
 
 class AlignBuffers:

@@ -2,7 +2,7 @@
 
 Translation units are compiled in parallel, then linked into
 lora_moe_gb300/_build/libmoe_lora.so.  Beside it, where Python's headers and
-torch are installed, fastcall.*.so: the 8-bit operators' calls from Python
+torch are installed, fastcall.*.so: the serving operators' calls from Python
 without ctypes (a C++ extension, named by the Python and the torch that it was
 built against).  Where it does not build, a warning says so and the calls go
 through ctypes.
@@ -26,7 +26,8 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmoe_lora.so")
 SOURCES = ["api.cu", "align.cu", "fused_cuda_core.cu", "fused_tcgen05.cu", "stream_pipeline.cu",
            "fused_stream_cluster.cu", "align_static_workspace.cu", "api_fp8.cu", "fp8_rows.cu", "fp8_matmul.cu", "fp8_stream.cu",
-           "gather.cu"]
+           "gather.cu", "api_bf16.cu", "bf16_matmul.cu", "bf16_stream.cu",
+           "api_route.cu", "route.cu"]
 
 
 def _torch_version():
@@ -86,7 +87,7 @@ def _try_fastcall():
     except Exception as e:
         with open(FASTCALL + ".failed", "w") as f:
             f.write(str(e))
-        warnings.warn("the 8-bit operators' calls go through ctypes: %s" % e)
+        warnings.warn("the serving operators' calls go through ctypes: %s" % e)
 
 
 def _fastcall_settled():
