@@ -8,13 +8,13 @@
 //
 // Two kernels, both persistent, with a warp that loads (TMA), one that issues
 // the MMAs and epilogue warps:
-//   narrow  the weight on the 128 rows of the MMA, 16 to 128 pairs on its
+//   narrow  the weight on the 128 rows of the MMA, 16 to 64 pairs on its
 //           columns: few pairs for each weight (decode), bound by the weight's
 //           bytes.  Where there are few items, clusters of CTAs split K, their
 //           partial sums exchanged through distributed shared memory and added
 //           in a fixed order.
-//   wide    pairs of CTAs (cta_group::2), 256 pairs by 256 output columns, on
-//           rows gathered into the blocks' order: bound by the tensor cores.
+//   wide    pairs of CTAs (cta_group::2), 256 of the weight's rows by up to 256
+//           pairs, on rows gathered into the blocks' order: bound by the tensor cores.
 // Products of few rows and small weights are bf16_stream.cu's.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -40,13 +40,15 @@ constexpr int kTileBytes = kRows * kGroupBytes;   // 128 rows of one group: 16 K
 struct Bf16Maps {
   CUtensorMap w;   // [E][N][K] in bytes, box 1 x 128 x 128
   CUtensorMap x;   // [rows][K], box BT x 128 (dense), 1 x 128 (gathered by row) or 128 x 128 (wide)
+  CUtensorMap x16; // the same, box 16 x 128 (wide)
 };
 
 // Launch shape of a call.
 struct Bf16Cfg {
   int stages;      // operand ring
   int nt;          // output tiles along N
-  int cluster;     // CTAs that split K (narrow)
+  int cluster;     // CTAs of a cluster, which splits K
+  int tile_rows;   // pairs of a tile (wide, dense)
   int off_red, off_list, off_ctrl;
   int list;        // units that the list of live ones holds (0: none is made)
   int smem_bytes;
@@ -63,7 +65,7 @@ template <int BT>
 struct Narrow {
   static constexpr int kGroup = kTileBytes + BT * kGroupBytes;
   static constexpr int kStage = 2 * kGroup;           // two groups a stage, requested together
-  static constexpr int kBufs = BT == 128 ? 2 : 4;     // accumulators in tensor memory
+  static constexpr int kBufs = 4;                     // accumulators in tensor memory
   static constexpr int kCols = kBufs * BT;            // power of two, >= 32
   static constexpr int kRedBytes = BT * kRows * 4;    // every rank's partial sums of this CTA's columns
 };
@@ -285,67 +287,64 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
 
 // ------------------------------------------------------------------ wide
 
-// Pairs of CTAs (cta_group::2), 256 rows by 256 output columns.  Each CTA holds
-// 128 of the rows and 128 of the weight's in shared memory, 32 KB a group, and
-// 128 x 256 of an accumulator in tensor memory, twice: one is read while the
-// next item's is added up.
+// Pairs of CTAs (cta_group::2): 256 of the weight's rows on the rows of the MMA,
+// up to 256 pairs on its columns (as many as the tile has, in steps of 32: MMAs
+// of a partly filled tile take less).  Each CTA holds 128 of the weight's rows
+// and half of the pairs', at most 32 KB a group, and 128 x 256 of an
+// accumulator in tensor memory, twice.
+//
+// CHUNKED = false: an accumulator takes all of K; one is read while the next
+// item's is added up.  CHUNKED: an accumulator takes a chunk of K, and the
+// epilogue adds the chunks in registers (fp32 outputs, see kChunk).  A cluster
+// of several pairs splits K where there are few items: each pair's sums go to
+// the pair that owns the columns, in the operand ring's memory.
 constexpr int kWideThreads = 384;
 constexpr int kWideN = 256;
 constexpr int kHalf = kWideN / 2;
-constexpr int kWideStage = 2 * kTileBytes;       // 128 rows, and 128 of the weight
+constexpr int kWideStage = 2 * kTileBytes;       // 128 of the weight's rows, and of the pairs'
 constexpr int kWideStages = 6;
-constexpr int kWideOut = 32 * 128;               // an epilogue warp's sums on their way out: 32 rows of 32 fp32
+constexpr int kPart = 32;                        // columns of an accumulator that a warp takes at a time
+constexpr int kParts = kTileRows / kPart / 2;    // of one of the two warps of a lane quarter
+// Rows of tiles that are neighbours in the order of the items: the pairs' rows
+// of so many tiles stay in L2 while the weight goes by (Mixtral-shaped w13
+// prefill reads 134 MB of rows 112 times otherwise).
+constexpr int kRaster = 16;
+// Registers a thread where chunks are added: loading and MMA warps, epilogue warps.
+constexpr int kWideRegsIssue = 56, kWideRegsEpilogue = 216;
 
 struct WideCtrl {
   uint64_t full[kWideStages], empty[kWideStages];
   uint64_t tfull[2], tempty[2];
-  uint64_t done;   // every MMA of the pair
+  uint64_t done;       // every MMA of the pair
+  uint64_t red_full;   // the other pairs' sums
   uint32_t tmem;
   int abort;
 };
 
-// 8 columns of a row of y (or of the residual, which is alike) from n on, `cols`
-// of which exist.
-__device__ __forceinline__ void load_columns(const void *p, long long at, int f32, bool whole, int cols, float (&v)[8]) {
-  if (whole && f32) {
-    const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
-    const float4 lo = load_global(s), hi = load_global(s + 1);
-    v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
-  } else if (whole) {
-    const uint4 u = load_global(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < cols ? load_as_f32(p, at + i, f32) : 0.f;
+// The items of a pair: tiles of rows in groups of kRaster, within a group the
+// weight's tiles one after the other.
+struct WideWork {
+  int ntiles, nt_all, it, step, items;
+  int t, nt;   // of the item
+  __device__ __forceinline__ WideWork(int tiles, int nts, int first, int stride)
+      : ntiles(tiles), nt_all(nts), it(first - stride), step(stride), items(tiles * nts) {}
+  __device__ __forceinline__ bool advance() {
+    it += step;
+    if (it >= items) return false;
+    const int g = it / (kRaster * nt_all), r = it - g * kRaster * nt_all, size = min(kRaster, ntiles - g * kRaster);
+    nt = r / size;
+    t = g * kRaster + r - nt * size;
+    return true;
   }
-}
-__device__ __forceinline__ void store_columns(void *p, long long at, int f32, bool whole, int cols, const float (&v)[8]) {
-  if (whole && f32) {
-    float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(p) + at);
-    d[0] = make_float4(v[0], v[1], v[2], v[3]);
-    d[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else if (whole) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < cols) {
-        if (f32) static_cast<float *>(p)[at + i] = v[i];
-        else static_cast<uint16_t *>(p)[at + i] = float_to_bf16_bits(v[i]);
-      }
-  }
-}
-// Whether rows of p, ld elements apart, start on 16 bytes.
-__device__ __forceinline__ bool rows_on_16(const void *p, long long ld, int f32) {
-  return (ld & (f32 ? 3 : 7)) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+};
+
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
-template <int MODE>
+template <int MODE, bool CHUNKED>
 __global__ void __launch_bounds__(kWideThreads, 1)
     bf16_wide_kernel(const __grid_constant__ Bf16Maps maps, const Bf16Args p, const WideTile *tiles, const Bf16Cfg cfg) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -353,6 +352,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   WideCtrl &ctl = *reinterpret_cast<WideCtrl *>(smem + cfg.off_ctrl);
   volatile int *abort = &ctl.abort;
   const int rank = blockIdx.x & 1;   // rank 0 issues the pair's MMAs
+  // the pair in its cluster, and its share of K
+  const int pairs = CHUNKED ? cfg.cluster >> 1 : 1, q = CHUNKED ? (blockIdx.x >> 1) % pairs : 0;
+  const int kb0 = (int)((long long)p.KB * q / pairs), kb1 = (int)((long long)p.KB * (q + 1) / pairs);
+  const int leader = q * 2;          // the pair's rank 0 in the cluster
 
   if (tid == 0) {
     for (int s = 0; s < kWideStages; ++s) {
@@ -364,10 +367,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       mbar_init(&ctl.tempty[s], 16);   // the epilogue warps of both CTAs
     }
     mbar_init(&ctl.done, 1);
+    mbar_init(&ctl.red_full, 1);
     ctl.abort = 0;
     fence_barrier_init();
     prefetch_tensor_map(&maps.w);
     prefetch_tensor_map(&maps.x);
+    prefetch_tensor_map(&maps.x16);
   }
   if (warp == 1) tmem_alloc_pair(&ctl.tmem, 512);
   tc_fence_before();
@@ -377,151 +382,248 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   tc_fence_after();
   wait_for_prior_grid();
   const uint32_t tmem = ctl.tmem;
-  const int ntiles = MODE == kDense ? (p.pairs + kTileRows - 1) / kTileRows : load_global(&tiles[0].row0);
-  const int items = ntiles * cfg.nt;   // rows fastest: pairs at work share the weight's columns
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int height = cfg.tile_rows;   // of a dense call's tiles
+  const int ntiles = MODE == kDense ? (p.pairs + height - 1) / height : load_global(&tiles[0].row0);
+  WideWork wk(ntiles, cfg.nt, blockIdx.x / (2 * pairs), gridDim.x / (2 * pairs));
   auto tile = [&](int t) {
-    if (MODE == kDense) return WideTile{t * kTileRows, min(kTileRows, p.pairs - t * kTileRows), 0, 0};
+    if (MODE == kDense) return WideTile{t * height, min(height, p.pairs - t * height), 0, 0};
     const int4 v = load_global(reinterpret_cast<const int4 *>(tiles) + 1 + t);
     return WideTile{v.x, v.y, v.z, 0};
   };
+  auto columns = [](int rows) { return (rows + kPart - 1) / kPart * kPart; };   // of the MMA
 
-  if (warp == 0) {
-    // ---------------- operands: this CTA's half of the rows, and of the weight's
-    const uint32_t full0 = cluster_map(smem_addr(&ctl.full[0]), 0);   // rank 0's
-    int s = 0;
-    uint32_t ph = 0, fills = 0;
-    bool go = true;   // falls with a wait that gave up: nothing more is requested
-    for (int it = first; go && it < items; it += step) {
-      const int nt = it / ntiles;
-      const WideTile t = tile(it - nt * ntiles);
-      const bool have = t.rows > rank * kRows;
-      const uint32_t bytes = 2 * kTileBytes + (t.rows > kRows ? 2 : 1) * kTileBytes;
-      for (int kb = 0; kb < p.KB; ++kb) {
-        go = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl.empty[s], ph ^ 1, abort, p.err));
-        if (!go) break;
-        ++fills;
-        uint8_t *st = smem + (size_t)s * kWideStage;
-        if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(&ctl.full[s], bytes);
-          if (have) tma_load_2d_pair(st, &maps.x, kb * kGroupBytes, t.row0 + rank * kRows, full0 + s * 8);
-          tma_load_3d_pair(st + kTileBytes, &maps.w, kb * kGroupBytes, nt * kWideN + rank * kHalf, t.expert, full0 + s * 8);
+  if (warp < 4) {
+    if (CHUNKED) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideRegsIssue));
+    if (warp == 0) {
+      // ---------------- operands: this CTA's half of the weight's rows, and of the pairs'
+      const uint32_t full0 = cluster_map(smem_addr(&ctl.full[0]), leader);
+      int s = 0;
+      uint32_t ph = 0, fills = 0;
+      bool go = true;   // falls with a wait that gave up: nothing more is requested
+      while (go && wk.advance()) {
+        const WideTile t = tile(wk.t);
+        const int half = columns(t.rows) / 2, row0 = t.row0 + rank * half;
+        const uint32_t bytes = 2 * kTileBytes + 2 * half * kGroupBytes;
+        // two groups at a time: 256 consecutive bytes of each row
+        for (int kb = kb0; kb < kb1; kb += 2) {
+          const int n = min(2, kb1 - kb);
+          const int s1 = s + 1 == kWideStages ? 0 : s + 1;
+          const uint32_t ph1 = s + 1 == kWideStages ? ph ^ 1 : ph;
+          bool ok = mbar_wait(&ctl.empty[s], ph ^ 1, abort, p.err);
+          if (n > 1) ok = mbar_wait(&ctl.empty[s1], ph1 ^ 1, abort, p.err) && ok;
+          go = __all_sync(0xFFFFFFFFu, ok);
+          if (!go) break;
+          fills += n;
+          if (elect_one()) {
+            for (int i = 0; i < n; ++i) {
+              const int at = i ? s1 : s;
+              if (rank == 0) mbar_arrive_expect_tx(&ctl.full[at], bytes);
+              tma_load_3d_pair(smem + (size_t)at * kWideStage, &maps.w, (kb + i) * kGroupBytes,
+                               wk.nt * kWideN + rank * kRows, t.expert, full0 + at * 8);
+            }
+            for (int i = 0; i < n; ++i) {
+              const int at = i ? s1 : s;
+              uint8_t *st = smem + (size_t)at * kWideStage + kTileBytes;
+              if (half == kRows) {
+                tma_load_2d_pair(st, &maps.x, (kb + i) * kGroupBytes, row0, full0 + at * 8);
+              } else {
+                for (int r = 0; r < half; r += 16)
+                  tma_load_2d_pair(st + r * kGroupBytes, &maps.x16, (kb + i) * kGroupBytes, row0 + r, full0 + at * 8);
+              }
+            }
+          }
+          __syncwarp();
+          s = n > 1 ? s1 : s;
+          ph = n > 1 ? ph1 : ph;
+          if (++s == kWideStages) { s = 0; ph ^= 1; }
         }
-        __syncwarp();
-        if (++s == kWideStages) { s = 0; ph ^= 1; }
       }
-    }
-    // The pair's copies have landed (rank 0's barriers count both CTAs'), the
-    // hand-backs of the last stages have arrived here and the MMAs have
-    // completed before the pair exits: the epilogue waits for neither.
-    __syncwarp();
-    if (lane == 0) {
-      if (rank == 0) drain_ring(ctl.full, kWideStages, fills);
-      drain_ring(ctl.empty, kWideStages, fills);
-      drain_wait(&ctl.done, 0);
-    }
-    __syncwarp();
-  } else if (warp == 1 && rank == 0) {
-    // ---------------- MMA, for both CTAs
-    constexpr uint32_t idesc = make_idesc_bf16(2 * kRows, kWideN);
-    const uint64_t desc0 = make_sdesc_sw128(smem_addr(smem));   // (addresses in units of 16 bytes)
-    int s = 0, a = 0;
-    uint32_t ph = 0, aph = 0;
-    for (int it = first; it < items; it += step) {
-      mbar_wait(&ctl.tempty[a], aph ^ 1, abort, p.err);
-      for (int kb = 0; kb < p.KB; ++kb) {
-        mbar_wait(&ctl.full[s], ph, abort, p.err);
-        tc_fence_after();
-        const uint64_t dx = desc0 + s * (kWideStage >> 4), dw = dx + (kTileBytes >> 4);
-        if (elect_one()) {
+      // The pair's copies have landed (rank 0's barriers count both CTAs'), the
+      // hand-backs of the last stages have arrived here and the MMAs have
+      // completed before the pair exits: the epilogue waits for neither.
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) drain_ring(ctl.full, kWideStages, fills);
+        drain_ring(ctl.empty, kWideStages, fills);
+        drain_wait(&ctl.done, 0);
+      }
+    } else if (warp == 1 && rank == 0) {
+      // ---------------- MMA, for both CTAs
+      const uint64_t desc0 = make_sdesc_sw128(smem_addr(smem));   // (addresses in units of 16 bytes)
+      const uint16_t both = (uint16_t)(3u << leader);
+      int s = 0, a = 0;
+      uint32_t ph = 0, aph = 0;
+      bool more = wk.advance();
+      int rows = more ? tile(wk.t).rows : 0;
+      while (more) {
+        const uint32_t idesc = make_idesc_bf16(2 * kRows, columns(rows));
+        more = wk.advance();
+        rows = more ? tile(wk.t).rows : 0;   // the next item's, on its way meanwhile
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const int at = CHUNKED ? (kb - kb0) % kChunk : kb;
+          const bool last = kb + 1 == kb1 || (CHUNKED && at == kChunk - 1);   // of the accumulator
+          if (at == 0) mbar_wait(&ctl.tempty[a], aph ^ 1, abort, p.err);
+          mbar_wait(&ctl.full[s], ph, abort, p.err);
+          tc_fence_after();
+          const uint64_t dw = desc0 + s * (kWideStage >> 4), dx = dw + (kTileBytes >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kBf16Group / 16; ++k)
-            tc_mma_bf16_pair(tmem + a * kWideN, dx + k * 2, dw + k * 2, idesc, kb > 0 || k > 0);
-          tc_commit_pair(&ctl.empty[s]);
-          if (kb + 1 == p.KB) tc_commit_pair(&ctl.tfull[a]);
+            for (int k = 0; k < kBf16Group / 16; ++k)
+              tc_mma_bf16_pair(tmem + a * kTileRows, dw + k * 2, dx + k * 2, idesc, at > 0 || k > 0);
+            tc_commit_pair(&ctl.empty[s], both);
+            if (last) tc_commit_pair(&ctl.tfull[a], both);
+          }
+          __syncwarp();
+          if (++s == kWideStages) { s = 0; ph ^= 1; }
+          if (last) {
+            a ^= 1;
+            if (a == 0) aph ^= 1;
+          }
         }
-        __syncwarp();
-        if (++s == kWideStages) { s = 0; ph ^= 1; }
       }
-      a ^= 1;
-      if (a == 0) aph ^= 1;
+      if (elect_one()) tc_commit_pair(&ctl.done, both);
     }
-    if (elect_one()) tc_commit_pair(&ctl.done);
     __syncwarp();
-  } else if (warp >= 4) {
-    // ---------------- epilogue: 32 rows, and 128 of the output columns, a warp
+    if (CHUNKED && pairs > 1) {   // the ring is free for other pairs' sums
+      cluster_arrive_release();
+      cluster_wait();
+    }
+  } else {
+    if (CHUNKED) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWideRegsEpilogue));
+    // ---------------- epilogue: this thread's weight row; 32 pairs at a time, every other 32 of the tile's
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t lane_addr = tmem + ((uint32_t)quarter << 21) + half * kHalf;
-    const uint32_t tempty0 = cluster_map(smem_addr(&ctl.tempty[0]), 0);   // rank 0's
-    uint8_t *out = smem + kWideStages * kWideStage + (warp - 4) * kWideOut;
-    const bool y16 = rows_on_16(p.y, p.ldy, p.y_f32), r16 = rows_on_16(p.residual, p.ldr, p.y_f32);
+    const uint32_t lane_addr = tmem + ((uint32_t)quarter << 21);
+    const uint32_t tempty0 = cluster_map(smem_addr(&ctl.tempty[0]), leader);
     int a = 0;
     uint32_t aph = 0;
-    for (int it = first; it < items; it += step) {
-      const int nt = it / ntiles;
-      const WideTile t = tile(it - nt * ntiles);
-      const int r = rank * kRows + quarter * 32 + lane;   // row of the tile
-      int f = -1;
-      if (r < t.rows) f = MODE == kDense ? t.row0 + r : load_global(p.sorted_token_ids + t.row0 + r);
-      if ((unsigned)f >= (unsigned)p.pairs) f = -1;
-      const float weight = f < 0 ? 0.f : pair_weight<MODE>(p, f);
-      mbar_wait(&ctl.tfull[a], aph, abort, p.err);
-      tc_fence_after();
-      // 32 columns at a time, through shared memory, so that 4 lanes write
-      // neighbouring columns of one row
+    bool met = false;   // the cluster's pairs, at the barrier that frees the ring
+    while (wk.advance()) {
+      const WideTile t = tile(wk.t);
+      const int n = wk.nt * kWideN + rank * kRows + quarter * 32 + lane, cols = columns(t.rows);
+      const float bias = bias_of(p, t.expert, n);
+      // the pair that lane j of part i has: its row of y, or -1
+      auto pair_of = [&](int i) {
+        const int r = (2 * i + half) * kPart + lane;
+        int f = -1;
+        if (r < t.rows) f = MODE == kDense ? t.row0 + r : load_global(p.sorted_token_ids + t.row0 + r);
+        return (unsigned)f < (unsigned)p.pairs ? f : -1;
+      };
+      auto hand_back = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_relaxed(tempty0 + a * 8);   // (only tensor memory is handed back)
+        a ^= 1;
+        if (a == 0) aph ^= 1;
+      };
+      if constexpr (!CHUNKED) {
+        mbar_wait(&ctl.tfull[a], aph, abort, p.err);
+        tc_fence_after();
 #pragma unroll 1
-      for (int part = 0; part < 4; ++part) {
-        uint32_t v[32];
-        tmem_ld32(lane_addr + a * kWideN + part * 32, v);
-        tc_wait_ld();
-        tc_pin(v);
-        if (part == 3) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote_relaxed(tempty0 + a * 8);   // (only tensor memory is handed back)
+        for (int i = 0; i < kParts; ++i) {
+          const int c0 = (2 * i + half) * kPart;
+          if (c0 >= cols) break;
+          const int f = pair_of(i);
+          uint32_t raw[kPart];
+          tmem_ld32(lane_addr + a * kTileRows + c0, raw);
+          tc_wait_ld();
+          tc_pin(raw);
+          float v[kPart];
+#pragma unroll
+          for (int j = 0; j < kPart; ++j) v[j] = __uint_as_float(raw[j]);
+          finish_part<MODE>(p, f, n, bias, v);
         }
-        __syncwarp();
+        hand_back();
+      } else {
+        f32x2 acc[kParts][kPart / 2];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4 *>(out + lane * 128 + ((c ^ (lane & 7)) << 4)) =
-              make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-        __syncwarp();
-        const int chunk = lane & 3, n = nt * kWideN + half * kHalf + part * 32 + chunk * 8, cols = p.N - n;
-        const bool whole = cols >= 8;
-        float bias[8];
+        for (int i = 0; i < kParts; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) bias[j] = bias_of(p, t.expert, n + j);
-        int fr[4];
-        float res[4][8];
+          for (int j = 0; j < kPart / 2; ++j) acc[i][j] = 0;
+#pragma unroll 1
+        for (int kb = kb0; kb < kb1; kb += kChunk) {
+          mbar_wait_lean(smem_addr(&ctl.tfull[0]) + a * 8, aph, abort, p.err);
+          tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          fr[i] = __shfl_sync(0xFFFFFFFFu, f, i * 8 + (lane >> 2));
-          if (p.residual && fr[i] >= 0) load_columns(p.residual, fr[i] * p.ldr + n, p.y_f32, whole && r16, cols, res[i]);
-        }
+          for (int i = 0; i < kParts; ++i) {
+            if ((2 * i + half) * kPart < cols) {
+              uint32_t raw[kPart];
+              tmem_ld32(lane_addr + a * kTileRows + (2 * i + half) * kPart, raw);
+              tc_wait_ld();
+              tc_pin(raw);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = i * 8 + (lane >> 2);
-          const float w = __shfl_sync(0xFFFFFFFFu, weight, rr);
-          const float4 lo = *reinterpret_cast<const float4 *>(out + rr * 128 + (((2 * chunk) ^ (rr & 7)) << 4));
-          const float4 hi = *reinterpret_cast<const float4 *>(out + rr * 128 + (((2 * chunk + 1) ^ (rr & 7)) << 4));
-          float o[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-          if (fr[i] < 0) continue;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            o[j] = activate(o[j] + bias[j], p.act) * w;
-            if (p.residual) o[j] += res[i][j];
+              for (int j = 0; j < kPart / 2; ++j)
+                acc[i][j] = add2(acc[i][j], f2_pack(__uint_as_float(raw[2 * j]), __uint_as_float(raw[2 * j + 1])));
+            }
           }
-          store_columns(p.y, fr[i] * p.ldy + n, p.y_f32, whole && y16, cols, o);
+          hand_back();
+        }
+        if (pairs > 1) {
+          // Part i belongs to pair i * pairs / kParts.  A sum's place: [part of the owner][source][quad][this thread].
+          // One item a cluster, so that the memory is used once; what is sent to a CTA is waited for there.
+          const int own = kParts / pairs;   // parts a pair
+          if (tid == kWideThreads - 1)
+            mbar_arrive_expect_tx(&ctl.red_full, (pairs - 1) * own * kPart * 256 * 4);
+          cluster_arrive_release();
+          cluster_wait();
+          met = true;
+          const uint32_t base = smem_addr(smem) + (tid - 128) * 16, bar = smem_addr(&ctl.red_full);
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) {
+            const int to = i / own;
+            if (to == q) continue;
+            const uint32_t dst = cluster_map(base, to * 2 + rank), rbar = cluster_map(bar, to * 2 + rank);
+#pragma unroll
+            for (int j = 0; j < kPart / 4; ++j) {
+              float4 v;
+              f2_unpack(acc[i][2 * j], v.x, v.y);
+              f2_unpack(acc[i][2 * j + 1], v.z, v.w);
+              st_async_v4(dst + (((i - to * own) * pairs + q) * (kPart / 4) + j) * 4096, v, rbar);
+            }
+          }
+          mbar_wait_cluster(&ctl.red_full, 0, abort, p.err);
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) {
+            if (i / own != q) continue;
+            float v[kPart];
+#pragma unroll
+            for (int j = 0; j < kPart; ++j) v[j] = 0.f;
+            for (int src = 0; src < pairs; ++src) {
+              const uint8_t *from = smem + (tid - 128) * 16 + ((i - q * own) * pairs + src) * (kPart / 4) * 4096;
+#pragma unroll
+              for (int j = 0; j < kPart / 4; ++j) {
+                float4 u;
+                if (src == q) {
+                  f2_unpack(acc[i][2 * j], u.x, u.y);
+                  f2_unpack(acc[i][2 * j + 1], u.z, u.w);
+                } else {
+                  u = *reinterpret_cast<const float4 *>(from + j * 4096);
+                }
+                v[4 * j] += u.x, v[4 * j + 1] += u.y, v[4 * j + 2] += u.z, v[4 * j + 3] += u.w;
+              }
+            }
+            if ((2 * i + half) * kPart < cols) finish_part<MODE>(p, pair_of(i), n, bias, v);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kParts; ++i) {
+            if ((2 * i + half) * kPart >= cols) continue;
+            float v[kPart];
+#pragma unroll
+            for (int j = 0; j < kPart / 2; ++j) f2_unpack(acc[i][j], v[2 * j], v[2 * j + 1]);
+            finish_part<MODE>(p, pair_of(i), n, bias, v);
+          }
         }
       }
-      a ^= 1;
-      if (a == 0) aph ^= 1;
+    }
+    if (CHUNKED && pairs > 1 && !met) {
+      cluster_arrive_release();
+      cluster_wait();
     }
   }
   tc_fence_before();
   __syncthreads();
-  // The pair's accumulators are read, and nothing is on its way to either CTA's shared memory: copies and commits were
-  // waited for above, and the release orders the epilogue's remote arrivals.
+  // The pair's accumulators are read, and nothing is on its way to any CTA's shared memory: copies, commits and the
+  // other pairs' sums were waited for above, and the release orders the epilogue's remote arrivals.
   cluster_arrive_release();
   cluster_wait();
   if (warp == 1) {
@@ -535,6 +637,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 // (in bytes: tiles of 128 bytes a row whatever the type)
 int make_maps(const Bf16Args &a, const void *x, long long rows, long long ld_bytes, int x_box_rows, Bf16Maps *maps) {
   if (int st = stream::encode_u8(&maps->w, a.w, 3, 2ull * a.K, a.N, a.E, 2ull * a.ldw, 2ull * a.ldw * a.N, kRows)) return st;
+  if (int st = stream::encode_u8(&maps->x16, x, 2, 2ull * a.K, rows, 1, ld_bytes, 0, 16)) return st;
   return stream::encode_u8(&maps->x, x, 2, 2ull * a.K, rows, 1, ld_bytes, 0, x_box_rows);
 }
 
@@ -573,15 +676,55 @@ int launch_narrow(const Bf16Args &a, const DeviceInfo &dev, cudaStream_t stream)
                           cfg);
 }
 
-template <int MODE>
+// The chunked kernel's warps trade registers after the launch: the shares must
+// fit what the block was launched with, or the trade would wait forever.
+template <typename Kernel>
+bool register_shares_fit(Kernel kernel) {
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, (const void *)kernel) != cudaSuccess) return false;
+  return attr.numRegs * kWideThreads >= 128 * kWideRegsIssue + 256 * kWideRegsEpilogue;
+}
+
+// Height of a dense call's tiles, and the pairs of CTAs that split K: the
+// cheapest by a count of clocks.  A group of 64 columns takes a pair 2 clk for
+// each of the tile's rows in the tensor cores, and its operands 64 bytes a clk
+// into each SM; joining shares of K, 4000.  Shares of K take chunks: several
+// rounds of items, or a share below two chunks, are not split.
+template <typename Kernel>
+void wide_shape(const Bf16Args &a, Kernel kernel, bool chunked, const DeviceInfo &dev, Bf16Cfg *cfg, long long *items) {
+  double best = 0;
+  for (int pairs = 1; pairs <= (chunked ? 4 : 1); pairs *= 2) {
+    if (pairs > 1 && a.KB < pairs * 2 * kChunk) break;
+    const int fit = std::min(resident_clusters(kernel, 2 * pairs, cfg->smem_bytes, kWideThreads, dev), dev.sm_count / (2 * pairs));
+    for (int rows = kTileRows; rows >= 64; rows -= 32) {
+      const long long n = ((long long)a.pairs + rows - 1) / rows * cfg->nt, rounds = (n + fit - 1) / fit;
+      if (pairs > 1 && rounds > 1) continue;
+      const double group = std::max(2.0 * rows, (kTileBytes + rows / 2 * kGroupBytes) / 64.0);
+      const double cost = rounds * ((double)a.KB / pairs) * group + (pairs > 1 ? 4000 : 0);
+      if (best == 0 || cost < best) {
+        best = cost;
+        cfg->cluster = 2 * pairs;
+        cfg->tile_rows = rows;
+        *items = n;
+      }
+    }
+  }
+}
+
+template <int MODE, bool CHUNKED>
 int launch_wide(const Bf16Args &a, void *workspace, const DeviceInfo &dev, cudaStream_t stream) {
+  const auto kernel = bf16_wide_kernel<MODE, CHUNKED>;
   Bf16Cfg cfg = {};
   cfg.nt = (a.N + kWideN - 1) / kWideN;
   const long long tiles = tile_bound(a, MODE == kSorted);
   if (tiles <= 0) return 0;
-  cfg.off_ctrl = kWideStages * kWideStage + 8 * kWideOut;
+  cfg.off_ctrl = kWideStages * kWideStage;
   cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(WideCtrl);
-  if (int st = allow_dynamic_smem((const void *)bf16_wide_kernel<MODE>)) return st;
+  if (CHUNKED) {
+    static const bool fits = register_shares_fit(kernel);
+    if (!fits) return MOE_LORA_ERR_LAUNCH;
+  }
+  if (int st = allow_dynamic_smem((const void *)kernel)) return st;
   Bf16Maps maps;
   const WideTile *list = nullptr;
   if (MODE == kDense) {
@@ -594,18 +737,13 @@ int launch_wide(const Bf16Args &a, void *workspace, const DeviceInfo &dev, cudaS
     if (int st = make_maps(a, base + w.x, rows, w.ld, kRows, &maps)) return st;
     if (int st = launch_gather(a, a.x, 2 * a.ldx, 2ll * a.K, workspace, dev, stream)) return st;
   }
-  const long long items = tiles * cfg.nt;   // (the sorted arrays' own tiles are no more, but for entries that no align writes)
-  const unsigned grid = 2 * (unsigned)std::min<long long>(items, dev.sm_count / 2);
-  return launch_dependent(bf16_wide_kernel<MODE>, grid, kWideThreads, 2, cfg.smem_bytes, stream, maps, a, list, cfg);
-}
-
-// The narrow kernel while one round of its 128 x 128 items covers the output,
-// else the wide one.  The narrow one for fp32 outputs of any size: all of K
-// added up by the tensor cores is 2.4e-5 off for 7168 products of one sign.
-bool dense_is_wide(const Bf16Args &a, int sms) {
-  if (a.y_f32) return false;
-  const long long items = ((a.pairs + 127ll) / 128) * ((a.N + kRows - 1) / kRows);
-  return a.pairs > 128 && items > sms;
+  cfg.cluster = 2;
+  cfg.tile_rows = kTileRows;
+  long long items = tiles * cfg.nt;   // (the sorted arrays' own tiles are no more, but for entries that no align writes)
+  if (MODE == kDense) wide_shape(a, kernel, CHUNKED, dev, &cfg, &items);
+  const long long clusters = std::min<long long>(items, dev.sm_count / cfg.cluster);
+  return launch_dependent(kernel, (unsigned)(clusters * cfg.cluster), kWideThreads, cfg.cluster, cfg.smem_bytes, stream,
+                          maps, a, list, cfg);
 }
 
 // A round is a GB300's 152 SMs, not the current device's: the workspace's size
@@ -627,7 +765,7 @@ size_t bf16_sorted_workspace(const Bf16Args &a) {
 }
 
 bool bf16_items_fit(const Bf16Args &a, ProductMode mode) {
-  if (mode == kDense ? dense_is_wide(a, 0) : mode == kSorted && sorted_is_wide(a))
+  if (mode == kDense ? a.pairs > 64 : mode == kSorted && sorted_is_wide(a))
     return tile_bound(a, mode == kSorted) * ((a.N + kWideN - 1) / kWideN) <= INT32_MAX / 16;
   // every unit that the sorted arrays can hold, whatever they hold
   const long long units = mode == kSorted ? (long long)a.max_blocks * (a.block / 16) : unit_bound(a, mode, 16);
@@ -638,14 +776,18 @@ int launch_bf16_matmul(const Bf16Args &a, ProductMode mode, void *workspace, con
   const bool small = (mode == kNaive ? (double)a.pairs : 1.0) * a.N * a.K * 2 <= kStreamBytes;
   if (mode == kNaive) return small ? launch_bf16_stream(a, mode, dev, s) : launch_narrow<16, kNaive>(a, dev, s);
   if (mode == kSorted) {
-    if (sorted_is_wide(a)) return launch_wide<kSorted>(a, workspace, dev, s);
+    if (sorted_is_wide(a)) return launch_wide<kSorted, false>(a, workspace, dev, s);
     return launch_narrow<16, kSorted>(a, dev, s);
   }
   if (small && a.pairs <= 16) return launch_bf16_stream(a, mode, dev, s);
   if (a.pairs <= 16) return launch_narrow<16, kDense>(a, dev, s);
   if (a.pairs <= 32) return launch_narrow<32, kDense>(a, dev, s);
   if (a.pairs <= 64) return launch_narrow<64, kDense>(a, dev, s);
-  return dense_is_wide(a, dev.sm_count) ? launch_wide<kDense>(a, nullptr, dev, s) : launch_narrow<128, kDense>(a, dev, s);
+  // chunks where the output is fp32 (all of K added up by the tensor cores is
+  // 2.4e-5 off for 7168 products of one sign), or where K is split
+  const long long items = tile_bound(a, false) * ((a.N + kWideN - 1) / kWideN);
+  if (a.y_f32 || items * 4 <= dev.sm_count) return launch_wide<kDense, true>(a, nullptr, dev, s);
+  return launch_wide<kDense, false>(a, nullptr, dev, s);
 }
 
 }  // namespace moe_lora

@@ -589,12 +589,13 @@ __device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc,
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrive on `bar` of both CTAs once the pair's previously issued MMAs of this thread have completed.
-__device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
+// Arrive on `bar` of both CTAs (bits of `ctas` by their rank in the cluster) once the pair's previously issued MMAs of
+// this thread have completed.
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar, uint16_t ctas = 3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_addr(bar)),
-      "h"((uint16_t)3)
+      "h"(ctas)
       : "memory");
 }
 
