@@ -2,7 +2,11 @@
 //
 //   y[f][n] = weight[f] * act(sum + bias[e][n]) + residual[f][n]
 //
-// in fp32, rounded once to y's type.  Exponentials are CUDA's expf (its fast
+// in fp32, rounded once to y's type.  The tensor-core kernels bring the sums to
+// shared memory, where a loop of few instructions takes them four columns a
+// thread: a tile's epilogue runs a few times a launch, and code that is unrolled
+// over the sums in registers costs more to fetch than to run (64 x 2880, K of
+// 256: 7700 clk of 12900).  Exponentials are CUDA's expf (its fast
 // form is 2^-21 off, 8 fp32 roundings; the sums cost more than either).
 #pragma once
 
@@ -49,53 +53,80 @@ __device__ __forceinline__ float bias_of(const Bf16Args &p, int e, int n) {
   return p.bias && n < p.N ? load_as_f32(p.bias, (long long)e * p.N + n, p.bias_f32) : 0.f;
 }
 
-__device__ __forceinline__ void store_one(const Bf16Args &p, int f, int n, float v) {
-  if (p.y_f32) static_cast<float *>(p.y)[f * p.ldy + n] = v;
-  else static_cast<uint16_t *>(p.y)[f * p.ldy + n] = float_to_bf16_bits(v);
+__device__ __forceinline__ void store_one(const Bf16Args &p, long long at, float v) {
+  if (p.y_f32) static_cast<float *>(p.y)[at] = v;
+  else static_cast<uint16_t *>(p.y)[at] = float_to_bf16_bits(v);
 }
 
-// Column n of the pairs f (negative: none), whose sums v are.  All loads come
-// before the first store: residual may be y.
-template <int MODE, int W>
-__device__ __forceinline__ void finish_column(const Bf16Args &p, const int (&f)[W], int n, float bias, const float (&v)[W]) {
-  if (n >= p.N) return;
-  float w[W], r[W], o[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    w[i] = f[i] >= 0 ? pair_weight<MODE>(p, f[i]) : 0.f;
-    r[i] = f[i] >= 0 && p.residual ? load_as_f32(p.residual, f[i] * p.ldr + n, p.y_f32) : 0.f;
-    o[i] = v[i] + bias;
-  }
-  activate(o, p.act);
-#pragma unroll
-  for (int i = 0; i < W; ++i)
-    if (f[i] >= 0) store_one(p, f[i], n, o[i] * w[i] + r[i]);
-}
-
-// The same for a warp whose lanes hold neighbouring columns n, and the pairs f:
-// pair j is lane j's.
+// One sum: column n of pair f (negative: none).
 template <int MODE>
-__device__ __forceinline__ void finish_part(const Bf16Args &p, int f, int n, float bias, float (&v)[32]) {
-  const float w = f < 0 ? 0.f : pair_weight<MODE>(p, f);
-  const bool weighted = MODE != kDense && p.topk_weights;
+__device__ __forceinline__ void finish_one(const Bf16Args &p, int f, int e, int n, float v) {
+  if (f < 0 || n >= p.N) return;
+  const float w = pair_weight<MODE>(p, f);
+  const float r = p.residual ? load_as_f32(p.residual, f * p.ldr + n, p.y_f32) : 0.f;
+  float o[1] = {v + bias_of(p, e, n)};
+  activate(o, p.act);
+  store_one(p, f * p.ldy + n, o[0] * w + r);
+}
+
+// Whether four neighbouring elements, from a multiple of four on, of rows of p
+// can be read and written at once.
+__device__ __forceinline__ bool in_fours(const void *p, long long ld, int f32) {
+  return (ld & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & (f32 ? 15 : 7)) == 0;
+}
+
+// Four columns from n on (a multiple of four) of the pairs f (negative: none),
+// whose sums v are.  All loads come before the first store: residual may be y.
+template <int B>
+__device__ __forceinline__ void finish_fours(const Bf16Args &p, const int (&f)[B], const float (&w)[B], int n,
+                                             const float (&bias)[4], float (&v)[4 * B]) {
+  const bool whole = n + 4 <= p.N;
+  float r[4 * B];
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] += bias;
-  activate(v, p.act);
-  if (weighted) {
+  for (int i = 0; i < 4 * B; ++i) r[i] = 0.f;
+  if (p.residual) {
+    const bool fours = whole && in_fours(p.residual, p.ldr, p.y_f32);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] *= __shfl_sync(0xFFFFFFFFu, w, j);
-  }
-  if (MODE == kDense && p.residual) {
+    for (int b = 0; b < B; ++b) {
+      if (f[b] < 0) continue;
+      const long long at = f[b] * p.ldr + n;
+      if (fours && p.y_f32) {
+        const float4 u = load_global(reinterpret_cast<const float4 *>(static_cast<const float *>(p.residual) + at));
+        r[4 * b] = u.x, r[4 * b + 1] = u.y, r[4 * b + 2] = u.z, r[4 * b + 3] = u.w;
+      } else if (fours) {
+        const uint2 u = load_global(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.residual) + at));
+        r[4 * b] = __uint_as_float(u.x << 16), r[4 * b + 1] = __uint_as_float(u.x & 0xFFFF0000u);
+        r[4 * b + 2] = __uint_as_float(u.y << 16), r[4 * b + 3] = __uint_as_float(u.y & 0xFFFF0000u);
+      } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const int fj = __shfl_sync(0xFFFFFFFFu, f, j);
-      if (fj >= 0 && n < p.N) v[j] += load_as_f32(p.residual, fj * p.ldr + n, p.y_f32);
+        for (int i = 0; i < 4; ++i)
+          if (n + i < p.N) r[4 * b + i] = load_as_f32(p.residual, at + i, p.y_f32);
+      }
     }
   }
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const int fj = __shfl_sync(0xFFFFFFFFu, f, j);
-    if (fj >= 0 && n < p.N) store_one(p, fj, n, v[j]);
+  for (int i = 0; i < 4 * B; ++i) v[i] += bias[i & 3];
+  activate(v, p.act);
+  const bool fours = whole && in_fours(p.y, p.ldy, p.y_f32);
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    if (f[b] < 0) continue;
+    const long long at = f[b] * p.ldy + n;
+    float o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = v[4 * b + i] * w[b] + r[4 * b + i];
+    if (fours && p.y_f32) {
+      *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + at) = make_float4(o[0], o[1], o[2], o[3]);
+    } else if (fours) {
+      uint2 u;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(o[1]), "f"(o[0]));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(o[3]), "f"(o[2]));
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.y) + at) = u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < p.N) store_one(p, at + i, o[i]);
+    }
   }
 }
 

@@ -39,8 +39,7 @@ constexpr int kTileBytes = kRows * kGroupBytes;   // 128 rows of one group: 16 K
 
 struct Bf16Maps {
   CUtensorMap w;   // [E][N][K] in bytes, box 1 x 128 x 128
-  CUtensorMap x;   // [rows][K], box BT x 128 (dense), 1 x 128 (gathered by row) or 128 x 128 (wide)
-  CUtensorMap x16; // the same, box 16 x 128 (wide)
+  CUtensorMap x[4];   // [rows][K], box BT x 128 (dense), 1 x 128 (gathered by row); wide: 128, 64, 32 and 16 x 128
 };
 
 // Launch shape of a call.
@@ -49,7 +48,8 @@ struct Bf16Cfg {
   int nt;          // output tiles along N
   int cluster;     // CTAs of a cluster, which splits K
   int tile_rows;   // pairs of a tile (wide, dense)
-  int off_red, off_list, off_ctrl;
+  int stage_bytes; // (wide)
+  int off_red, off_tile, off_list, off_ctrl;
   int list;        // units that the list of live ones holds (0: none is made)
   int smem_bytes;
 };
@@ -57,6 +57,7 @@ struct Bf16Cfg {
 // ------------------------------------------------------------------ narrow
 
 constexpr int kMaxRing = 12;
+constexpr int kMaxSmem = 227 * 1024;
 // Groups of K whose products the tensor cores add up.  Their additions truncate,
 // so a long sum drifts; the epilogue adds the chunks in fp32, rounding to nearest.
 constexpr int kChunk = 4;
@@ -67,7 +68,6 @@ struct Narrow {
   static constexpr int kStage = 2 * kGroup;           // two groups a stage, requested together
   static constexpr int kBufs = 4;                     // accumulators in tensor memory
   static constexpr int kCols = kBufs * BT;            // power of two, >= 32
-  static constexpr int kRedBytes = BT * kRows * 4;    // every rank's partial sums of this CTA's columns
 };
 
 struct NarrowCtrl {
@@ -91,21 +91,23 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   volatile int *abort = &ctl.abort;
   const int cs = cfg.cluster;
 
-  if (tid == 0) {
-    for (int s = 0; s < cfg.stages; ++s) {
-      mbar_init(&ctl.full[s], 1);
-      mbar_init(&ctl.empty[s], 1);
+  if (warp == 0) {
+    if (lane < cfg.stages) {
+      mbar_init(&ctl.full[lane], 1);
+      mbar_init(&ctl.empty[lane], 1);
     }
-    for (int s = 0; s < C::kBufs; ++s) {
-      mbar_init(&ctl.tfull[s], 1);
-      mbar_init(&ctl.tempty[s], 4);
+    if (lane < C::kBufs) {
+      mbar_init(&ctl.tfull[lane], 1);
+      mbar_init(&ctl.tempty[lane], 4);
     }
-    mbar_init(&ctl.red_full, 1);
-    mbar_init(&ctl.done, 1);
-    ctl.abort = 0;
+    if (lane == 0) {
+      mbar_init(&ctl.red_full, 1);
+      mbar_init(&ctl.done, 1);
+      ctl.abort = 0;
+      prefetch_tensor_map(&maps.w);
+      prefetch_tensor_map(&maps.x[0]);
+    }
     fence_barrier_init();
-    prefetch_tensor_map(&maps.w);
-    prefetch_tensor_map(&maps.x);
   }
   if (warp == 1) {
     tmem_alloc(&ctl.tmem, C::kCols);
@@ -167,12 +169,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
             tma_load_3d(st + i * C::kGroup, &maps.w, (kb + i) * kGroupBytes, nt * kRows, e, &ctl.full[s]);
           if (MODE == kDense)
             for (int i = 0; i < n; ++i)
-              tma_load_2d(st + i * C::kGroup + kTileBytes, &maps.x, (kb + i) * kGroupBytes, b * BT, &ctl.full[s]);
+              tma_load_2d(st + i * C::kGroup + kTileBytes, &maps.x[0], (kb + i) * kGroupBytes, b * BT, &ctl.full[s]);
         }
         __syncwarp();
         if (MODE != kDense && mine)
           for (int i = 0; i < n; ++i)
-            tma_gather4(st + i * C::kGroup + kTileBytes + lane * 4 * kGroupBytes, &maps.x, (kb + i) * kGroupBytes, row,
+            tma_gather4(st + i * C::kGroup + kTileBytes + lane * 4 * kGroupBytes, &maps.x[0], (kb + i) * kGroupBytes, row,
                         &ctl.full[s]);
         if (++s == cfg.stages) { s = 0; ph ^= 1; }
       }
@@ -224,16 +226,26 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       for (int b = blockIdx.x; b < all_units; b += gridDim.x)
         flag_unit<MODE>(p, b, BT, block_expert<MODE>(p, b, BT), lane);
   } else {
-    // ---------------- epilogue: this thread's weight row, BT pairs
+    // ---------------- epilogue: this thread's weight row, BT pairs; then four rows, a pair a warp
     const int row = (warp - 4) * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(warp - 4) << 21);   // lane offset 32 * quarter in bits 16..31
+    float *sums = reinterpret_cast<float *>(smem + cfg.off_tile);     // [this CTA's positions][kRows]
     int a = 0;
     uint32_t aph = 0;
     while (wk.advance()) {
       const int ui = wk.it / cfg.nt, nt = wk.it - ui * cfg.nt, b = unit(ui), e = block_expert<MODE>(p, b, BT);
       if (e < 0) continue;
-      const int n = nt * kRows + row;
-      const float bias = bias_of(p, e, n);
+      // pairs of positions `lane` and lane + 32, and biases of the four rows
+      const int n = nt * kRows + lane * 4;
+      int pair[2];
+      float weight[2], bias[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        pair[i] = lane + 32 * i < BT ? block_pair<MODE>(p, b, lane + 32 * i, BT) : -1;
+        weight[i] = pair[i] < 0 ? 0.f : pair_weight<MODE>(p, pair[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bias[i] = bias_of(p, e, n + i);
       float acc[BT];
 #pragma unroll
       for (int c = 0; c < BT; ++c) acc[c] = 0.f;
@@ -254,26 +266,43 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         if (lane == 0) mbar_arrive(&ctl.tempty[a]);
         if (++a == C::kBufs) { a = 0; aph ^= 1; }
       }
-      auto store = [&](int t, const auto &v) {
-        constexpr int W = sizeof(v) / sizeof(float);
-        int f[W];
-#pragma unroll
-        for (int i = 0; i < W; ++i) f[i] = block_pair<MODE>(p, b, t + i, BT);
-        finish_column<MODE, W>(p, f, n, bias, v);
-      };
+      constexpr int kLive = MODE == kNaive ? 1 : BT;   // positions that can hold a pair
+      int first = 0, last = kLive;
       if (cs == 1) {
-        constexpr int W = MODE == kNaive ? 1 : 16;   // positions at a time; the naive form has one pair
+        named_barrier(1, 128);   // the last item's sums are out
 #pragma unroll
-        for (int c = 0; c < (MODE == kNaive ? 1 : BT); c += W) {
-          float v[W];
+        for (int c = 0; c < kLive; ++c) sums[c * kRows + row] = acc[c];
+      } else {
+        first = BT, last = 0;
+        join_ranks<BT, MODE == kNaive>(acc, cs, wk.rank, row, smem + cfg.off_red, &ctl.red_full, abort, p.err,
+                                       [&](int t, const auto &v) {
+                                         constexpr int W = sizeof(v) / sizeof(float);
+                                         first = min(first, t);
+                                         last = t + W;
 #pragma unroll
-          for (int i = 0; i < W; ++i) v[i] = acc[c + i];
-          store(c, v);
-        }
-        continue;
+                                         for (int i = 0; i < W; ++i) sums[(t - first + i) * kRows + row] = v[i];
+                                       });
+        waited = true;
       }
-      join_ranks<BT, MODE == kNaive>(acc, cs, wk.rank, row, smem + cfg.off_red, &ctl.red_full, abort, p.err, store);
-      waited = true;
+      named_barrier(1, 128);
+#pragma unroll 1
+      for (int c = first + warp - 4; c < last; c += 16) {
+        int f[4];
+        float w[4], v[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = c + 4 * i;
+          const int lo = __shfl_sync(0xFFFFFFFFu, pair[0], t & 31), hi = __shfl_sync(0xFFFFFFFFu, pair[1], t & 31);
+          const float wlo = __shfl_sync(0xFFFFFFFFu, weight[0], t & 31), whi = __shfl_sync(0xFFFFFFFFu, weight[1], t & 31);
+          f[i] = t >= last ? -1 : (t < 32 ? lo : hi);
+          w[i] = t < 32 ? wlo : whi;
+          if (t < last) {
+            const float4 u = *reinterpret_cast<const float4 *>(sums + (t - first) * kRows + lane * 4);
+            v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+          }
+        }
+        finish_fours<4>(p, f, w, n, bias, v);
+      }
     }
   }
   if (cs > 1 && !waited) cluster_wait();
@@ -300,9 +329,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
 // the pair that owns the columns, in the operand ring's memory.
 constexpr int kWideThreads = 384;
 constexpr int kWideN = 256;
-constexpr int kHalf = kWideN / 2;
-constexpr int kWideStage = 2 * kTileBytes;       // 128 of the weight's rows, and of the pairs'
-constexpr int kWideStages = 6;
+constexpr int kWideRing = 12;                    // stages at most; each 128 of the weight's rows, and half of a tile's pairs'
+constexpr int kPartBytes = 32 * 32 * 4;          // 32 pairs' sums of 32 rows, on their way out, for each epilogue warp
 constexpr int kPart = 32;                        // columns of an accumulator that a warp takes at a time
 constexpr int kParts = kTileRows / kPart / 2;    // of one of the two warps of a lane quarter
 // Rows of tiles that are neighbours in the order of the items: the pairs' rows
@@ -313,7 +341,7 @@ constexpr int kRaster = 16;
 constexpr int kWideRegsIssue = 56, kWideRegsEpilogue = 216;
 
 struct WideCtrl {
-  uint64_t full[kWideStages], empty[kWideStages];
+  uint64_t full[kWideRing], empty[kWideRing];
   uint64_t tfull[2], tempty[2];
   uint64_t done;       // every MMA of the pair
   uint64_t red_full;   // the other pairs' sums
@@ -357,22 +385,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int kb0 = (int)((long long)p.KB * q / pairs), kb1 = (int)((long long)p.KB * (q + 1) / pairs);
   const int leader = q * 2;          // the pair's rank 0 in the cluster
 
-  if (tid == 0) {
-    for (int s = 0; s < kWideStages; ++s) {
-      mbar_init(&ctl.full[s], 1);
-      mbar_init(&ctl.empty[s], 1);
+  const int stages = cfg.stages, stage_bytes = cfg.stage_bytes;
+  if (warp == 0) {
+    if (lane < stages) {
+      mbar_init(&ctl.full[lane], 1);
+      mbar_init(&ctl.empty[lane], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&ctl.tfull[s], 1);
-      mbar_init(&ctl.tempty[s], 16);   // the epilogue warps of both CTAs
+    if (lane < 2) {
+      mbar_init(&ctl.tfull[lane], 1);
+      mbar_init(&ctl.tempty[lane], 16);   // the epilogue warps of both CTAs
     }
-    mbar_init(&ctl.done, 1);
-    mbar_init(&ctl.red_full, 1);
-    ctl.abort = 0;
+    if (lane == 0) {
+      mbar_init(&ctl.done, 1);
+      mbar_init(&ctl.red_full, 1);
+      ctl.abort = 0;
+    }
+    if (lane < 5) prefetch_tensor_map(lane < 4 ? &maps.x[lane] : &maps.w);
     fence_barrier_init();
-    prefetch_tensor_map(&maps.w);
-    prefetch_tensor_map(&maps.x);
-    prefetch_tensor_map(&maps.x16);
   }
   if (warp == 1) tmem_alloc_pair(&ctl.tmem, 512);
   tc_fence_before();
@@ -407,8 +436,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         // two groups at a time: 256 consecutive bytes of each row
         for (int kb = kb0; kb < kb1; kb += 2) {
           const int n = min(2, kb1 - kb);
-          const int s1 = s + 1 == kWideStages ? 0 : s + 1;
-          const uint32_t ph1 = s + 1 == kWideStages ? ph ^ 1 : ph;
+          const int s1 = s + 1 == stages ? 0 : s + 1;
+          const uint32_t ph1 = s + 1 == stages ? ph ^ 1 : ph;
           bool ok = mbar_wait(&ctl.empty[s], ph ^ 1, abort, p.err);
           if (n > 1) ok = mbar_wait(&ctl.empty[s1], ph1 ^ 1, abort, p.err) && ok;
           go = __all_sync(0xFFFFFFFFu, ok);
@@ -418,24 +447,27 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             for (int i = 0; i < n; ++i) {
               const int at = i ? s1 : s;
               if (rank == 0) mbar_arrive_expect_tx(&ctl.full[at], bytes);
-              tma_load_3d_pair(smem + (size_t)at * kWideStage, &maps.w, (kb + i) * kGroupBytes,
+              tma_load_3d_pair(smem + (size_t)at * stage_bytes, &maps.w, (kb + i) * kGroupBytes,
                                wk.nt * kWideN + rank * kRows, t.expert, full0 + at * 8);
             }
             for (int i = 0; i < n; ++i) {
               const int at = i ? s1 : s;
-              uint8_t *st = smem + (size_t)at * kWideStage + kTileBytes;
-              if (half == kRows) {
-                tma_load_2d_pair(st, &maps.x, (kb + i) * kGroupBytes, row0, full0 + at * 8);
-              } else {
-                for (int r = 0; r < half; r += 16)
-                  tma_load_2d_pair(st + r * kGroupBytes, &maps.x16, (kb + i) * kGroupBytes, row0 + r, full0 + at * 8);
+              uint8_t *st = smem + (size_t)at * stage_bytes + kTileBytes;
+              // half is a multiple of 16, at most 128: a box for each of its bits
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int box = kRows >> j;
+                if (half & box) {
+                  const int r = half & ~(2 * box - 1);
+                  tma_load_2d_pair(st + r * kGroupBytes, &maps.x[j], (kb + i) * kGroupBytes, row0 + r, full0 + at * 8);
+                }
               }
             }
           }
           __syncwarp();
           s = n > 1 ? s1 : s;
           ph = n > 1 ? ph1 : ph;
-          if (++s == kWideStages) { s = 0; ph ^= 1; }
+          if (++s == stages) { s = 0; ph ^= 1; }
         }
       }
       // The pair's copies have landed (rank 0's barriers count both CTAs'), the
@@ -443,8 +475,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // completed before the pair exits: the epilogue waits for neither.
       __syncwarp();
       if (lane == 0) {
-        if (rank == 0) drain_ring(ctl.full, kWideStages, fills);
-        drain_ring(ctl.empty, kWideStages, fills);
+        if (rank == 0) drain_ring(ctl.full, stages, fills);
+        drain_ring(ctl.empty, stages, fills);
         drain_wait(&ctl.done, 0);
       }
     } else if (warp == 1 && rank == 0) {
@@ -465,7 +497,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           if (at == 0) mbar_wait(&ctl.tempty[a], aph ^ 1, abort, p.err);
           mbar_wait(&ctl.full[s], ph, abort, p.err);
           tc_fence_after();
-          const uint64_t dw = desc0 + s * (kWideStage >> 4), dx = dw + (kTileBytes >> 4);
+          const uint64_t dw = desc0 + s * (stage_bytes >> 4), dx = dw + (kTileBytes >> 4);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kBf16Group / 16; ++k)
@@ -474,7 +506,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (last) tc_commit_pair(&ctl.tfull[a], both);
           }
           __syncwarp();
-          if (++s == kWideStages) { s = 0; ph ^= 1; }
+          if (++s == stages) { s = 0; ph ^= 1; }
           if (last) {
             a ^= 1;
             if (a == 0) aph ^= 1;
@@ -494,26 +526,47 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_addr = tmem + ((uint32_t)quarter << 21);
     const uint32_t tempty0 = cluster_map(smem_addr(&ctl.tempty[0]), leader);
+    float *stage = reinterpret_cast<float *>(smem + cfg.off_tile + (warp - 4) * kPartBytes);   // [pair][row]
     int a = 0;
     uint32_t aph = 0;
     bool met = false;   // the cluster's pairs, at the barrier that frees the ring
     while (wk.advance()) {
       const WideTile t = tile(wk.t);
-      const int n = wk.nt * kWideN + rank * kRows + quarter * 32 + lane, cols = columns(t.rows);
-      const float bias = bias_of(p, t.expert, n);
-      // the pair that lane j of part i has: its row of y, or -1
-      auto pair_of = [&](int i) {
-        const int r = (2 * i + half) * kPart + lane;
-        int f = -1;
-        if (r < t.rows) f = MODE == kDense ? t.row0 + r : load_global(p.sorted_token_ids + t.row0 + r);
-        return (unsigned)f < (unsigned)p.pairs ? f : -1;
-      };
+      const int cols = columns(t.rows);
+      const int n = wk.nt * kWideN + rank * kRows + quarter * 32 + (lane & 7) * 4;   // four rows, for the way out
+      float bias[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bias[i] = bias_of(p, t.expert, n + i);
       auto hand_back = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote_relaxed(tempty0 + a * 8);   // (only tensor memory is handed back)
         a ^= 1;
         if (a == 0) aph ^= 1;
+      };
+      // The sums of part i, which the warp has put into `stage`; the pair that lane j has: its row of y, or -1.
+      auto put_out = [&](int i) {
+        const int r = (2 * i + half) * kPart + lane;
+        int f = -1;
+        if (r < t.rows) f = MODE == kDense ? t.row0 + r : load_global(p.sorted_token_ids + t.row0 + r);
+        if ((unsigned)f >= (unsigned)p.pairs) f = -1;
+        const float weight = f < 0 ? 0.f : pair_weight<MODE>(p, f);
+        __syncwarp();
+#pragma unroll 1
+        for (int j0 = 0; j0 < kPart; j0 += 16) {
+          int fj[4];
+          float w[4], v[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = j0 + 4 * k + (lane >> 3);
+            fj[k] = __shfl_sync(0xFFFFFFFFu, f, j);
+            w[k] = __shfl_sync(0xFFFFFFFFu, weight, j);
+            const float4 u = *reinterpret_cast<const float4 *>(stage + j * 32 + (lane & 7) * 4);
+            v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
+          }
+          finish_fours<4>(p, fj, w, n, bias, v);
+        }
+        __syncwarp();
       };
       if constexpr (!CHUNKED) {
         mbar_wait(&ctl.tfull[a], aph, abort, p.err);
@@ -522,15 +575,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         for (int i = 0; i < kParts; ++i) {
           const int c0 = (2 * i + half) * kPart;
           if (c0 >= cols) break;
-          const int f = pair_of(i);
           uint32_t raw[kPart];
           tmem_ld32(lane_addr + a * kTileRows + c0, raw);
           tc_wait_ld();
           tc_pin(raw);
-          float v[kPart];
 #pragma unroll
-          for (int j = 0; j < kPart; ++j) v[j] = __uint_as_float(raw[j]);
-          finish_part<MODE>(p, f, n, bias, v);
+          for (int j = 0; j < kPart; ++j) stage[j * 32 + lane] = __uint_as_float(raw[j]);
+          put_out(i);
         }
         hand_back();
       } else {
@@ -558,59 +609,66 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           hand_back();
         }
         if (pairs > 1) {
-          // Part i belongs to pair i * pairs / kParts.  A sum's place: [part of the owner][source][quad][this thread].
-          // One item a cluster, so that the memory is used once; what is sent to a CTA is waited for there.
-          const int own = kParts / pairs;   // parts a pair
-          if (tid == kWideThreads - 1)
-            mbar_arrive_expect_tx(&ctl.red_full, (pairs - 1) * own * kPart * 256 * 4);
+          // The parts that exist are dealt to the pairs in turn.  A sum's place: [part of the owner][source][quad][this
+          // thread].  One item a cluster, so that the memory is used once; what is sent to a CTA is waited for there.
+          const int live = max(0, (cols / kPart - half + 1) / 2);              // of this warp
+          const int all = cols / kPart;                                        // of both warps of the lane quarter
+          const int mine = (all + 1) / 2 > q ? ((all + 1) / 2 - q - 1) / pairs + 1 : 0;   // of half 0, of this pair
+          const int mine1 = all / 2 > q ? (all / 2 - q - 1) / pairs + 1 : 0;
+          if (tid == kWideThreads - 1) mbar_arrive_expect_tx(&ctl.red_full, (mine + mine1) * pairs * kPart * 128 * 4);
           cluster_arrive_release();
           cluster_wait();
           met = true;
           const uint32_t base = smem_addr(smem) + (tid - 128) * 16, bar = smem_addr(&ctl.red_full);
 #pragma unroll
           for (int i = 0; i < kParts; ++i) {
-            const int to = i / own;
-            if (to == q) continue;
+            if (i >= live) continue;
+            const int to = i & (pairs - 1), at = i / pairs;
             const uint32_t dst = cluster_map(base, to * 2 + rank), rbar = cluster_map(bar, to * 2 + rank);
 #pragma unroll
             for (int j = 0; j < kPart / 4; ++j) {
               float4 v;
               f2_unpack(acc[i][2 * j], v.x, v.y);
               f2_unpack(acc[i][2 * j + 1], v.z, v.w);
-              st_async_v4(dst + (((i - to * own) * pairs + q) * (kPart / 4) + j) * 4096, v, rbar);
+              st_async_v4(dst + ((at * pairs + q) * (kPart / 4) + j) * 4096, v, rbar);
             }
           }
-          mbar_wait_cluster(&ctl.red_full, 0, abort, p.err);
+          if (mine + mine1 > 0) mbar_wait_cluster(&ctl.red_full, 0, abort, p.err);
+#pragma unroll 1
+          for (int i = q; i < live; i += pairs) {
+            const uint8_t *from = smem + (tid - 128) * 16 + (i / pairs) * pairs * (kPart / 4) * 4096;
+#pragma unroll 1
+            for (int j = 0; j < kPart / 4; ++j) {
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < kParts; ++i) {
-            if (i / own != q) continue;
-            float v[kPart];
-#pragma unroll
-            for (int j = 0; j < kPart; ++j) v[j] = 0.f;
-            for (int src = 0; src < pairs; ++src) {
-              const uint8_t *from = smem + (tid - 128) * 16 + ((i - q * own) * pairs + src) * (kPart / 4) * 4096;
-#pragma unroll
-              for (int j = 0; j < kPart / 4; ++j) {
-                float4 u;
-                if (src == q) {
-                  f2_unpack(acc[i][2 * j], u.x, u.y);
-                  f2_unpack(acc[i][2 * j + 1], u.z, u.w);
-                } else {
-                  u = *reinterpret_cast<const float4 *>(from + j * 4096);
-                }
-                v[4 * j] += u.x, v[4 * j + 1] += u.y, v[4 * j + 2] += u.z, v[4 * j + 3] += u.w;
+              for (int src = 0; src < 4; ++src) {
+                if (src >= pairs) break;
+                const float4 u = *reinterpret_cast<const float4 *>(from + (src * (kPart / 4) + j) * 4096);
+                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
               }
+              stage[(4 * j) * 32 + lane] = v.x;
+              stage[(4 * j + 1) * 32 + lane] = v.y;
+              stage[(4 * j + 2) * 32 + lane] = v.z;
+              stage[(4 * j + 3) * 32 + lane] = v.w;
             }
-            if ((2 * i + half) * kPart < cols) finish_part<MODE>(p, pair_of(i), n, bias, v);
+            put_out(i);
           }
         } else {
+#pragma unroll 1
+          for (int part = 0; part < kParts; ++part) {
+            if ((2 * part + half) * kPart >= cols) break;
 #pragma unroll
-          for (int i = 0; i < kParts; ++i) {
-            if ((2 * i + half) * kPart >= cols) continue;
-            float v[kPart];
+            for (int i = 0; i < kParts; ++i) {
+              if (i != part) continue;
 #pragma unroll
-            for (int j = 0; j < kPart / 2; ++j) f2_unpack(acc[i][j], v[2 * j], v[2 * j + 1]);
-            finish_part<MODE>(p, pair_of(i), n, bias, v);
+              for (int j = 0; j < kPart / 2; ++j) {
+                float lo, hi;
+                f2_unpack(acc[i][j], lo, hi);
+                stage[(2 * j) * 32 + lane] = lo;
+                stage[(2 * j + 1) * 32 + lane] = hi;
+              }
+            }
+            put_out(part);
           }
         }
       }
@@ -635,10 +693,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 // ------------------------------------------------------------------ launch
 
 // (in bytes: tiles of 128 bytes a row whatever the type)
-int make_maps(const Bf16Args &a, const void *x, long long rows, long long ld_bytes, int x_box_rows, Bf16Maps *maps) {
+int make_maps(const Bf16Args &a, const void *x, long long rows, long long ld_bytes, int x_box_rows, int x_maps,
+              Bf16Maps *maps) {
   if (int st = stream::encode_u8(&maps->w, a.w, 3, 2ull * a.K, a.N, a.E, 2ull * a.ldw, 2ull * a.ldw * a.N, kRows)) return st;
-  if (int st = stream::encode_u8(&maps->x16, x, 2, 2ull * a.K, rows, 1, ld_bytes, 0, 16)) return st;
-  return stream::encode_u8(&maps->x, x, 2, 2ull * a.K, rows, 1, ld_bytes, 0, x_box_rows);
+  for (int i = 0; i < x_maps; ++i)
+    if (int st = stream::encode_u8(&maps->x[i], x, 2, 2ull * a.K, rows, 1, ld_bytes, 0, x_box_rows >> i)) return st;
+  return 0;
 }
 
 template <int BT, int MODE>
@@ -655,23 +715,24 @@ int launch_narrow(const Bf16Args &a, const DeviceInfo &dev, cudaStream_t stream)
   // longer than a CTA's share lets more clusters fit.
   auto shape = [&](int cs) {
     cfg.cluster = cs;
-    const int list_bytes = cfg.list * 4;
-    const int fixed = (cs > 1 ? C::kRedBytes : 0) + list_bytes + (int)sizeof(NarrowCtrl) + 128;
+    const int red = cs > 1 ? join_bytes(BT, cs, MODE == kNaive) : 0;
+    const int tile = cs > 1 ? red / cs : (MODE == kNaive ? 1 : BT) * kRows * 4;
+    const int fixed = red + tile + cfg.list * 4 + (int)sizeof(NarrowCtrl);
     const int share = items * cs <= dev.sm_count ? ((a.KB + cs - 1) / cs + 1) / 2 : kMaxRing;
-    cfg.stages = std::max(2, std::min(share, std::min(kMaxRing, (224 * 1024 - fixed) / C::kStage)));
+    cfg.stages = std::max(2, std::min(share, std::min(kMaxRing, (kMaxSmem - fixed) / C::kStage)));
     cfg.off_red = cfg.stages * C::kStage;
-    cfg.off_list = cfg.off_red + (cs > 1 ? C::kRedBytes : 0);
-    cfg.off_ctrl = cfg.off_list + list_bytes;
+    cfg.off_tile = cfg.off_red + red;
+    cfg.off_list = cfg.off_tile + tile;
+    cfg.off_ctrl = cfg.off_list + cfg.list * 4;
     cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(NarrowCtrl);
     return resident_clusters(bf16_narrow_kernel<BT, MODE>, cs, cfg.smem_bytes, kNarrowThreads, dev);
   };
-  int cs = 1;
-  while (cs < 8 && items * cs * 2 <= dev.sm_count && a.KB >= cs * 2 * kChunk) cs *= 2;
+  int cs = (int)std::max<long long>(1, std::min<long long>(std::min<long long>(8, dev.sm_count / items), a.KB / kChunk));
   int fit = shape(cs);
-  while (cs > 1 && fit < items) fit = shape(cs /= 2);
+  while (cs > 1 && fit < items) fit = shape(--cs);
   const unsigned clusters = (unsigned)std::min<long long>(items, std::min(fit, dev.sm_count / cs));
   Bf16Maps maps;
-  if (int st = make_maps(a, a.x, a.rows, 2 * a.ldx, MODE == kDense ? BT : 1, &maps)) return st;
+  if (int st = make_maps(a, a.x, a.rows, 2 * a.ldx, MODE == kDense ? BT : 1, 1, &maps)) return st;
   return launch_dependent(bf16_narrow_kernel<BT, MODE>, clusters * cs, kNarrowThreads, cs, cfg.smem_bytes, stream, maps, a,
                           cfg);
 }
@@ -718,8 +779,16 @@ int launch_wide(const Bf16Args &a, void *workspace, const DeviceInfo &dev, cudaS
   cfg.nt = (a.N + kWideN - 1) / kWideN;
   const long long tiles = tile_bound(a, MODE == kSorted);
   if (tiles <= 0) return 0;
-  cfg.off_ctrl = kWideStages * kWideStage;
-  cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(WideCtrl);
+  // a ring as long as fits, of stages for the highest tile
+  auto ring = [&](int rows) {
+    cfg.tile_rows = rows;
+    cfg.stage_bytes = kTileBytes + rows / 2 * kGroupBytes;
+    cfg.stages = std::min(kWideRing, (kMaxSmem - 8 * kPartBytes - (int)sizeof(WideCtrl)) / cfg.stage_bytes);
+    cfg.off_tile = cfg.stages * cfg.stage_bytes;
+    cfg.off_ctrl = cfg.off_tile + 8 * kPartBytes;
+    cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(WideCtrl);
+  };
+  ring(kTileRows);
   if (CHUNKED) {
     static const bool fits = register_shares_fit(kernel);
     if (!fits) return MOE_LORA_ERR_LAUNCH;
@@ -728,19 +797,21 @@ int launch_wide(const Bf16Args &a, void *workspace, const DeviceInfo &dev, cudaS
   Bf16Maps maps;
   const WideTile *list = nullptr;
   if (MODE == kDense) {
-    if (int st = make_maps(a, a.x, a.rows, 2 * a.ldx, kRows, &maps)) return st;
+    if (int st = make_maps(a, a.x, a.rows, 2 * a.ldx, kRows, 4, &maps)) return st;
   } else {
     const long long rows = (long long)a.max_blocks * a.block;
     const GatherSpace w = gather_space(rows, 2ll * a.K);
     uint8_t *base = static_cast<uint8_t *>(workspace);
     list = reinterpret_cast<const WideTile *>(base);
-    if (int st = make_maps(a, base + w.x, rows, w.ld, kRows, &maps)) return st;
+    if (int st = make_maps(a, base + w.x, rows, w.ld, kRows, 4, &maps)) return st;
     if (int st = launch_gather(a, a.x, 2 * a.ldx, 2ll * a.K, workspace, dev, stream)) return st;
   }
   cfg.cluster = 2;
-  cfg.tile_rows = kTileRows;
   long long items = tiles * cfg.nt;   // (the sorted arrays' own tiles are no more, but for entries that no align writes)
-  if (MODE == kDense) wide_shape(a, kernel, CHUNKED, dev, &cfg, &items);
+  if (MODE == kDense) {
+    wide_shape(a, kernel, CHUNKED, dev, &cfg, &items);
+    ring(cfg.tile_rows);
+  }
   const long long clusters = std::min<long long>(items, dev.sm_count / cfg.cluster);
   return launch_dependent(kernel, (unsigned)(clusters * cfg.cluster), kWideThreads, cfg.cluster, cfg.smem_bytes, stream,
                           maps, a, list, cfg);

@@ -137,11 +137,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) bf16_stream_kerne
     constexpr int kLive = MODE == kNaive ? 1 : kUnit;
     for (int o = tid; o < kRowsCta * kLive; o += kThreads) {
       const int r = o % kRowsCta, c = o / kRowsCta, n = tile * kRowsCta + r;
-      float v[1] = {0.f};
+      float v = 0.f;
 #pragma unroll
-      for (int q = 0; q < KS; ++q) v[0] += red[q * RG + (r >> 4)][c][r & 15];
-      const int f[1] = {block_pair<MODE>(p, b, c, kUnit)};
-      finish_column<MODE, 1>(p, f, n, bias_of(p, e, n), v);
+      for (int q = 0; q < KS; ++q) v += red[q * RG + (r >> 4)][c][r & 15];
+      finish_one<MODE>(p, block_pair<MODE>(p, b, c, kUnit), e, n, v);
     }
     __syncthreads();
   }

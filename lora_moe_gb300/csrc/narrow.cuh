@@ -59,87 +59,78 @@ struct NarrowWork {
   }
 };
 
-// The sums of one CTA's positions over CS ranks, in rank order; Q of 4
-// positions (or 2) at a time.
-template <int CS, int W>
-__device__ __forceinline__ void sum_ranks(const float *buf, int per_rank, int at, int row, float (&v)[W]) {
-#pragma unroll
-  for (int i = 0; i < W; ++i) v[i] = 0.f;
-#pragma unroll
-  for (int q = 0; q < CS; ++q) {
-    const float *src = buf + ((q * per_rank + at) * kRows + row) * W;
-    if constexpr (W == 4) {
-      const float4 u = *reinterpret_cast<const float4 *>(src);
-      v[0] += u.x;
-      v[1] += u.y;
-      v[2] += u.z;
-      v[3] += u.w;
-    } else if constexpr (W == 2) {
-      const float2 u = *reinterpret_cast<const float2 *>(src);
-      v[0] += u.x;
-      v[1] += u.y;
-    } else {
-      v[0] += *src;
-    }
-  }
+// Units of W neighbouring positions of a tile of BT: 4, or 2 where a cluster of
+// cs CTAs has more than BT / 4; rank q of the cluster has the units [U * q / cs,
+// U * (q + 1) / cs).
+__host__ __device__ constexpr int join_width(int BT, int cs) { return BT / 4 >= cs ? 4 : 2; }
+// Bytes that join_ranks() needs in each CTA (SINGLE: one position).
+__host__ __device__ constexpr int join_bytes(int BT, int cs, bool single) {
+  return single ? cs * kRows * 4
+                : (BT / join_width(BT, cs) + cs - 1) / cs * join_width(BT, cs) * cs * kRows * 4;
 }
 
 // The sums over a cluster of cs > 1 CTAs of their acc (this thread's row, BT
-// positions), passed to store(first position, sums) 1, 2 or 4 at a time in one of
-// them; by the 128 epilogue threads.  Rank q sums the positions [q * tc, (q + 1) * tc) of every
+// positions), each passed to emit(first position, W sums) in the CTA that has
+// them; by the 128 epilogue threads.  A rank sums its positions of every
 // rank's partial sums, in rank order (SINGLE: position 0, by rank 0).  There is
-// one item at most, so that the buffer `red` (BT * kRows floats; SINGLE: cs *
-// kRows) is used once, and every CTA waits for all that is sent to it: nothing
-// reaches a CTA that has left.  Waits for the cluster's first barrier phase (every CTA has
-// initialised its barriers) itself.
-template <int BT, bool SINGLE, typename Store>
+// one item at most, so that the buffer `red` is used once, and every CTA waits
+// for all that is sent to it: nothing reaches a CTA that has left.  Waits for the cluster's
+// first barrier phase (every CTA has initialised its barriers) itself.
+template <int BT, bool SINGLE, typename Emit>
 __device__ __forceinline__ void join_ranks(const float (&acc)[BT], int cs, int rank, int row, uint8_t *red,
-                                           uint64_t *red_full, volatile int *abort, int32_t *err, Store store) {
-  const int tc = SINGLE ? 1 : BT / cs, lg = __ffs(tc) - 1;
+                                           uint64_t *red_full, volatile int *abort, int32_t *err, Emit emit) {
   const uint32_t red_base = smem_addr(red), red_bar = smem_addr(red_full);
-  const bool receives = !SINGLE || rank == 0;
-  if (row == 0 && receives) mbar_arrive_expect_tx(red_full, (SINGLE ? cs : BT) * kRows * 4);
-  cluster_wait();
   if constexpr (SINGLE) {
+    if (row == 0 && rank == 0) mbar_arrive_expect_tx(red_full, cs * kRows * 4);
+    cluster_wait();
     st_async_f1(cluster_map(red_base + (rank * kRows + row) * 4, 0), acc[0], cluster_map(red_bar, 0));
-  } else if (tc >= 4) {
+    if (rank != 0) return;
+    mbar_wait_cluster(red_full, 0, abort, err);
+    float v[1] = {0.f};
+    for (int q = 0; q < cs; ++q) v[0] += reinterpret_cast<const float *>(red)[q * kRows + row];
+    emit(0, v);
+  } else {
+    auto run = [&](auto width) {
+      constexpr int W = decltype(width)::value, U = BT / W;
+      const int first = U * rank / cs, own = U * (rank + 1) / cs - first;
+      if (row == 0) mbar_arrive_expect_tx(red_full, own * cs * W * kRows * 4);
+      cluster_wait();
 #pragma unroll
-    for (int c = 0; c < BT; c += 4) {
-      const int q = c >> lg, quad = (c - (q << lg)) >> 2;
-      st_async_v4(cluster_map(red_base + (((rank * tc) >> 2) + quad) * kRows * 16 + row * 16, q),
-                  make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]), cluster_map(red_bar, q));
-    }
-  } else {   // two positions a rank
-#pragma unroll
-    for (int c = 0; c < BT; c += 2)
-      st_async_f2(cluster_map(red_base + (rank * kRows + row) * 8, c >> 1), acc[c], acc[c + 1],
-                  cluster_map(red_bar, c >> 1));
-  }
-  if (!receives) return;
-  mbar_wait_cluster(red_full, 0, abort, err);
-  const float *buf = reinterpret_cast<const float *>(red);
-  auto finish = [&](auto ranks) {
-    constexpr int CS = decltype(ranks)::value;
-    if constexpr (SINGLE) {
-      float v[1];
-      sum_ranks<CS>(buf, 1, 0, row, v);
-      store(0, v);
-    } else if constexpr (BT / CS >= 4) {
-#pragma unroll 4
-      for (int quad = 0; quad < BT / CS / 4; ++quad) {
-        float v[4];
-        sum_ranks<CS>(buf, BT / CS / 4, quad, row, v);
-        store(rank * (BT / CS) + quad * 4, v);
+      for (int u = 0; u < U; ++u) {
+        const int q = ((u + 1) * cs - 1) / U, at = u - U * q / cs, of = U * (q + 1) / cs - U * q / cs;
+        const uint32_t dst = cluster_map(red_base + ((rank * of + at) * kRows + row) * W * 4, q), bar = cluster_map(red_bar, q);
+        if constexpr (W == 4)
+          st_async_v4(dst, make_float4(acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]), bar);
+        else
+          st_async_f2(dst, acc[2 * u], acc[2 * u + 1], bar);
       }
-    } else {
-      float v[2];
-      sum_ranks<CS>(buf, 1, 0, row, v);
-      store(rank * 2, v);
+      mbar_wait_cluster(red_full, 0, abort, err);
+      const float *buf = reinterpret_cast<const float *>(red) + row * W;
+#pragma unroll 1   // (code that runs once a launch is fetched as it runs)
+      for (int u = 0; u < own; ++u) {
+        float v[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (q >= cs) break;
+          const float *src = buf + (q * own + u) * kRows * W;
+          if constexpr (W == 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(src);
+            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2 *>(src);
+            v[0] += x.x, v[1] += x.y;
+          }
+        }
+        emit((first + u) * W, v);
+      }
+    };
+    if constexpr (BT == 16) {
+      if (cs > 4) return run(std::integral_constant<int, 2>());
     }
-  };
-  if (cs == 2) finish(std::integral_constant<int, 2>());
-  else if (cs == 4) finish(std::integral_constant<int, 4>());
-  else finish(std::integral_constant<int, 8>());
+    run(std::integral_constant<int, 4>());
+  }
 }
 
 }  // namespace moe_lora
