@@ -7,15 +7,22 @@
 //   w[k] = s[ids[k]] (/ sum_k s[ids[k]]) * scale
 //
 // One warp a token, VPL neighbouring experts a lane, so that the lowest lane
-// among equals holds the lowest index.  Bound by latency for a few tokens, by
-// instructions for many (the logits' bytes are less).
+// among equals holds the lowest index.  The topk-th largest of the lanes' maxima
+// is a bound that all chosen experts reach; those that do are few (topk to 2
+// topk, mostly): a lane takes each and counts the ones before it, which is its
+// place (route_fast).  What that form leaves (numbers that are none, masked
+// experts under a bias, more than 32 experts that reach the bound, groups that do
+// not end with lanes) takes the largest topk times (route_general).  Bound by
+// latency for a few tokens, by instructions for many (the logits' bytes are less).
 //
 // Which experts are chosen is what arithmetic in 64 bits says.  Without a bias
 // (and sums of a group's scores) the logits decide, which needs no arithmetic.
-// With one, c is computed in fp32 with a bound of its error, and a token for
-// which two neighbours of the order lie within that bound is done again in
-// fp64: few tokens, as the bound is 1e-6 of the scores.
+// With one, c is computed in fp32 with a bound of its error, and where two
+// neighbours of the order lie within that bound it is done again in fp64: for
+// few tokens, as the bound is 1e-6 of the scores.
 #include <cuda_runtime.h>
+
+#include <cfloat>
 
 #include <algorithm>
 
@@ -77,9 +84,6 @@ __device__ __forceinline__ void merge2(T &a1, T &a2, T b1, T b2) {
   a2 = a2 < lo ? lo : a2;
 }
 
-// Numerators and scores.  expf, its argument and the quotient: within 2^-21 of s
-// each (an ulp, half an ulp of 1 + e and of the quotient, and for the softmax
-// |x| exp(-|x|) half ulps of x); a sum of VPL + 5 steps, (VPL + 5) half ulps.
 template <typename T>
 __device__ __forceinline__ T sigmoid(T x) {
   const T e = exp(-fabs(x));
@@ -91,11 +95,27 @@ __device__ __forceinline__ float logit_at(const RouteArgs &p, long long i) {
                       : bf16_bits_to_float(load_global(static_cast<const uint16_t *>(p.logits) + i));
 }
 
-// Experts of one token: id of place `lane` (lanes below topk), and its weight.
-// Returns whether the fp32 scores cannot tell the order (T = float).
+struct Routed {
+  int id;         // of place `lane`, in lanes below topk
+  float weight;
+  bool unsure;    // the fp32 scores cannot tell the order (T = float)
+};
+
+// One token, whatever its logits.  Apart, so that the fast form keeps its
+// registers.  Errors of fp32 scores: expf, its argument and the quotient within
+// 2^-21 of s (an ulp, half an ulp of 1 + e and of the quotient, and for the
+// softmax |x| exp(-|x|) half ulps of x); a sum of VPL + 5 steps, (VPL + 5) half ulps.
 template <typename T, int VPL>
-__device__ __forceinline__ bool route_token(const RouteArgs &p, const float (&l)[VPL], const float (&b)[VPL], int lane,
-                                            long long row, int *id, float *weight) {
+__device__ __noinline__ Routed route_general(const RouteArgs &p, long long row) {
+  const int lane = threadIdx.x & 31;
+  Routed r = {0, 0.f, false};
+  float l[VPL], b[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane * VPL + i;
+    l[i] = e < p.E ? logit_at(p, row + e) : -INFINITY;
+    b[i] = e < p.E && p.bias ? load_global(p.bias + e) : 0.f;
+  }
   typedef typename KeyOf<T>::type Key;
   const T kLow = -INFINITY;
   const int E = p.E, e0 = lane * VPL;
@@ -194,7 +214,6 @@ __device__ __forceinline__ bool route_token(const RouteArgs &p, const float (&l)
     if (key[i] > best) best = key[i], at = i;
   }
   T mine = kLow, before = INFINITY;
-  *id = 0;
   int last = -1;
   for (int k = 0; k < p.topk; ++k) {
     const Key m = warp_max(best);
@@ -210,7 +229,7 @@ __device__ __forceinline__ bool route_token(const RouteArgs &p, const float (&l)
     before = v;
     last = e;
     if (lane == k) {
-      *id = e;
+      r.id = e;
       mine = v;
     }
     if (lane == from) {
@@ -226,23 +245,289 @@ __device__ __forceinline__ bool route_token(const RouteArgs &p, const float (&l)
     }
   }
   if (sizeof(T) == 4 && scores) unsure |= close(before, from_key(warp_max(best)), 1.f);
-  if (unsure) return true;
+  r.unsure = unsure;
+  if (unsure) return r;
 
   T s = 0;
   if (lane < p.topk && mine > kLow) {
     float x = (float)mine;   // without scores, the logit itself
-    if (scores) x = logit_at(p, row + *id);
+    if (scores) x = logit_at(p, row + r.id);
     s = score(x);
   }
   if (p.renormalize) {
     const T total = warp_sum(s);
     if (total > 0) s = s / total;
   }
-  *weight = bad ? __int_as_float(0x7FC00000) : (float)(s * T(p.scale));
-  return false;
+  r.weight = bad ? __int_as_float(0x7FC00000) : (float)(s * T(p.scale));
+  return r;
 }
 
-// VPL values of a row from element e0 on, n of which exist.
+// ------------------------------------------------------------------ fast
+
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// The approximate units, without their handling of denormals: 2^x within 2^-22
+// of itself and 1 / x within an ulp.
+__device__ __forceinline__ float exp2_unit(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_unit(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.44269504f;
+// Scores that only order experts.  x log2(e) is rounded twice: exp(x) is within
+// 2^-22 + |x| 2^-23 of itself (and, as |x| exp(-|x|) < 0.37, within 2^-22 + 2^-24 of
+// one), zero below 2^-126; so a sigmoid, whose slope is s (1 - s), is within 2^-21,
+// a softmax's numerator within 2^-21 of the largest, and a sum of them in VPL + 5
+// steps within 2^-21 + (VPL + 5) 2^-24 of itself.
+__device__ __forceinline__ float order_sigmoid(float x) {
+  const float e = exp2_unit(-kLog2e * fabsf(x)), r = rcp_unit(1.f + e);
+  return x < 0.f ? e * r : r;
+}
+
+// What does not depend on the token.
+struct Lane {
+  int lane, span;   // span: lanes of a group (a power of two)
+  bool ok;          // the fast form takes the groups and the bias
+};
+
+// Experts of a token that reach the bound: expert and choice, then a key (the
+// larger choice first, then the lower index), then in order.  Unused entries
+// are zero, as all are between tokens.
+struct __align__(16) Picks {
+  unsigned long long entry[32];
+  int count;
+};
+__device__ __forceinline__ unsigned long long pack(uint32_t lo, uint32_t hi) { return lo | (unsigned long long)hi << 32; }
+
+// The choice, in fp64, of the expert that each lane has (negative: none).
+template <int VPL>
+__device__ __noinline__ double exact_choice(const RouteArgs &p, long long row, int expert) {
+  double sum = 1.0;
+  float top = -INFINITY;
+  if (!p.sigmoid) {
+    const int e0 = (threadIdx.x & 31) * VPL;
+    for (int i = 0; i < VPL && e0 + i < p.E; ++i) top = fmaxf(top, logit_at(p, row + e0 + i));
+    top = warp_max(top);
+    sum = 0.0;
+    for (int i = 0; i < VPL && e0 + i < p.E; ++i) sum += exp((double)logit_at(p, row + e0 + i) - top);
+    sum = warp_sum(sum);
+  }
+  if (expert < 0) return 0.0;
+  const double x = logit_at(p, row + expert);
+  return (p.sigmoid ? sigmoid(x) : exp(x - top) / sum) + (p.bias ? (double)load_global(p.bias + expert) : 0.0);
+}
+
+// One token without NaN or +inf (SCORES: without -inf either); false where it
+// is left to the general form.
+template <int VPL, bool SCORES, bool FULL>
+__device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[VPL], const float (&b)[VPL], const Lane &at,
+                                           long long row, Picks &picks, Routed *out) {
+  const int lane = at.lane, e0 = lane * VPL;
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const bool exists = FULL || e0 + i < p.E;
+    odd |= exists && (SCORES ? !(fabsf(l[i]) < INFINITY) : !(l[i] < INFINITY));
+  }
+  if (__any_sync(kAll, odd)) return false;
+
+  float c[VPL], top = 0.f, sum = 1.f, slack = 0.f;
+  if (!p.sigmoid && (SCORES || !p.renormalize)) {
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+    top = warp_max(m);
+    float part = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      c[i] = exp2_unit((l[i] - top) * kLog2e);
+      part += c[i];
+    }
+    sum = warp_sum(part);
+  }
+  if constexpr (SCORES) {
+    // twice the scores' error
+    if (p.sigmoid) {
+      slack = 9.5367432e-7f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = order_sigmoid(l[i]) + b[i];
+    } else {
+      const float inv = rcp_unit(sum);
+      slack = inv * ((VPL + 32) * 2 * 5.9604645e-8f);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = c[i] * inv + b[i];
+    }
+    if (!FULL) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (e0 + i >= p.E) c[i] = -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c[i] = l[i];
+  }
+  // by how much a choice near v may be wrong, twice: the scores' errors, and half an ulp of its sum
+  auto doubt = [&](float v) { return slack + 2.3841858e-7f * fabsf(v); };
+
+  if (p.groups > p.topk_groups) {
+    float a1 = c[0], a2 = -INFINITY;
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) {
+      a2 = fmaxf(a2, fminf(a1, c[i]));
+      a1 = fmaxf(a1, c[i]);
+    }
+    for (int d = 1; d < at.span; d <<= 1) {
+      const float b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
+      a2 = fmaxf(fmaxf(a2, b2), fminf(a1, b1));
+      a1 = fmaxf(a1, b1);
+    }
+    const int g = lane / at.span;                                              // of this lane's experts
+    const float sums = p.best == 2 && a2 > -INFINITY ? a1 + a2 : a1;
+    float worth = __shfl_sync(kAll, sums, lane * at.span & 31);                // of group `lane`
+    if (lane >= p.groups) worth = -INFINITY;
+    int before = 0;                                                            // groups that come before it
+#pragma unroll 4
+    for (int o = 0; o < p.groups; ++o) {
+      const float w = __shfl_sync(kAll, worth, o);
+      before += w > worth || (w == worth && o < lane);
+    }
+    if (lane >= p.groups) before = 32;
+    if (SCORES) {
+      // the last that stays against the first that does not
+      const float stays = __shfl_sync(kAll, worth, __ffs(__ballot_sync(kAll, before == p.topk_groups - 1)) - 1);
+      const float goes = __shfl_sync(kAll, worth, __ffs(__ballot_sync(kAll, before == p.topk_groups)) - 1);
+      const float near = p.best * doubt(fmaxf(fabsf(stays), fabsf(goes)));
+      if (stays - goes <= near) {
+        // The groups near them again, from exact choices of those experts that may be their best.
+        const bool close = sums >= stays - near && sums <= goes + near;
+        const float least = (p.best == 2 && a2 > -INFINITY ? a2 : a1) - doubt(a1);
+        double exact = worth;
+        if (lane < p.groups && worth >= stays - near && worth <= goes + near) exact = -INFINITY;
+        double second = -INFINITY;
+        for (int i = 0; i < VPL; ++i) {   // (one expert a lane at a time, where any has one)
+          float ci = 0.f;
+#pragma unroll
+          for (int k = 0; k < VPL; ++k)
+            if (k == i) ci = c[k];
+          const bool need = close && ci >= least;
+          uint32_t who = __ballot_sync(kAll, need);
+          if (!who) continue;
+          const double x = exact_choice<VPL>(p, row, need ? e0 + i : -1);
+          for (; who; who &= who - 1) {
+            const int from = __ffs(who) - 1;
+            const double v = __shfl_sync(kAll, x, from);
+            if (from / at.span == lane) merge2(exact, second, v, (double)-INFINITY);
+          }
+        }
+        if (p.best == 2 && second > -INFINITY) exact += second;
+        before = 0;
+        for (int o = 0; o < p.groups; ++o) {
+          const double w = __shfl_sync(kAll, exact, o);
+          before += w > exact || (w == exact && o < lane);
+        }
+        if (lane >= p.groups) before = 32;
+      }
+    }
+    const uint32_t open = __ballot_sync(kAll, before < p.topk_groups);
+    if (!(open >> g & 1)) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = -INFINITY;
+    }
+  }
+
+  // the bound: at least topk lanes reach it (every finite choice does where fewer have one)
+  float best = c[0], bound = -INFINITY;
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) best = fmaxf(best, c[i]);
+#pragma unroll 2
+  for (int k = 0; k < p.topk; ++k) {
+    bound = warp_max(best);
+    if (best == bound) best = -INFINITY;
+  }
+  if (bound == -INFINITY) bound = -FLT_MAX;
+  else if (SCORES) bound -= doubt(bound);   // and what is as large but for errors
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) mine += c[i] >= bound;
+  int to = 0;
+  if (mine) to = atomicAdd(&picks.count, mine);
+  __syncwarp();
+  const int count = picks.count;
+  __syncwarp();
+  picks.count = 0;
+  if (count > 32 || count < p.topk) return false;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    if (c[i] >= bound) picks.entry[to++] = pack(e0 + i, __float_as_uint(c[i]));
+  }
+  __syncwarp();
+  const bool have = lane < count;
+  const unsigned long long own = picks.entry[lane];
+  int expert = have ? (int)(uint32_t)own : -1;
+  const float choice = __uint_as_float((uint32_t)(own >> 32));
+  const unsigned long long key = have ? pack(~(uint32_t)expert, to_key(choice)) : 0;
+  __syncwarp();
+  picks.entry[lane] = key;
+  __syncwarp();
+  int place = 0;
+#pragma unroll 1
+  for (int j = 0; j < count; j += 4) {
+    const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(&picks.entry[j]);
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&picks.entry[j + 2]);
+    place += (u.x > key) + (u.y > key) + (v.x > key) + (v.y > key);
+  }
+  __syncwarp();
+  if (have) picks.entry[place] = pack(expert, __float_as_uint(choice));
+  __syncwarp();
+  const unsigned long long first = picks.entry[lane], after = picks.entry[min(lane + 1, 31)];
+  expert = have ? (int)(uint32_t)first : -1;
+  float mine_c = __uint_as_float((uint32_t)(first >> 32));
+  if constexpr (SCORES) {
+    const float next = __uint_as_float((uint32_t)(after >> 32));
+    if (__any_sync(kAll, lane < p.topk && lane + 1 < count && mine_c - next <= doubt(fmaxf(fabsf(mine_c), fabsf(next))))) {
+      // again in 64 bits, which tell equal inputs from others
+      const double exact = exact_choice<VPL>(p, row, expert);
+      place = 0;
+      for (int j = 0; j < count; ++j) {
+        const double o = __shfl_sync(kAll, exact, j);
+        const int e = __shfl_sync(kAll, expert, j);
+        place += o > exact || (o == exact && e < expert);
+      }
+      if (have) picks.entry[place] = (uint32_t)expert;
+      __syncwarp();
+      expert = have ? (int)(uint32_t)picks.entry[lane] : -1;
+    }
+  }
+  __syncwarp();
+  picks.entry[lane] = 0;   // (for the next token)
+
+  const float logit = !SCORES ? mine_c : (lane < p.topk ? logit_at(p, row + expert) : 0.f);
+  // (where the softmax's sum cancels, the largest of the chosen is as good as the row's)
+  const float ref = SCORES || !p.renormalize ? top : __shfl_sync(kAll, logit, 0);
+  float s = 0.f;
+  if (lane < p.topk) s = p.sigmoid ? sigmoid(logit) : expf(logit - ref);
+  float scale = p.scale;
+  if (p.renormalize) {
+    const float total = warp_sum(s);
+    if (total > 0.f) scale = __fdividef(scale, total);
+  } else if (!p.sigmoid) {
+    scale = __fdividef(scale, sum);
+  }
+  out->id = expert;
+  out->weight = s * scale;
+  return true;
+}
+
+// VPL values of a row, n of which exist.
 template <int VPL, typename V>
 __device__ __forceinline__ void load_row(const V *src, int n, bool vec, float missing, float (&v)[VPL]) {
   constexpr int kBytes = VPL * (int)sizeof(V), kUnit = kBytes < 16 ? kBytes : 16, kPer = kUnit / (int)sizeof(V);
@@ -280,43 +565,54 @@ __device__ __forceinline__ void load_row(const V *src, int n, bool vec, float mi
   }
 }
 
-// The same in fp64; apart, so that the fp32 form keeps its registers.
-struct Routed {
-  int id;
-  float weight;
-};
 template <int VPL>
-__device__ __noinline__ Routed route_token_64(const RouteArgs &p, int lane, long long row) {
-  float l[VPL], b[VPL];
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane * VPL + i;
-    l[i] = e < p.E ? logit_at(p, row + e) : -INFINITY;
-    b[i] = e < p.E && p.bias ? load_global(p.bias + e) : 0.f;
-  }
-  Routed r;
-  route_token<double, VPL>(p, l, b, lane, row, &r.id, &r.weight);
-  return r;
+__device__ __forceinline__ void load_logits(const RouteArgs &p, long long at, int n, bool vec, float (&v)[VPL]) {
+  if (p.logits_f32) load_row<VPL, float>(static_cast<const float *>(p.logits) + at, n, vec, -INFINITY, v);
+  else load_row<VPL, uint16_t>(static_cast<const uint16_t *>(p.logits) + at, n, vec, -INFINITY, v);
 }
 
-template <int VPL, typename V>
-__global__ void __launch_bounds__(kThreads, VPL <= 8 ? 8 : 4) route_kernel(const __grid_constant__ RouteArgs p, bool vec) {
-  const int lane = threadIdx.x & 31;
+template <int VPL, bool SCORES, bool FULL>
+__global__ void __launch_bounds__(kThreads, VPL <= 8 ? 8 : VPL <= 16 ? 5 : 3)
+    route_kernel(const __grid_constant__ RouteArgs p, bool vec) {
+  __shared__ Picks picks[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int warps = gridDim.x * (kThreads / 32);
-  const int n = p.E - lane * VPL;   // (VPL at least, or none where rows are read as vectors)
+  const int n = FULL ? VPL : p.E - lane * VPL;   // (VPL at least, or none where rows are read as vectors)
+  picks[warp].entry[lane] = 0;
+  picks[warp].count = 0;
+  __syncwarp();
   wait_for_prior_grid();
-  float b[VPL];
-  load_row<VPL, float>(p.bias + lane * VPL, p.bias ? n : 0, vec, 0.f, b);
-  for (long long m = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); m < p.M; m += warps) {
+  Lane at = {lane, 1, true};
+  if (p.groups > p.topk_groups) {
+    const int size = p.E / p.groups;
+    at.span = max(1, size / VPL);
+    at.ok = size % VPL == 0 && (at.span & (at.span - 1)) == 0;
+  }
+  float b[VPL], l[VPL];
+  if (SCORES) {
+    load_row<VPL, float>(p.bias + lane * VPL, p.bias ? n : 0, vec, 0.f, b);
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) odd |= !(fabsf(b[i]) < INFINITY);
+    at.ok &= !__any_sync(kAll, odd);
+  }
+  long long m = (long long)blockIdx.x * (kThreads / 32) + warp;
+  if (m < p.M) load_logits<VPL>(p, m * p.ld + lane * VPL, n, vec, l);
+  for (; m < p.M; m += warps) {
+    float next[VPL];   // on its way meanwhile
+    if (m + warps < p.M) load_logits<VPL>(p, (m + warps) * p.ld + lane * VPL, n, vec, next);
     const long long row = m * p.ld;
-    float l[VPL];
-    load_row<VPL, V>(static_cast<const V *>(p.logits) + row + lane * VPL, n, vec, -INFINITY, l);
     Routed r;
-    if (route_token<float, VPL>(p, l, b, lane, row, &r.id, &r.weight)) r = route_token_64<VPL>(p, lane, row);
+    if (!at.ok || !route_fast<VPL, SCORES, FULL>(p, l, b, at, row, picks[warp], &r)) {
+      r = route_general<float, VPL>(p, row);
+      if (r.unsure) r = route_general<double, VPL>(p, row);
+    }
     if (lane < p.topk) {
       p.ids[m * p.topk + lane] = r.id;
       p.weights[m * p.topk + lane] = r.weight;
     }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = next[i];
   }
 }
 
@@ -326,8 +622,10 @@ template <int VPL>
 int launch_vpl(const RouteArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
   const bool vec = a.E % VPL == 0 && on16(a.logits) && on16(a.bias) && a.ld % (a.logits_f32 ? 4 : 8) == 0;
   const unsigned grid = (unsigned)std::min<long long>((a.M + kThreads / 32 - 1) / (kThreads / 32), dev.sm_count * 8ll);
-  return a.logits_f32 ? launch_dependent(route_kernel<VPL, float>, grid, kThreads, 1, 0, stream, a, vec)
-                      : launch_dependent(route_kernel<VPL, uint16_t>, grid, kThreads, 1, 0, stream, a, vec);
+  const bool scores = a.bias || (a.groups > a.topk_groups && a.best == 2), full = a.E == 32 * VPL;
+  const auto kernel = scores ? (full ? route_kernel<VPL, true, true> : route_kernel<VPL, true, false>)
+                             : (full ? route_kernel<VPL, false, true> : route_kernel<VPL, false, false>);
+  return launch_dependent(kernel, grid, kThreads, 1, 0, stream, a, vec);
 }
 
 }  // namespace
