@@ -295,8 +295,8 @@ __device__ __forceinline__ float order_sigmoid(float x) {
 
 // What does not depend on the token.
 struct Lane {
-  int lane, span;   // span: lanes of a group (a power of two)
-  bool ok;          // the fast form takes the groups and the bias
+  int lane, span, group;   // span: lanes of a group (a power of two); group: of this lane's experts
+  bool ok;                 // the fast form takes the groups and the bias
 };
 
 // Experts of a token that reach the bound: expert and choice, then a key (the
@@ -390,22 +390,20 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
       a2 = fmaxf(fmaxf(a2, b2), fminf(a1, b1));
       a1 = fmaxf(a1, b1);
     }
-    const int g = lane / at.span;                                              // of this lane's experts
     const float sums = p.best == 2 && a2 > -INFINITY ? a1 + a2 : a1;
-    float worth = __shfl_sync(kAll, sums, lane * at.span & 31);                // of group `lane`
+    float worth = __shfl_sync(kAll, sums, lane * at.span & 31);   // of group `lane`
     if (lane >= p.groups) worth = -INFINITY;
-    int before = 0;                                                            // groups that come before it
-#pragma unroll 4
-    for (int o = 0; o < p.groups; ++o) {
-      const float w = __shfl_sync(kAll, worth, o);
-      before += w > worth || (w == worth && o < lane);
+    uint32_t open = 0;
+    float rest = worth, stays = 0.f;
+    for (int k = 0; k < p.topk_groups; ++k) {
+      stays = warp_max(rest);
+      const int from = __ffs(__ballot_sync(kAll, rest == stays)) - 1;
+      open |= 1u << from;
+      if (lane == from) rest = -INFINITY;
     }
-    if (lane >= p.groups) before = 32;
     if (SCORES) {
       // the last that stays against the first that does not
-      const float stays = __shfl_sync(kAll, worth, __ffs(__ballot_sync(kAll, before == p.topk_groups - 1)) - 1);
-      const float goes = __shfl_sync(kAll, worth, __ffs(__ballot_sync(kAll, before == p.topk_groups)) - 1);
-      const float near = p.best * doubt(fmaxf(fabsf(stays), fabsf(goes)));
+      const float goes = warp_max(rest), near = p.best * doubt(fmaxf(fabsf(stays), fabsf(goes)));
       if (stays - goes <= near) {
         // The groups near them again, from exact choices of those experts that may be their best.
         const bool close = sums >= stays - near && sums <= goes + near;
@@ -425,20 +423,19 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
           for (; who; who &= who - 1) {
             const int from = __ffs(who) - 1;
             const double v = __shfl_sync(kAll, x, from);
-            if (from / at.span == lane) merge2(exact, second, v, (double)-INFINITY);
+            if (__shfl_sync(kAll, at.group, from) == lane) merge2(exact, second, v, (double)-INFINITY);
           }
         }
         if (p.best == 2 && second > -INFINITY) exact += second;
-        before = 0;
+        int before = 0;
         for (int o = 0; o < p.groups; ++o) {
           const double w = __shfl_sync(kAll, exact, o);
           before += w > exact || (w == exact && o < lane);
         }
-        if (lane >= p.groups) before = 32;
+        open = __ballot_sync(kAll, lane < p.groups && before < p.topk_groups);
       }
     }
-    const uint32_t open = __ballot_sync(kAll, before < p.topk_groups);
-    if (!(open >> g & 1)) {
+    if (!(open >> at.group & 1)) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) c[i] = -INFINITY;
     }
@@ -514,7 +511,10 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
   // (where the softmax's sum cancels, the largest of the chosen is as good as the row's)
   const float ref = SCORES || !p.renormalize ? top : __shfl_sync(kAll, logit, 0);
   float s = 0.f;
-  if (lane < p.topk) s = p.sigmoid ? sigmoid(logit) : expf(logit - ref);
+  if (lane < p.topk) {
+    const float e = expf(p.sigmoid ? -fabsf(logit) : logit - ref);
+    s = p.sigmoid ? __fdividef(logit < 0.f ? e : 1.f, 1.f + e) : e;
+  }
   float scale = p.scale;
   if (p.renormalize) {
     const float total = warp_sum(s);
@@ -582,10 +582,11 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 8 : VPL <= 16 ? 5 : 3)
   picks[warp].count = 0;
   __syncwarp();
   wait_for_prior_grid();
-  Lane at = {lane, 1, true};
+  Lane at = {lane, 1, 0, true};
   if (p.groups > p.topk_groups) {
     const int size = p.E / p.groups;
     at.span = max(1, size / VPL);
+    at.group = lane / at.span;
     at.ok = size % VPL == 0 && (at.span & (at.span - 1)) == 0;
   }
   float b[VPL], l[VPL];
