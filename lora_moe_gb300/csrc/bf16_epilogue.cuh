@@ -69,65 +69,84 @@ __device__ __forceinline__ void finish_one(const Bf16Args &p, int f, int e, int 
   store_one(p, f * p.ldy + n, o[0] * w + r);
 }
 
-// Whether four neighbouring elements, from a multiple of four on, of rows of p
-// can be read and written at once.
+// Rows of p, ld elements apart, whose elements can be read and written four at
+// a time, from a multiple of four on.
 __device__ __forceinline__ bool in_fours(const void *p, long long ld, int f32) {
   return (ld & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & (f32 ? 15 : 7)) == 0;
 }
 
-// Four columns from n on (a multiple of four) of the pairs f (negative: none),
-// whose sums v are.  All loads come before the first store: residual may be y.
-template <int B>
+// The sums' way out, four columns of a row of the output a thread: what the rows
+// allow is looked at once, so that the loops run through.
+enum { kOutSingly, kOutBf16, kOutF32 };
+__device__ __forceinline__ int out_kind(const Bf16Args &p) {
+  if (p.N % 4 != 0 || !in_fours(p.y, p.ldy, p.y_f32) || (p.residual && !in_fours(p.residual, p.ldr, p.y_f32)))
+    return kOutSingly;
+  return p.y_f32 ? kOutF32 : kOutBf16;
+}
+
+// Four columns from n on (a multiple of four, below N) of the pairs f (negative:
+// none), whose sums v are, times w (dense: not used).  All loads come before the first
+// store: residual may be y.
+template <int MODE, int KIND, int B>
 __device__ __forceinline__ void finish_fours(const Bf16Args &p, const int (&f)[B], const float (&w)[B], int n,
                                              const float (&bias)[4], float (&v)[4 * B]) {
-  const bool whole = n + 4 <= p.N;
-  float r[4 * B];
 #pragma unroll
-  for (int i = 0; i < 4 * B; ++i) r[i] = 0.f;
+  for (int i = 0; i < 4 * B; ++i) v[i] += bias[i & 3];
+  if (p.act != MOE_ACT_NONE) activate(v, p.act);
+  if (MODE != kDense) {
+#pragma unroll
+    for (int i = 0; i < 4 * B; ++i) v[i] *= w[i >> 2];
+  }
   if (p.residual) {
-    const bool fours = whole && in_fours(p.residual, p.ldr, p.y_f32);
+    if constexpr (KIND == kOutSingly) {
+      float r[4 * B];
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      if (f[b] < 0) continue;
-      const long long at = f[b] * p.ldr + n;
-      if (fours && p.y_f32) {
-        const float4 u = load_global(reinterpret_cast<const float4 *>(static_cast<const float *>(p.residual) + at));
-        r[4 * b] = u.x, r[4 * b + 1] = u.y, r[4 * b + 2] = u.z, r[4 * b + 3] = u.w;
-      } else if (fours) {
-        const uint2 u = load_global(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.residual) + at));
-        r[4 * b] = __uint_as_float(u.x << 16), r[4 * b + 1] = __uint_as_float(u.x & 0xFFFF0000u);
-        r[4 * b + 2] = __uint_as_float(u.y << 16), r[4 * b + 3] = __uint_as_float(u.y & 0xFFFF0000u);
-      } else {
+      for (int i = 0; i < 4 * B; ++i)
+        r[i] = f[i >> 2] >= 0 && n + (i & 3) < p.N ? load_as_f32(p.residual, f[i >> 2] * p.ldr + n + (i & 3), p.y_f32) : 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n + i < p.N) r[4 * b + i] = load_as_f32(p.residual, at + i, p.y_f32);
+      for (int i = 0; i < 4 * B; ++i) v[i] += r[i];
+    } else if constexpr (KIND == kOutF32) {
+      float4 r[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b)   // (for no pair: another's, not used)
+        r[b] = load_global(reinterpret_cast<const float4 *>(static_cast<const float *>(p.residual) + max(f[b], 0) * p.ldr + min(n, p.N - 4)));
+#pragma unroll
+      for (int b = 0; b < B; ++b) v[4 * b] += r[b].x, v[4 * b + 1] += r[b].y, v[4 * b + 2] += r[b].z, v[4 * b + 3] += r[b].w;
+    } else {
+      uint2 r[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        r[b] = load_global(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.residual) + max(f[b], 0) * p.ldr + min(n, p.N - 4)));
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        v[4 * b] += __uint_as_float(r[b].x << 16), v[4 * b + 1] += __uint_as_float(r[b].x & 0xFFFF0000u);
+        v[4 * b + 2] += __uint_as_float(r[b].y << 16), v[4 * b + 3] += __uint_as_float(r[b].y & 0xFFFF0000u);
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4 * B; ++i) v[i] += bias[i & 3];
-  activate(v, p.act);
-  const bool fours = whole && in_fours(p.y, p.ldy, p.y_f32);
-#pragma unroll
   for (int b = 0; b < B; ++b) {
-    if (f[b] < 0) continue;
-    const long long at = f[b] * p.ldy + n;
-    float o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = v[4 * b + i] * w[b] + r[4 * b + i];
-    if (fours && p.y_f32) {
-      *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + at) = make_float4(o[0], o[1], o[2], o[3]);
-    } else if (fours) {
-      uint2 u;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(o[1]), "f"(o[0]));
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(o[3]), "f"(o[2]));
-      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.y) + at) = u;
-    } else {
+    if constexpr (KIND == kOutSingly) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (n + i < p.N) store_one(p, at + i, o[i]);
+        if (f[b] >= 0 && n + i < p.N) store_one(p, f[b] * p.ldy + n + i, v[4 * b + i]);
+    } else if constexpr (KIND == kOutF32) {
+      if (f[b] >= 0)
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + f[b] * p.ldy + n) =
+            make_float4(v[4 * b], v[4 * b + 1], v[4 * b + 2], v[4 * b + 3]);
+    } else {
+      uint2 u;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(v[4 * b + 1]), "f"(v[4 * b]));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(v[4 * b + 3]), "f"(v[4 * b + 2]));
+      if (f[b] >= 0) *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.y) + f[b] * p.ldy + n) = u;
     }
   }
+}
+
+// Fetches the residual's line at column n of row f into L2, while the sums are on their way.
+__device__ __forceinline__ void fetch_residual(const Bf16Args &p, int f, int n) {
+  const char *at = static_cast<const char *>(p.residual) + (f * p.ldr + n) * (p.y_f32 ? 4 : 2);
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
 }
 
 }  // namespace moe_lora

@@ -20,6 +20,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "bf16.h"
 #include "bf16_epilogue.cuh"
@@ -38,7 +39,7 @@ constexpr int kGroupBytes = kBf16Group * 2;       // of a row
 constexpr int kTileBytes = kRows * kGroupBytes;   // 128 rows of one group: 16 KB
 
 struct Bf16Maps {
-  CUtensorMap w;   // [E][N][K] in bytes, box 1 x 128 x 128
+  CUtensorMap w;      // [E][N][K] in bytes, box 1 x 128 x 128
   CUtensorMap x[4];   // [rows][K], box BT x 128 (dense), 1 x 128 (gathered by row); wide: 128, 64, 32 and 16 x 128
 };
 
@@ -56,7 +57,7 @@ struct Bf16Cfg {
 
 // ------------------------------------------------------------------ narrow
 
-constexpr int kMaxRing = 12;
+constexpr int kMaxRing = 5;    // stages: 5 gave 264 us, 4 265, 3 272, 6 272 and 12 278 (64 tokens, 4 of 128 experts of 2880 x 2880)
 constexpr int kMaxSmem = 227 * 1024;
 // Groups of K whose products the tensor cores add up.  Their additions truncate,
 // so a long sum drifts; the epilogue adds the chunks in fp32, rounding to nearest.
@@ -230,22 +231,29 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     const int row = (warp - 4) * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(warp - 4) << 21);   // lane offset 32 * quarter in bits 16..31
     float *sums = reinterpret_cast<float *>(smem + cfg.off_tile);     // [this CTA's positions][kRows]
+    const int out = out_kind(p);
     int a = 0;
     uint32_t aph = 0;
     while (wk.advance()) {
       const int ui = wk.it / cfg.nt, nt = wk.it - ui * cfg.nt, b = unit(ui), e = block_expert<MODE>(p, b, BT);
       if (e < 0) continue;
-      // pairs of positions `lane` and lane + 32, and biases of the four rows
+      // the pair of position `lane` (dense: not used), and biases of the four rows
       const int n = nt * kRows + lane * 4;
-      int pair[2];
-      float weight[2], bias[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        pair[i] = lane + 32 * i < BT ? block_pair<MODE>(p, b, lane + 32 * i, BT) : -1;
-        weight[i] = pair[i] < 0 ? 0.f : pair_weight<MODE>(p, pair[i]);
+      int pair = -1;
+      float weight = 0.f, bias[4];
+      if (MODE != kDense) {
+        static_assert(MODE == kDense || BT <= 32, "a lane for each position");
+        pair = lane < BT ? block_pair<MODE>(p, b, lane, BT) : -1;
+        weight = pair < 0 ? 0.f : pair_weight<MODE>(p, pair);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) bias[i] = bias_of(p, e, n + i);
+      if (MODE == kDense && p.residual) {   // this warp's rows of it, 64 bytes a lane
+        const int from = cs == 1 ? 0 : join_first(BT, cs, wk.rank), to = cs == 1 ? BT : join_first(BT, cs, wk.rank + 1);
+        const int at = nt * kRows + (lane & 7) * (p.y_f32 ? 16 : 32);
+        for (int t = from + (warp - 4) * 4 + (lane >> 3); t < to; t += 16)
+          if (at < min(p.N, (nt + 1) * kRows) && b * BT + t < p.pairs) fetch_residual(p, b * BT + t, at);
+      }
       float acc[BT];
 #pragma unroll
       for (int c = 0; c < BT; ++c) acc[c] = 0.f;
@@ -285,24 +293,30 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         waited = true;
       }
       named_barrier(1, 128);
+      auto put_out = [&](auto kind) {
 #pragma unroll 1
-      for (int c = first + warp - 4; c < last; c += 16) {
-        int f[4];
-        float w[4], v[16];
+        for (int c = first + warp - 4; c < last; c += 16) {
+          int f[4];
+          float w[4], v[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = c + 4 * i;
-          const int lo = __shfl_sync(0xFFFFFFFFu, pair[0], t & 31), hi = __shfl_sync(0xFFFFFFFFu, pair[1], t & 31);
-          const float wlo = __shfl_sync(0xFFFFFFFFu, weight[0], t & 31), whi = __shfl_sync(0xFFFFFFFFu, weight[1], t & 31);
-          f[i] = t >= last ? -1 : (t < 32 ? lo : hi);
-          w[i] = t < 32 ? wlo : whi;
-          if (t < last) {
-            const float4 u = *reinterpret_cast<const float4 *>(sums + (t - first) * kRows + lane * 4);
+          for (int i = 0; i < 4; ++i) {
+            const int t = c + 4 * i;
+            if (MODE == kDense) {
+              f[i] = b * BT + t < p.pairs ? b * BT + t : -1;
+            } else {
+              f[i] = __shfl_sync(0xFFFFFFFFu, pair, t & 31);
+              w[i] = __shfl_sync(0xFFFFFFFFu, weight, t & 31);
+            }
+            if (t >= last || n >= p.N) f[i] = -1;
+            const float4 u = *reinterpret_cast<const float4 *>(sums + (min(t, last - 1) - first) * kRows + lane * 4);
             v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
           }
+          finish_fours<MODE, decltype(kind)::value, 4>(p, f, w, n, bias, v);
         }
-        finish_fours<4>(p, f, w, n, bias, v);
-      }
+      };
+      if (out == kOutBf16) put_out(std::integral_constant<int, kOutBf16>());
+      else if (out == kOutF32) put_out(std::integral_constant<int, kOutF32>());
+      else put_out(std::integral_constant<int, kOutSingly>());
     }
   }
   if (cs > 1 && !waited) cluster_wait();
@@ -529,6 +543,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     float *stage = reinterpret_cast<float *>(smem + cfg.off_tile + (warp - 4) * kPartBytes);   // [pair][row]
     int a = 0;
     uint32_t aph = 0;
+    const int out = out_kind(p);
     bool met = false;   // the cluster's pairs, at the barrier that frees the ring
     while (wk.advance()) {
       const WideTile t = tile(wk.t);
@@ -544,30 +559,48 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         a ^= 1;
         if (a == 0) aph ^= 1;
       };
-      // The sums of part i, which the warp has put into `stage`; the pair that lane j has: its row of y, or -1.
+      // The sums of part i, which the warp has put into `stage`.
       auto put_out = [&](int i) {
-        const int r = (2 * i + half) * kPart + lane;
+        const int r0 = (2 * i + half) * kPart;
         int f = -1;
-        if (r < t.rows) f = MODE == kDense ? t.row0 + r : load_global(p.sorted_token_ids + t.row0 + r);
-        if ((unsigned)f >= (unsigned)p.pairs) f = -1;
-        const float weight = f < 0 ? 0.f : pair_weight<MODE>(p, f);
-        __syncwarp();
-#pragma unroll 1
-        for (int j0 = 0; j0 < kPart; j0 += 16) {
-          int fj[4];
-          float w[4], v[16];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int j = j0 + 4 * k + (lane >> 3);
-            fj[k] = __shfl_sync(0xFFFFFFFFu, f, j);
-            w[k] = __shfl_sync(0xFFFFFFFFu, weight, j);
-            const float4 u = *reinterpret_cast<const float4 *>(stage + j * 32 + (lane & 7) * 4);
-            v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
-          }
-          finish_fours<4>(p, fj, w, n, bias, v);
+        float weight = 0.f;
+        if (MODE != kDense) {
+          if (r0 + lane < t.rows) f = load_global(p.sorted_token_ids + t.row0 + r0 + lane);
+          if ((unsigned)f >= (unsigned)p.pairs) f = -1;
+          if (f >= 0) weight = pair_weight<MODE>(p, f);
         }
         __syncwarp();
+        auto rows = [&](auto kind) {
+#pragma unroll 1
+          for (int j0 = 0; j0 < kPart; j0 += 16) {
+            int fj[4];
+            float w[4], v[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int j = j0 + 4 * k + (lane >> 3);
+              if (MODE == kDense) {
+                fj[k] = r0 + j < t.rows ? t.row0 + r0 + j : -1;
+              } else {
+                fj[k] = __shfl_sync(0xFFFFFFFFu, f, j);
+                w[k] = __shfl_sync(0xFFFFFFFFu, weight, j);
+              }
+              if (n >= p.N) fj[k] = -1;
+              const float4 u = *reinterpret_cast<const float4 *>(stage + j * 32 + (lane & 7) * 4);
+              v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
+            }
+            finish_fours<MODE, decltype(kind)::value, 4>(p, fj, w, n, bias, v);
+          }
+        };
+        if (out == kOutBf16) rows(std::integral_constant<int, kOutBf16>());
+        else if (MODE == kDense && out == kOutF32) rows(std::integral_constant<int, kOutF32>());
+        else rows(std::integral_constant<int, kOutSingly>());
+        __syncwarp();
       };
+      if (MODE == kDense && p.residual) {
+        const int at = wk.nt * kWideN + rank * kRows + quarter * 32;
+        for (int r = half * kPart + lane; r < t.rows; r += 2 * kPart)
+          if (at < p.N) fetch_residual(p, t.row0 + r, at);
+      }
       if constexpr (!CHUNKED) {
         mbar_wait(&ctl.tfull[a], aph, abort, p.err);
         tc_fence_after();
@@ -772,12 +805,16 @@ void wide_shape(const Bf16Args &a, Kernel kernel, bool chunked, const DeviceInfo
   }
 }
 
+// Height of a sorted call's tiles.
+int sorted_height(const Bf16Args &a) { return a.pairs <= 96ll * a.E ? 128 : kTileRows; }
+
 template <int MODE, bool CHUNKED>
 int launch_wide(const Bf16Args &a, void *workspace, const DeviceInfo &dev, cudaStream_t stream) {
   const auto kernel = bf16_wide_kernel<MODE, CHUNKED>;
   Bf16Cfg cfg = {};
   cfg.nt = (a.N + kWideN - 1) / kWideN;
-  const long long tiles = tile_bound(a, MODE == kSorted);
+  const int height = MODE == kSorted ? sorted_height(a) : kTileRows;
+  const long long tiles = tile_bound(a, MODE == kSorted, height);
   if (tiles <= 0) return 0;
   // a ring as long as fits, of stages for the highest tile
   auto ring = [&](int rows) {
@@ -788,7 +825,7 @@ int launch_wide(const Bf16Args &a, void *workspace, const DeviceInfo &dev, cudaS
     cfg.off_ctrl = cfg.off_tile + 8 * kPartBytes;
     cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(WideCtrl);
   };
-  ring(kTileRows);
+  ring(height);
   if (CHUNKED) {
     static const bool fits = register_shares_fit(kernel);
     if (!fits) return MOE_LORA_ERR_LAUNCH;
@@ -804,7 +841,7 @@ int launch_wide(const Bf16Args &a, void *workspace, const DeviceInfo &dev, cudaS
     uint8_t *base = static_cast<uint8_t *>(workspace);
     list = reinterpret_cast<const WideTile *>(base);
     if (int st = make_maps(a, base + w.x, rows, w.ld, kRows, 4, &maps)) return st;
-    if (int st = launch_gather(a, a.x, 2 * a.ldx, 2ll * a.K, workspace, dev, stream)) return st;
+    if (int st = launch_gather(a, a.x, 2 * a.ldx, 2ll * a.K, height, workspace, dev, stream)) return st;
   }
   cfg.cluster = 2;
   long long items = tiles * cfg.nt;   // (the sorted arrays' own tiles are no more, but for entries that no align writes)
@@ -827,7 +864,7 @@ bool sorted_is_wide(const Bf16Args &a) {
 
 // Up to this many bytes of weights, calls of single pairs or of at most 16 rows
 // run the kernel that streams the weight through registers.
-constexpr double kStreamBytes = 32e6;
+constexpr double kStreamBytes = 256e6;
 
 }  // namespace
 
@@ -837,7 +874,7 @@ size_t bf16_sorted_workspace(const Bf16Args &a) {
 
 bool bf16_items_fit(const Bf16Args &a, ProductMode mode) {
   if (mode == kDense ? a.pairs > 64 : mode == kSorted && sorted_is_wide(a))
-    return tile_bound(a, mode == kSorted) * ((a.N + kWideN - 1) / kWideN) <= INT32_MAX / 16;
+    return tile_bound(a, mode == kSorted, mode == kSorted ? sorted_height(a) : 64) * ((a.N + kWideN - 1) / kWideN) <= INT32_MAX / 16;
   // every unit that the sorted arrays can hold, whatever they hold
   const long long units = mode == kSorted ? (long long)a.max_blocks * (a.block / 16) : unit_bound(a, mode, 16);
   return units * ((a.N + kRows - 1) / kRows) <= INT32_MAX;
@@ -856,7 +893,7 @@ int launch_bf16_matmul(const Bf16Args &a, ProductMode mode, void *workspace, con
   if (a.pairs <= 64) return launch_narrow<64, kDense>(a, dev, s);
   // chunks where the output is fp32 (all of K added up by the tensor cores is
   // 2.4e-5 off for 7168 products of one sign), or where K is split
-  const long long items = tile_bound(a, false) * ((a.N + kWideN - 1) / kWideN);
+  const long long items = tile_bound(a, false, kTileRows) * ((a.N + kWideN - 1) / kWideN);
   if (a.y_f32 || items * 4 <= dev.sm_count) return launch_wide<kDense, true>(a, nullptr, dev, s);
   return launch_wide<kDense, false>(a, nullptr, dev, s);
 }

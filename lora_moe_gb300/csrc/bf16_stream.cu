@@ -39,11 +39,15 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // RG groups of 16 weight rows a CTA, K split over its other warps; NT tiles of 8 pairs.
+// Groups of K in flight a warp, and registers for two CTAs an SM (three for
+// single pairs, whose items are many), measured best of 2 to 4 groups and 2 or 3
+// CTAs (1 x 4096 x 4096 7.3 us with four groups, 7.5 with two; 16 rows 14.4 and
+// 9.3; single pairs 10.8 and 9.7).
 constexpr int ctas_per_sm(int mode) { return mode == kNaive ? 3 : 2; }
-constexpr int kUnroll = 2;   // groups of K in flight a warp
+constexpr int unroll(int mode, int nt) { return mode == kNaive || nt > 1 ? 2 : 4; }
 template <int NT, int RG, int MODE>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) bf16_stream_kernel(const Bf16Args p, int tiles) {
-  constexpr int KS = kWarps / RG, kRowsCta = 16 * RG, U = kUnroll;
+  constexpr int KS = kWarps / RG, kRowsCta = 16 * RG, U = unroll(MODE, NT);
   __shared__ float red[kWarps][8 * NT][16 + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rg = warp % RG, ks = warp / RG;

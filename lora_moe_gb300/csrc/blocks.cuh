@@ -34,10 +34,10 @@ inline long long unit_bound(const PairBlocks &a, ProductMode mode, int bt) {
   return std::min<long long>(a.max_blocks, fused_block_bound(a.pairs, 1, a.E, 1, a.block)) * (a.block / bt);
 }
 
-constexpr int kTileRows = 256;   // rows of the wide kernels' tiles
-// Upper bound of the wide kernels' tiles of rows.
-inline long long tile_bound(const PairBlocks &a, bool sorted) {
-  return sorted ? a.pairs / kTileRows + std::min(a.E, a.pairs) : ((long long)a.pairs + kTileRows - 1) / kTileRows;
+constexpr int kTileRows = 256;   // most rows of the wide kernels' tiles
+// Upper bound of the wide kernels' tiles of `rows` rows.
+inline long long tile_bound(const PairBlocks &a, bool sorted, int rows) {
+  return sorted ? a.pairs / rows + std::min(a.E, a.pairs) : ((long long)a.pairs + rows - 1) / rows;
 }
 
 // Blocks that the sorted arrays hold.

@@ -655,7 +655,7 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
   Fp8Cfg cfg = {};
   cfg.nt = (a.N + kWideN - 1) / kWideN;
   const long long rows = (long long)a.max_blocks * a.block;
-  const long long tiles = tile_bound(a, MODE == kSorted);
+  const long long tiles = tile_bound(a, MODE == kSorted, kTileRows);
   if (tiles <= 0) return 0;
   cfg.stages = kWideStages;
   cfg.off_ctrl = kWideStages * kWideStage + 8 * kWideOut;
@@ -672,7 +672,7 @@ int launch_wide(const Fp8Args &a, void *workspace, const DeviceInfo &dev, cudaSt
     uint8_t *base = static_cast<uint8_t *>(workspace);
     g.tiles = reinterpret_cast<WideTile *>(base);
     if (int st = make_maps(a, base + w.x, rows, w.ld, kHalf / 2, kRows, &maps)) return st;
-    if (int st = launch_gather(a, a.x, a.ldx, a.K, workspace, dev, stream)) return st;
+    if (int st = launch_gather(a, a.x, a.ldx, a.K, kTileRows, workspace, dev, stream)) return st;
   }
   const long long items = tiles * cfg.nt;   // (the sorted arrays' own tiles are no more, but for entries that no align writes)
   const unsigned grid = 2 * (unsigned)std::min<long long>(items, dev.sm_count / 2);
@@ -712,7 +712,7 @@ size_t fp8_sorted_workspace(const Fp8Args &a) {
 
 bool fp8_items_fit(const Fp8Args &a, ProductMode mode) {
   if (mode == kDense ? a.pairs > 64 : mode == kSorted && fp8_sorted_is_wide(a))
-    return tile_bound(a, mode == kSorted) * ((a.N + kWideN - 1) / kWideN) <= INT32_MAX / 16;
+    return tile_bound(a, mode == kSorted, kTileRows) * ((a.N + kWideN - 1) / kWideN) <= INT32_MAX / 16;
   // every unit that the sorted arrays can hold, whatever they hold
   const long long units = mode == kSorted ? (long long)a.max_blocks * (a.block / 16) : unit_bound(a, mode, 16);
   return units * ((a.N + kRows - 1) / kRows) <= INT32_MAX;

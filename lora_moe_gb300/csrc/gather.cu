@@ -2,7 +2,7 @@
 // sorted_token_ids: the wide kernels read each of them N / 256 times, and TMA
 // fetches gathered rows four at a time at 80 clk each, cp.async by the 8-bit
 // kernel's own warps at 40 % of the tensor cores' time.  CTA 0 also lists the
-// tiles of at most 256 rows of one expert.  Bound by the rows' bytes.
+// tiles of at most tile_rows rows of one expert.  Bound by the rows' bytes.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -18,20 +18,20 @@ namespace {
 constexpr int kGatherThreads = 256;
 
 __global__ void __launch_bounds__(kGatherThreads)
-    gather_kernel(const PairBlocks p, const uint8_t *x, long long row_bytes, long long bytes, WideTile *tiles, uint8_t *xg,
-                  long long ld) {
+    gather_kernel(const PairBlocks p, const uint8_t *x, long long row_bytes, long long bytes, int tile_rows, WideTile *tiles,
+                  uint8_t *xg, long long ld) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bs = p.block;
   wait_for_prior_grid();
   const int nb = num_blocks(p);
   if (blockIdx.x == 0) {
     // Tile list.  Blocks of one expert are neighbours: a run.  A block heads a
-    // tile when the blocks before it in its run are a multiple of 256 rows; the
+    // tile when the blocks before it in its run are a multiple of tile_rows rows; the
     // last block of a tile writes it down.
     __shared__ int warp_last[kGatherThreads / 32], warp_heads[kGatherThreads / 32], carry_first, carry_heads;
     if (tid == 0) carry_first = carry_heads = 0;
     __syncthreads();
-    const int per_tile = kTileRows / bs;
+    const int per_tile = tile_rows / bs;
     for (int base = 0; base < nb; base += kGatherThreads) {
       const int b = base + tid;
       const int e = b < nb ? load_global(p.expert_ids + b) : -1;
@@ -98,14 +98,14 @@ GatherSpace gather_space(long long rows, long long bytes) {
   return w;
 }
 
-int launch_gather(const PairBlocks &a, const void *x, long long row_bytes, long long bytes, void *workspace,
+int launch_gather(const PairBlocks &a, const void *x, long long row_bytes, long long bytes, int tile_rows, void *workspace,
                   const DeviceInfo &dev, cudaStream_t stream) {
   const long long rows = (long long)a.max_blocks * a.block;
   const GatherSpace w = gather_space(rows, bytes);
   uint8_t *base = static_cast<uint8_t *>(workspace);
   return launch_dependent(gather_kernel, (unsigned)std::min<long long>((rows + 7) / 8, dev.sm_count * 8ll),
                           kGatherThreads, 1, 0, stream, a, static_cast<const uint8_t *>(x), row_bytes, bytes,
-                          reinterpret_cast<WideTile *>(base), base + w.x, w.ld);
+                          tile_rows, reinterpret_cast<WideTile *>(base), base + w.x, w.ld);
 }
 
 }  // namespace moe_lora

@@ -11,7 +11,7 @@
 
 namespace moe_lora {
 
-// At most kTileRows rows of one expert, from row row0 of the gathered ones.
+// Neighbouring rows of one expert, from row row0 of the gathered ones.
 struct WideTile {
   int row0, rows, expert, pad;
 };
@@ -22,8 +22,8 @@ struct GatherSpace {
   long long ld;      // bytes from row to row
 };
 GatherSpace gather_space(long long rows, long long bytes);   // rows: capacity of the sorted arrays in whole blocks
-// Rows of `bytes` bytes, row_bytes apart.
-int launch_gather(const PairBlocks &a, const void *x, long long row_bytes, long long bytes, void *workspace,
+// Rows of `bytes` bytes, row_bytes apart; tiles of at most tile_rows, a multiple of the block.
+int launch_gather(const PairBlocks &a, const void *x, long long row_bytes, long long bytes, int tile_rows, void *workspace,
                   const DeviceInfo &dev, cudaStream_t stream);
 
 }  // namespace moe_lora

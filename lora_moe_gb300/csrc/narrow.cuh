@@ -63,6 +63,10 @@ struct NarrowWork {
 // cs CTAs has more than BT / 4; rank q of the cluster has the units [U * q / cs,
 // U * (q + 1) / cs).
 __host__ __device__ constexpr int join_width(int BT, int cs) { return BT / 4 >= cs ? 4 : 2; }
+__device__ __forceinline__ int join_first(int BT, int cs, int rank) {
+  const int W = join_width(BT, cs);
+  return BT / W * rank / cs * W;
+}
 // Bytes that join_ranks() needs in each CTA (SINGLE: one position).
 __host__ __device__ constexpr int join_bytes(int BT, int cs, bool single) {
   return single ? cs * kRows * 4
@@ -92,12 +96,14 @@ __device__ __forceinline__ void join_ranks(const float (&acc)[BT], int cs, int r
   } else {
     auto run = [&](auto width) {
       constexpr int W = decltype(width)::value, U = BT / W;
-      const int first = U * rank / cs, own = U * (rank + 1) / cs - first;
+      const uint32_t inv = (65535u + cs) / cs;   // x / cs is x * inv >> 16 for the x here, at most 128
+      auto start = [&](int q) { return (int)(U * q * inv >> 16); };   // rank q's first unit
+      const int first = start(rank), own = start(rank + 1) - first;
       if (row == 0) mbar_arrive_expect_tx(red_full, own * cs * W * kRows * 4);
       cluster_wait();
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int q = ((u + 1) * cs - 1) / U, at = u - U * q / cs, of = U * (q + 1) / cs - U * q / cs;
+        const int q = ((u + 1) * cs - 1) / U, s = start(q), at = u - s, of = start(q + 1) - s;
         const uint32_t dst = cluster_map(red_base + ((rank * of + at) * kRows + row) * W * 4, q), bar = cluster_map(red_bar, q);
         if constexpr (W == 4)
           st_async_v4(dst, make_float4(acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]), bar);
