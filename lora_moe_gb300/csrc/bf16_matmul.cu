@@ -182,11 +182,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     }
     // the copies have landed, the stages' hand-backs arrived and the MMAs completed before this CTA exits
     __syncwarp();
-    if (lane == 0) {
-      drain_ring(ctl.full, cfg.stages, fills);
-      drain_ring(ctl.empty, cfg.stages, fills);
-      drain_wait(&ctl.done, 0);
-    }
+    drain_ring_warp(ctl.full, cfg.stages, fills, lane);
+    drain_ring_warp(ctl.empty, cfg.stages, fills, lane);
+    drain_wait(&ctl.done, 0);
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA: each chunk of K into an accumulator of its own
@@ -417,11 +415,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     if (lane < 5) prefetch_tensor_map(lane < 4 ? &maps.x[lane] : &maps.w);
     fence_barrier_init();
   }
+  __syncthreads();
+  cluster_arrive_release();   // the barriers are initialised
   if (warp == 1) tmem_alloc_pair(&ctl.tmem, 512);
   tc_fence_before();
-  __syncthreads();
-  cluster_arrive_release();
   cluster_wait();
+  __syncthreads();
   tc_fence_after();
   wait_for_prior_grid();
   const uint32_t tmem = ctl.tmem;
@@ -488,11 +487,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // hand-backs of the last stages have arrived here and the MMAs have
       // completed before the pair exits: the epilogue waits for neither.
       __syncwarp();
-      if (lane == 0) {
-        if (rank == 0) drain_ring(ctl.full, stages, fills);
-        drain_ring(ctl.empty, stages, fills);
-        drain_wait(&ctl.done, 0);
-      }
+      if (rank == 0) drain_ring_warp(ctl.full, stages, fills, lane);
+      drain_ring_warp(ctl.empty, stages, fills, lane);
+      drain_wait(&ctl.done, 0);
     } else if (warp == 1 && rank == 0) {
       // ---------------- MMA, for both CTAs
       const uint64_t desc0 = make_sdesc_sw128(smem_addr(smem));   // (addresses in units of 16 bytes)
@@ -559,32 +556,34 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         a ^= 1;
         if (a == 0) aph ^= 1;
       };
-      // The sums of part i, which the warp has put into `stage`.
-      auto put_out = [&](int i) {
-        const int r0 = (2 * i + half) * kPart;
+      // The sums of `count` pairs (a multiple of 8) that the warp has put into
+      // `stage`: pair k is number off + k % 2^lg of part i + k / 2^lg.
+      auto put_out = [&](int i, int off, int lg, int count) {
+        auto row = [&](int k) { return (2 * (i + (k >> lg)) + half) * kPart + off + (k & ((1 << lg) - 1)); };   // of the tile
         int f = -1;
         float weight = 0.f;
         if (MODE != kDense) {
-          if (r0 + lane < t.rows) f = load_global(p.sorted_token_ids + t.row0 + r0 + lane);
+          const int r = row(lane);
+          if (lane < count && r < t.rows) f = load_global(p.sorted_token_ids + t.row0 + r);
           if ((unsigned)f >= (unsigned)p.pairs) f = -1;
           if (f >= 0) weight = pair_weight<MODE>(p, f);
         }
         __syncwarp();
         auto rows = [&](auto kind) {
 #pragma unroll 1
-          for (int j0 = 0; j0 < kPart; j0 += 16) {
+          for (int j0 = 0; j0 < count; j0 += 16) {
             int fj[4];
             float w[4], v[16];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int j = j0 + 4 * k + (lane >> 3);
               if (MODE == kDense) {
-                fj[k] = r0 + j < t.rows ? t.row0 + r0 + j : -1;
+                fj[k] = row(j) < t.rows ? t.row0 + row(j) : -1;
               } else {
                 fj[k] = __shfl_sync(0xFFFFFFFFu, f, j);
                 w[k] = __shfl_sync(0xFFFFFFFFu, weight, j);
               }
-              if (n >= p.N) fj[k] = -1;
+              if (n >= p.N || j >= count) fj[k] = -1;
               const float4 u = *reinterpret_cast<const float4 *>(stage + j * 32 + (lane & 7) * 4);
               v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
             }
@@ -614,7 +613,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           tc_pin(raw);
 #pragma unroll
           for (int j = 0; j < kPart; ++j) stage[j * 32 + lane] = __uint_as_float(raw[j]);
-          put_out(i);
+          put_out(i, 0, 5, kPart);
         }
         hand_back();
       } else {
@@ -642,49 +641,58 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           hand_back();
         }
         if (pairs > 1) {
-          // The parts that exist are dealt to the pairs in turn.  A sum's place: [part of the owner][source][quad][this
-          // thread].  One item a cluster, so that the memory is used once; what is sent to a CTA is waited for there.
-          const int live = max(0, (cols / kPart - half + 1) / 2);              // of this warp
-          const int all = cols / kPart;                                        // of both warps of the lane quarter
-          const int mine = (all + 1) / 2 > q ? ((all + 1) / 2 - q - 1) / pairs + 1 : 0;   // of half 0, of this pair
-          const int mine1 = all / 2 > q ? (all / 2 - q - 1) / pairs + 1 : 0;
-          if (tid == kWideThreads - 1) mbar_arrive_expect_tx(&ctl.red_full, (mine + mine1) * pairs * kPart * 128 * 4);
+          // Pair q has its share of every part's columns: `own` quads from q * own on.  A sum's place: [quad of the
+          // owner's][source][this thread].  One item a cluster, so that the memory is used once; what is sent to a CTA
+          // is waited for there.
+          const int lg = pairs == 2 ? 2 : 1, own = 1 << lg;
+          const int live = max(0, (cols / kPart - half + 1) / 2);   // parts of this warp
+          if (tid == kWideThreads - 1)
+            mbar_arrive_expect_tx(&ctl.red_full, cols / kPart * own * (pairs - 1) * 128 * 16);
           cluster_arrive_release();
           cluster_wait();
           met = true;
-          const uint32_t base = smem_addr(smem) + (tid - 128) * 16, bar = smem_addr(&ctl.red_full);
+          uint8_t *here = smem + (tid - 128) * 16;
+          const uint32_t base = smem_addr(here), bar = smem_addr(&ctl.red_full);
+#pragma unroll 1   // (code that runs once a launch is fetched as it runs)
+          for (int part = 0; part < live; ++part) {
+            float4 *mine = reinterpret_cast<float4 *>(stage) + lane;   // [quad][this thread]
 #pragma unroll
-          for (int i = 0; i < kParts; ++i) {
-            if (i >= live) continue;
-            const int to = i & (pairs - 1), at = i / pairs;
-            const uint32_t dst = cluster_map(base, to * 2 + rank), rbar = cluster_map(bar, to * 2 + rank);
+            for (int i = 0; i < kParts; ++i) {
+              if (i != part) continue;
 #pragma unroll
+              for (int j = 0; j < kPart / 4; ++j) {
+                float4 u;
+                f2_unpack(acc[i][2 * j], u.x, u.y);
+                f2_unpack(acc[i][2 * j + 1], u.z, u.w);
+                mine[j * 32] = u;
+              }
+            }
+#pragma unroll 2
             for (int j = 0; j < kPart / 4; ++j) {
-              float4 v;
-              f2_unpack(acc[i][2 * j], v.x, v.y);
-              f2_unpack(acc[i][2 * j + 1], v.z, v.w);
-              st_async_v4(dst + ((at * pairs + q) * (kPart / 4) + j) * 4096, v, rbar);
+              const int to = j >> lg, at = (((part << lg) + (j & (own - 1))) * pairs + q) * 4096;
+              const float4 u = mine[j * 32];
+              if (to == q) *reinterpret_cast<float4 *>(here + at) = u;
+              else st_async_v4(cluster_map(base + at, to * 2 + rank), u, cluster_map(bar, to * 2 + rank));
             }
           }
-          if (mine + mine1 > 0) mbar_wait_cluster(&ctl.red_full, 0, abort, p.err);
+          __syncwarp();
+          mbar_wait_cluster(&ctl.red_full, 0, abort, p.err);
 #pragma unroll 1
-          for (int i = q; i < live; i += pairs) {
-            const uint8_t *from = smem + (tid - 128) * 16 + (i / pairs) * pairs * (kPart / 4) * 4096;
+          for (int j0 = 0; j0 < live * own; j0 += kPart / 4) {   // 32 pairs at a time
+            const int some = min(kPart / 4, live * own - j0);
 #pragma unroll 1
-            for (int j = 0; j < kPart / 4; ++j) {
+            for (int j = 0; j < some; ++j) {
               float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
               for (int src = 0; src < 4; ++src) {
                 if (src >= pairs) break;
-                const float4 u = *reinterpret_cast<const float4 *>(from + (src * (kPart / 4) + j) * 4096);
+                const float4 u = *reinterpret_cast<const float4 *>(here + ((j0 + j) * pairs + src) * 4096);
                 v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
               }
-              stage[(4 * j) * 32 + lane] = v.x;
-              stage[(4 * j + 1) * 32 + lane] = v.y;
-              stage[(4 * j + 2) * 32 + lane] = v.z;
-              stage[(4 * j + 3) * 32 + lane] = v.w;
+              float *to = stage + j * 4 * 32 + lane;
+              to[0] = v.x, to[32] = v.y, to[64] = v.z, to[96] = v.w;
             }
-            put_out(i);
+            put_out(j0 >> lg, q * own * 4, lg + 2, some * 4);
           }
         } else {
 #pragma unroll 1
@@ -701,7 +709,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 stage[(2 * j + 1) * 32 + lane] = hi;
               }
             }
-            put_out(part);
+            put_out(part, 0, 5, kPart);
           }
         }
       }
