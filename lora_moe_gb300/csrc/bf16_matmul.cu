@@ -557,9 +557,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (a == 0) aph ^= 1;
       };
       // The sums of `count` pairs (a multiple of 8) that the warp has put into
-      // `stage`: pair k is number off + k % 2^lg of part i + k / 2^lg.
-      auto put_out = [&](int i, int off, int lg, int count) {
-        auto row = [&](int k) { return (2 * (i + (k >> lg)) + half) * kPart + off + (k & ((1 << lg) - 1)); };   // of the tile
+      // `stage`: pair k is number off + k % width of part i + k / width.
+      auto put_out = [&](int i, int off, int width, int count) {
+        const uint32_t inv = (65535u + width) / width;   // k / width is k * inv >> 16 for k below 32
+        auto row = [&](int k) {                          // of the tile
+          const int part = k * inv >> 16;
+          return (2 * (i + part) + half) * kPart + off + k - part * width;
+        };
         int f = -1;
         float weight = 0.f;
         if (MODE != kDense) {
@@ -613,7 +617,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           tc_pin(raw);
 #pragma unroll
           for (int j = 0; j < kPart; ++j) stage[j * 32 + lane] = __uint_as_float(raw[j]);
-          put_out(i, 0, 5, kPart);
+          put_out(i, 0, kPart, kPart);
         }
         hand_back();
       } else {
@@ -641,10 +645,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           hand_back();
         }
         if (pairs > 1) {
-          // Pair q has its share of every part's columns: `own` quads from q * own on.  A sum's place: [quad of the
+          // Pair q has its share of every part's columns: `own` quads from `first` on.  A sum's place: [quad of the
           // owner's][source][this thread].  One item a cluster, so that the memory is used once; what is sent to a CTA
           // is waited for there.
-          const int lg = pairs == 2 ? 2 : 1, own = 1 << lg;
+          const uint32_t inv = (65535u + pairs) / pairs;   // (x / pairs is x * inv >> 16 here)
+          auto start = [&](int of) { return (int)(kPart / 4 * of * inv >> 16); };
+          const int first = start(q), own = start(q + 1) - first;
           const int live = max(0, (cols / kPart - half + 1) / 2);   // parts of this warp
           if (tid == kWideThreads - 1)
             mbar_arrive_expect_tx(&ctl.red_full, cols / kPart * own * (pairs - 1) * 128 * 16);
@@ -669,7 +675,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             }
 #pragma unroll 2
             for (int j = 0; j < kPart / 4; ++j) {
-              const int to = j >> lg, at = (((part << lg) + (j & (own - 1))) * pairs + q) * 4096;
+              const int to = ((j + 1) * pairs - 1) / (kPart / 4), s0 = start(to);
+              const int at = ((part * (start(to + 1) - s0) + j - s0) * pairs + q) * 4096;
               const float4 u = mine[j * 32];
               if (to == q) *reinterpret_cast<float4 *>(here + at) = u;
               else st_async_v4(cluster_map(base + at, to * 2 + rank), u, cluster_map(bar, to * 2 + rank));
@@ -677,22 +684,23 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           __syncwarp();
           mbar_wait_cluster(&ctl.red_full, 0, abort, p.err);
+          const int some = kPart / (own * 4);   // parts at a time, as `stage` holds
 #pragma unroll 1
-          for (int j0 = 0; j0 < live * own; j0 += kPart / 4) {   // 32 pairs at a time
-            const int some = min(kPart / 4, live * own - j0);
+          for (int i = 0; i < live; i += some) {
+            const int quads = min(some, live - i) * own;
 #pragma unroll 1
-            for (int j = 0; j < some; ++j) {
+            for (int j = 0; j < quads; ++j) {
               float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
               for (int src = 0; src < 4; ++src) {
                 if (src >= pairs) break;
-                const float4 u = *reinterpret_cast<const float4 *>(here + ((j0 + j) * pairs + src) * 4096);
+                const float4 u = *reinterpret_cast<const float4 *>(here + ((i * own + j) * pairs + src) * 4096);
                 v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
               }
               float *to = stage + j * 4 * 32 + lane;
               to[0] = v.x, to[32] = v.y, to[64] = v.z, to[96] = v.w;
             }
-            put_out(j0 >> lg, q * own * 4, lg + 2, some * 4);
+            put_out(i, first * 4, own * 4, quads * 4);
           }
         } else {
 #pragma unroll 1
@@ -709,7 +717,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 stage[(2 * j + 1) * 32 + lane] = hi;
               }
             }
-            put_out(part, 0, 5, kPart);
+            put_out(part, 0, kPart, kPart);
           }
         }
       }
@@ -788,21 +796,24 @@ bool register_shares_fit(Kernel kernel) {
 }
 
 // Height of a dense call's tiles, and the pairs of CTAs that split K: the
-// cheapest by a count of clocks.  A group of 64 columns takes a pair 2 clk for
-// each of the tile's rows in the tensor cores, and its operands 64 bytes a clk
-// into each SM; joining shares of K, 4000.  Shares of K take chunks: several
-// rounds of items, or a share below two chunks, are not split.
+// cheapest by a count of clocks, whose constants were measured.  A group of 64
+// columns takes a pair 2 clk for each of the tile's rows in the tensor cores,
+// and its operands come at 58 bytes a clk into each SM, all of them at 3100 a
+// clk from HBM; joining shares of K, 75 for each row that is sent (4096 x 256, K of
+// 7168: 22.0 us in 128 rows by two pairs, 23.6 in 192 by three).  Several rounds
+// of items, or a share below two chunks, are not split.
 template <typename Kernel>
 void wide_shape(const Bf16Args &a, Kernel kernel, bool chunked, const DeviceInfo &dev, Bf16Cfg *cfg, long long *items) {
   double best = 0;
-  for (int pairs = 1; pairs <= (chunked ? 4 : 1); pairs *= 2) {
+  for (int pairs = 1; pairs <= (chunked ? 4 : 1); ++pairs) {
     if (pairs > 1 && a.KB < pairs * 2 * kChunk) break;
     const int fit = std::min(resident_clusters(kernel, 2 * pairs, cfg->smem_bytes, kWideThreads, dev), dev.sm_count / (2 * pairs));
     for (int rows = kTileRows; rows >= 64; rows -= 32) {
       const long long n = ((long long)a.pairs + rows - 1) / rows * cfg->nt, rounds = (n + fit - 1) / fit;
       if (pairs > 1 && rounds > 1) continue;
-      const double group = std::max(2.0 * rows, (kTileBytes + rows / 2 * kGroupBytes) / 64.0);
-      const double cost = rounds * ((double)a.KB / pairs) * group + (pairs > 1 ? 4000 : 0);
+      const double group = std::max(2.0 * rows, (kTileBytes + rows / 2 * kGroupBytes) / 58.0);
+      const double run = std::max(rounds * ((double)a.KB / pairs) * group, 2.0 * a.K * ((double)a.pairs + a.N) / 3100);
+      const double cost = run + 75.0 * rows * (pairs - 1) / pairs;
       if (best == 0 || cost < best) {
         best = cost;
         cfg->cluster = 2 * pairs;
