@@ -50,7 +50,7 @@ class MoELayer:
 
         self.H, self.I, self.E, self.topk, self.L, self.r = H, I, E, topk, max_loras, rank
         self.norm = (1 + 0.1 * normal(H, scale=1)).to(BF)
-        self.router = normal(H, E, scale=H ** -0.5).to(BF)
+        self.router = normal(H, E, scale=H ** -0.5).to(BF).t().contiguous()      # [E, H]
         self.w13, self.s13 = quantize_weight(normal(E, 2 * I, H, scale=H ** -0.5))
         self.w2, self.s2 = quantize_weight(normal(E, H, I, scale=I ** -0.5))
         # adapters: one slice each for gate and up, one for w2
@@ -60,10 +60,15 @@ class MoELayer:
         self.b2 = normal(max_loras, E, H, rank, scale=0.3 * rank ** -0.5).to(BF)
         self.lora_ids = torch.arange(max_loras, dtype=torch.int32, device=device)
 
-    def route(self, x):
-        """Top-k experts of each token and their renormalised probabilities."""
-        p, ids = torch.softmax((x @ self.router).float(), -1).topk(self.topk, -1)
-        return ids.to(torch.int32), p / p.sum(-1, keepdim=True)
+    def route(self, x, err=None):
+        """Top-k experts of each token and their renormalised probabilities, from fp32 logits."""
+        M = x.shape[0]
+        logits = torch.empty((M, self.E), dtype=torch.float32, device=x.device)
+        ids = torch.empty((M, self.topk), dtype=torch.int32, device=x.device)
+        weights = torch.empty((M, self.topk), dtype=torch.float32, device=x.device)
+        B.moe_bf16_matmul(x, self.router, logits, err_flag=err)
+        B.moe_route(logits, ids, weights)
+        return ids, weights
 
     def step(self, rows, residual, lora, naive=None, err=None):
         """rows: bf16 [M, parts, H], the last layer's output rows (summed by the norm); residual: bf16 [M, H], updated
@@ -74,7 +79,7 @@ class MoELayer:
         new = lambda *shape, dtype=BF: torch.empty(shape, dtype=dtype, device=rows.device)  # noqa: E731
         x, x8, xs = new(M, H), new(M, H, dtype=F8), new(M, B.fp8_groups(H), dtype=torch.float32)
         B.moe_add_rms_norm_fp8(rows, self.norm, x8, xs, residual=residual, residual_out=residual, normed=x)
-        ids, weights = self.route(x)
+        ids, weights = self.route(x, err)
 
         # every id is one of this layer's experts, so every row is written (a rank that holds some of them zeroes these)
         y13, y2 = new(M, topk, 2 * I), new(M, topk, H)

@@ -345,10 +345,12 @@ constexpr int kWideRing = 12;                    // stages at most; each 128 of 
 constexpr int kPartBytes = 32 * 32 * 4;          // 32 pairs' sums of 32 rows, on their way out, for each epilogue warp
 constexpr int kPart = 32;                        // columns of an accumulator that a warp takes at a time
 constexpr int kParts = kTileRows / kPart / 2;    // of one of the two warps of a lane quarter
-// Rows of tiles that are neighbours in the order of the items: the pairs' rows
-// of so many tiles stay in L2 while the weight goes by (Mixtral-shaped w13
-// prefill reads 134 MB of rows 112 times otherwise).
-constexpr int kRaster = 16;
+// Tiles that are neighbours in the order of the items: the pairs' rows of so many
+// stay in L2 while the weight goes by (Mixtral-shaped w13 prefill reads 134 MB of
+// rows 112 times otherwise).  In calls that go on for seconds: dense 8192 x 4096 x
+// 14336 580 us with 16, 591 with 8 and 606 with 4 or 32; that prefill 2.61 ms with 16,
+// 2.57 with 8, 2.69 with 32.
+constexpr int raster(int mode) { return mode == kDense ? 16 : 8; }
 // Registers a thread where chunks are added: loading and MMA warps, epilogue warps.
 constexpr int kWideRegsIssue = 56, kWideRegsEpilogue = 216;
 
@@ -361,8 +363,9 @@ struct WideCtrl {
   int abort;
 };
 
-// The items of a pair: tiles of rows in groups of kRaster, within a group the
+// The items of a pair: tiles of rows in groups of RASTER, within a group the
 // weight's tiles one after the other.
+template <int RASTER>
 struct WideWork {
   int ntiles, nt_all, it, step, items;
   int t, nt;   // of the item
@@ -371,9 +374,9 @@ struct WideWork {
   __device__ __forceinline__ bool advance() {
     it += step;
     if (it >= items) return false;
-    const int g = it / (kRaster * nt_all), r = it - g * kRaster * nt_all, size = min(kRaster, ntiles - g * kRaster);
+    const int g = it / (RASTER * nt_all), r = it - g * RASTER * nt_all, size = min(RASTER, ntiles - g * RASTER);
     nt = r / size;
-    t = g * kRaster + r - nt * size;
+    t = g * RASTER + r - nt * size;
     return true;
   }
 };
@@ -426,7 +429,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const uint32_t tmem = ctl.tmem;
   const int height = cfg.tile_rows;   // of a dense call's tiles
   const int ntiles = MODE == kDense ? (p.pairs + height - 1) / height : load_global(&tiles[0].row0);
-  WideWork wk(ntiles, cfg.nt, blockIdx.x / (2 * pairs), gridDim.x / (2 * pairs));
+  WideWork<raster(MODE)> wk(ntiles, cfg.nt, blockIdx.x / (2 * pairs), gridDim.x / (2 * pairs));
   auto tile = [&](int t) {
     if (MODE == kDense) return WideTile{t * height, min(height, p.pairs - t * height), 0, 0};
     const int4 v = load_global(reinterpret_cast<const int4 *>(tiles) + 1 + t);

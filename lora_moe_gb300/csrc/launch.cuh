@@ -43,7 +43,7 @@ int resident_clusters(Kernel kernel, int cluster, int smem_bytes, int threads, c
     int device, cluster, smem, clusters;
   };
   static std::mutex mu;
-  static Entry known[64];
+  static Entry known[256];
   static int n = 0;
   std::lock_guard<std::mutex> lock(mu);
   for (int i = 0; i < n; ++i)
@@ -67,7 +67,7 @@ int resident_clusters(Kernel kernel, int cluster, int smem_bytes, int threads, c
     clusters = 0;
   }
   if (clusters < 1) clusters = std::max(1, dev.sm_count / cluster / 2);
-  if (n < 64) known[n++] = {(const void *)kernel, dev.device, cluster, smem_bytes, clusters};
+  if (n < 256) known[n++] = {(const void *)kernel, dev.device, cluster, smem_bytes, clusters};
   return clusters;
 }
 
