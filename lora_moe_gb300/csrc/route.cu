@@ -283,11 +283,11 @@ __device__ __forceinline__ float rcp_unit(float x) {
   return r;
 }
 constexpr float kLog2e = 1.44269504f;
-// Scores that only order experts.  x log2(e) is rounded twice: exp(x) is within
-// 2^-22 + |x| 2^-23 of itself (and, as |x| exp(-|x|) < 0.37, within 2^-22 + 2^-24 of
-// one), zero below 2^-126; so a sigmoid, whose slope is s (1 - s), is within 2^-21,
-// a softmax's numerator within 2^-21 of the largest, and a sum of them in VPL + 5
-// steps within 2^-21 + (VPL + 5) 2^-24 of itself.
+// Scores that only order experts.  x log2(e) is rounded twice, so that exp(x) is
+// within 2^-22 + |x| 2^-23 of itself, and zero below 2^-126.  A sigmoid, whose
+// slope is s (1 - s) <= 1/4, with s (1 - s) |x| < 0.23, and whose quotient adds 2^-23 +
+// 2^-24, is within 2^-22; a softmax's numerator (|x| exp(-|x|) < 0.37) within 2^-21 of
+// the largest, and a sum of them in VPL + 5 steps within 2^-21 + (VPL + 5) 2^-24 of itself.
 __device__ __forceinline__ float order_sigmoid(float x) {
   const float e = exp2_unit(-kLog2e * fabsf(x)), r = rcp_unit(1.f + e);
   return x < 0.f ? e * r : r;
@@ -316,6 +316,7 @@ __device__ __noinline__ double exact_choice(const RouteArgs &p, long long row, i
   if (!p.sigmoid) {
     const int e0 = (threadIdx.x & 31) * VPL;
     for (int i = 0; i < VPL && e0 + i < p.E; ++i) top = fmaxf(top, logit_at(p, row + e0 + i));
+    __syncwarp();
     top = warp_max(top);
     sum = 0.0;
     for (int i = 0; i < VPL && e0 + i < p.E; ++i) sum += exp((double)logit_at(p, row + e0 + i) - top);
@@ -357,7 +358,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
   if constexpr (SCORES) {
     // twice the scores' error
     if (p.sigmoid) {
-      slack = 9.5367432e-7f;
+      slack = 4.7683716e-7f;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) c[i] = order_sigmoid(l[i]) + b[i];
     } else {
@@ -376,7 +377,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
     for (int i = 0; i < VPL; ++i) c[i] = l[i];
   }
   // by how much a choice near v may be wrong, twice: the scores' errors, and half an ulp of its sum
-  auto doubt = [&](float v) { return slack + 2.3841858e-7f * fabsf(v); };
+  auto doubt = [&](float v) { return slack + 1.1920929e-7f * fabsf(v); };
 
   if (p.groups > p.topk_groups) {
     float a1 = c[0], a2 = -INFINITY;

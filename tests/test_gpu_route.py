@@ -110,6 +110,49 @@ def test_many_tokens(M, E):
     check(_logits(M, E), 8, bias=_bias(E), sigmoid=True, groups=8, topk_groups=4, best=2, scale=2.5)
 
 
+@pytest.mark.parametrize("E,topk,groups,topk_groups,best", [(64, 2, 1, 1, 1), (128, 8, 1, 1, 1), (128, 4, 4, 2, 2),
+                                                            (256, 8, 8, 4, 2), (256, 6, 2, 1, 1), (256, 8, 8, 1, 2),
+                                                            (64, 8, 16, 9, 2)])
+@pytest.mark.parametrize("sigmoid,biased,dtype,renormalize", [(False, False, BF, True), (True, True, F32, True),
+                                                              (False, True, F32, False), (True, False, BF, False),
+                                                              (False, False, F32, False)])
+def test_a_prefill(E, topk, groups, topk_groups, best, sigmoid, biased, dtype, renormalize):
+    """Several tokens a warp, one after the other; some rows with masked experts, ties, or few candidates."""
+    logits = _logits(4261, E, dtype)
+    logits[::97, ::3] = -INF
+    logits[::89, 2:] = -INF
+    logits[5::101] = logits[5::101].round()
+    check(logits, topk, bias=_bias(E) if biased else None, sigmoid=sigmoid, renormalize=renormalize, scale=1.5, groups=groups,
+          topk_groups=topk_groups, best=best)
+
+
+def test_a_prefill_with_rows_that_are_no_numbers():
+    E = 128
+    logits = _logits(4400, E)
+    logits[7, 9] = float("nan")
+    logits[4399] = INF
+    ids, weights = run(logits, 8)
+    bad = torch.isnan(weights).all(1)
+    assert bad.nonzero().flatten().tolist() == [7, 4399] and not torch.isnan(weights[~bad]).any()
+    assert (ids.sort(1).values.diff(dim=1) > 0).all() and ((ids >= 0) & (ids < E)).all()
+    bias = _bias(E)
+    bias[3] = float("nan")
+    ids, weights = run(logits, 8, bias=bias, sigmoid=True)
+    assert torch.isnan(weights).all() and (ids.sort(1).values.diff(dim=1) > 0).all()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_a_prefill_of_near_ties(sigmoid):
+    """Choices a fraction of an fp32 rounding apart in every row, and in the groups' worth."""
+    M, E = 4300, 64
+    logits = _logits(1, E, F32, 5)
+    s = torch.sigmoid(logits[0].double()) if sigmoid else torch.softmax(logits[0].double(), 0)
+    bias = (0.7 - s).float()
+    logits = logits + 1e-7 * torch.randn((M, E), device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    check(logits, 8, bias=bias, sigmoid=sigmoid)
+    check(logits, 8, bias=bias, sigmoid=sigmoid, groups=4, topk_groups=2, best=2)
+
+
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("groups,best", [(1, 1), (8, 1), (8, 2)])
