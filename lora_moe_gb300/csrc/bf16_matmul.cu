@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (cs > 1) cluster_arrive_release();   // this CTA's barriers are initialised; waited for before anything is sent
+  let_next_grid_start();
   wait_for_prior_grid();
   const uint32_t tmem = ctl.tmem;
   const int all_units = num_units<MODE>(p, BT);
@@ -425,6 +426,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   cluster_wait();
   __syncthreads();
   tc_fence_after();
+  let_next_grid_start();
   wait_for_prior_grid();
   const uint32_t tmem = ctl.tmem;
   const int height = cfg.tile_rows;   // of a dense call's tiles
