@@ -2,12 +2,14 @@
 //
 //   y[f][n] = weight[f] * act(sum + bias[e][n]) + residual[f][n]
 //
-// in fp32, rounded once to y's type.  The tensor-core kernels bring the sums to
-// shared memory, where a loop of few instructions takes them four columns a
-// thread: a tile's epilogue runs a few times a launch, and code that is unrolled
+// in fp32, rounded once to y's type.  For a bf16 y the activations use the
+// approximate units (a few instructions a value: with CUDA's own expf and its
+// division a decode batch's epilogue took four times the product, 48 x 176 with
+// silu 15.6 us); for an fp32 one, CUDA's functions.  The tensor-core kernels bring
+// the sums to shared memory, where a loop of few instructions takes them four
+// columns a thread: a tile's epilogue runs a few times a launch, and code that is unrolled
 // over the sums in registers costs more to fetch than to run (64 x 2880, K of
-// 256: 7700 clk of 12900).  Exponentials are CUDA's expf (its fast
-// form is 2^-21 off, 8 fp32 roundings; the sums cost more than either).
+// 256: 7700 clk of 12900).
 #pragma once
 
 #include "bf16.h"
@@ -17,13 +19,38 @@
 
 namespace moe_lora {
 
-// v / (1 + exp(-z)), from exp(-|z|), which cannot overflow.
+// v / (1 + exp(-z)), from exp(-|z|), which cannot overflow.  FAST: 2^x and 1 / x of
+// the approximate units, within 2^-21 + |z| 2^-23 of the value.
+template <bool FAST>
 __device__ __forceinline__ float times_sigmoid(float v, float z) {
-  const float e = expf(-fabsf(z));
-  return v * (z < 0.f ? e : 1.f) / (1.f + e);
+  if constexpr (FAST) {
+    const float e = exp2_unit(-1.44269504f * fabsf(z)), r = v * rcp_unit(1.f + e);
+    return z < 0.f ? r * e : r;
+  } else {
+    const float e = expf(-fabsf(z));
+    return v * (z < 0.f ? e : 1.f) / (1.f + e);
+  }
 }
 
-template <int W>
+// v * Phi(v), Phi(v) = erfc(-v / sqrt(2)) / 2: erfc keeps the bits that 1 + erf(v)
+// loses for v < 0.  FAST: the rational approximation 7.1.26 of Abramowitz and
+// Stegun, "Handbook of Mathematical Functions", erfc(x) = (a1 t + .. + a5 t^5)
+// exp(-x^2), t = 1 / (1 + 0.3275911 x), within 1.5e-7 for x >= 0.
+template <bool FAST>
+__device__ __forceinline__ float gelu(float v) {
+  if constexpr (FAST) {
+    const float x = 0.70710678f * fabsf(v), t = rcp_unit(1.f + 0.3275911f * x);
+    float q = 1.061405429f * t - 1.453152027f;
+    q = q * t + 1.421413741f;
+    q = q * t - 0.284496736f;
+    q = (q * t + 0.254829592f) * t * exp2_unit(-0.72134752f * v * v);   // erfc(x); x^2 log2(e) = v^2 log2(e) / 2
+    return v * (v < 0.f ? 0.5f * q : 1.f - 0.5f * q);
+  } else {
+    return 0.5f * v * erfcf(-0.70710678118654752f * v);
+  }
+}
+
+template <bool FAST, int W>
 __device__ __forceinline__ void activate(float (&v)[W], int act) {
   if (act == MOE_ACT_NONE) return;
   if (act == MOE_ACT_RELU) {
@@ -31,16 +58,15 @@ __device__ __forceinline__ void activate(float (&v)[W], int act) {
     for (int i = 0; i < W; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];   // (keeps NaN)
   } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = times_sigmoid(v[i], v[i]);
+    for (int i = 0; i < W; ++i) v[i] = times_sigmoid<FAST>(v[i], v[i]);
   } else if (act == MOE_ACT_GELU) {
-    // v * Phi(v): erfc keeps the bits that 1 + erf(v) loses for v < 0
 #pragma unroll
-    for (int i = 0; i < W; ++i) v[i] = 0.5f * v[i] * erfcf(-0.70710678118654752f * v[i]);
+    for (int i = 0; i < W; ++i) v[i] = gelu<FAST>(v[i]);
   } else {
     // 0.5 v (1 + tanh(u)) = v * sigmoid(2u), u = sqrt(2 / pi) (v + 0.044715 v^3)
 #pragma unroll
     for (int i = 0; i < W; ++i)
-      v[i] = times_sigmoid(v[i], 1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
+      v[i] = times_sigmoid<FAST>(v[i], 1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
   }
 }
 
@@ -65,7 +91,8 @@ __device__ __forceinline__ void finish_one(const Bf16Args &p, int f, int e, int 
   const float w = pair_weight<MODE>(p, f);
   const float r = p.residual ? load_as_f32(p.residual, f * p.ldr + n, p.y_f32) : 0.f;
   float o[1] = {v + bias_of(p, e, n)};
-  activate(o, p.act);
+  if (p.y_f32) activate<false>(o, p.act);
+  else activate<true>(o, p.act);
   store_one(p, f * p.ldy + n, o[0] * w + r);
 }
 
@@ -75,8 +102,9 @@ __device__ __forceinline__ bool in_fours(const void *p, long long ld, int f32) {
   return (ld & 3) == 0 && (reinterpret_cast<uintptr_t>(p) & (f32 ? 15 : 7)) == 0;
 }
 
-// The sums' way out, four columns of a row of the output a thread: what the rows
-// allow is looked at once, so that the loops run through.
+// The sums' way out, four columns of a row of the output a thread, neighbours
+// where the rows allow that they are written at once.  That is looked at once, so that
+// the loops run through.
 enum { kOutSingly, kOutBf16, kOutF32 };
 __device__ __forceinline__ int out_kind(const Bf16Args &p) {
   if (p.N % 4 != 0 || !in_fours(p.y, p.ldy, p.y_f32) || (p.residual && !in_fours(p.residual, p.ldr, p.y_f32)))
@@ -84,15 +112,18 @@ __device__ __forceinline__ int out_kind(const Bf16Args &p) {
   return p.y_f32 ? kOutF32 : kOutBf16;
 }
 
-// Four columns from n on (a multiple of four, below N) of the pairs f (negative:
-// none), whose sums v are, times w (dense: not used).  All loads come before the first
-// store: residual may be y.
+// Four columns, n + i * step, of the pairs f (negative: none), whose sums v are,
+// times w (dense: not used); step is 1 and n a multiple of four below N but for
+// kOutSingly.  All loads come before the first store: residual may be y.
 template <int MODE, int KIND, int B>
-__device__ __forceinline__ void finish_fours(const Bf16Args &p, const int (&f)[B], const float (&w)[B], int n,
+__device__ __forceinline__ void finish_fours(const Bf16Args &p, const int (&f)[B], const float (&w)[B], int n, int step,
                                              const float (&bias)[4], float (&v)[4 * B]) {
 #pragma unroll
   for (int i = 0; i < 4 * B; ++i) v[i] += bias[i & 3];
-  if (p.act != MOE_ACT_NONE) activate(v, p.act);
+  if (p.act != MOE_ACT_NONE) {
+    if (KIND == kOutF32 || (KIND == kOutSingly && p.y_f32)) activate<false>(v, p.act);
+    else activate<true>(v, p.act);
+  }
   if (MODE != kDense) {
 #pragma unroll
     for (int i = 0; i < 4 * B; ++i) v[i] *= w[i >> 2];
@@ -102,7 +133,8 @@ __device__ __forceinline__ void finish_fours(const Bf16Args &p, const int (&f)[B
       float r[4 * B];
 #pragma unroll
       for (int i = 0; i < 4 * B; ++i)
-        r[i] = f[i >> 2] >= 0 && n + (i & 3) < p.N ? load_as_f32(p.residual, f[i >> 2] * p.ldr + n + (i & 3), p.y_f32) : 0.f;
+        r[i] = f[i >> 2] >= 0 && n + (i & 3) * step < p.N
+                   ? load_as_f32(p.residual, f[i >> 2] * p.ldr + n + (i & 3) * step, p.y_f32) : 0.f;
 #pragma unroll
       for (int i = 0; i < 4 * B; ++i) v[i] += r[i];
     } else if constexpr (KIND == kOutF32) {
@@ -129,7 +161,7 @@ __device__ __forceinline__ void finish_fours(const Bf16Args &p, const int (&f)[B
     if constexpr (KIND == kOutSingly) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (f[b] >= 0 && n + i < p.N) store_one(p, f[b] * p.ldy + n + i, v[4 * b + i]);
+        if (f[b] >= 0 && n + i * step < p.N) store_one(p, f[b] * p.ldy + n + i * step, v[4 * b + i]);
     } else if constexpr (KIND == kOutF32) {
       if (f[b] >= 0)
         *reinterpret_cast<float4 *>(static_cast<float *>(p.y) + f[b] * p.ldy + n) =

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       const int ui = wk.it / cfg.nt, nt = wk.it - ui * cfg.nt, b = unit(ui), e = block_expert<MODE>(p, b, BT);
       if (e < 0) continue;
       // the pair of position `lane` (dense: not used), and biases of the four rows
-      const int n = nt * kRows + lane * 4;
+      const int step = out == kOutSingly ? 32 : 1, col = out == kOutSingly ? lane : lane * 4, n = nt * kRows + col;
       int pair = -1;
       float weight = 0.f, bias[4];
       if (MODE != kDense) {
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         weight = pair < 0 ? 0.f : pair_weight<MODE>(p, pair);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) bias[i] = bias_of(p, e, n + i);
+      for (int i = 0; i < 4; ++i) bias[i] = bias_of(p, e, n + i * step);
       if (MODE == kDense && p.residual) {   // this warp's rows of it, 64 bytes a lane
         const int from = cs == 1 ? 0 : join_first(BT, cs, wk.rank), to = cs == 1 ? BT : join_first(BT, cs, wk.rank + 1);
         const int at = nt * kRows + (lane & 7) * (p.y_f32 ? 16 : 32);
@@ -307,10 +307,16 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
               w[i] = __shfl_sync(0xFFFFFFFFu, weight, t & 31);
             }
             if (t >= last || n >= p.N) f[i] = -1;
-            const float4 u = *reinterpret_cast<const float4 *>(sums + (min(t, last - 1) - first) * kRows + lane * 4);
-            v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+            const float *from = sums + (min(t, last - 1) - first) * kRows + col;
+            if constexpr (decltype(kind)::value == kOutSingly) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[4 * i + k] = from[k * step];
+            } else {
+              const float4 u = *reinterpret_cast<const float4 *>(from);
+              v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
+            }
           }
-          finish_fours<MODE, decltype(kind)::value, 4>(p, f, w, n, bias, v);
+          finish_fours<MODE, decltype(kind)::value, 4>(p, f, w, n, step, bias, v);
         }
       };
       if (out == kOutBf16) put_out(std::integral_constant<int, kOutBf16>());
@@ -550,10 +556,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     while (wk.advance()) {
       const WideTile t = tile(wk.t);
       const int cols = columns(t.rows);
-      const int n = wk.nt * kWideN + rank * kRows + quarter * 32 + (lane & 7) * 4;   // four rows, for the way out
+      // four of the 32 rows, for the way out
+      const int step = out == kOutSingly ? 8 : 1, col = (lane & 7) * (out == kOutSingly ? 1 : 4);
+      const int n = wk.nt * kWideN + rank * kRows + quarter * 32 + col;
       float bias[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) bias[i] = bias_of(p, t.expert, n + i);
+      for (int i = 0; i < 4; ++i) bias[i] = bias_of(p, t.expert, n + i * step);
       auto hand_back = [&]() {
         tc_fence_before();
         __syncwarp();
@@ -593,10 +601,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 w[k] = __shfl_sync(0xFFFFFFFFu, weight, j);
               }
               if (n >= p.N || j >= count) fj[k] = -1;
-              const float4 u = *reinterpret_cast<const float4 *>(stage + j * 32 + (lane & 7) * 4);
-              v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
+              const float *from = stage + j * 32 + col;
+              if constexpr (decltype(kind)::value == kOutSingly) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * k + i] = from[i * step];
+              } else {
+                const float4 u = *reinterpret_cast<const float4 *>(from);
+                v[4 * k] = u.x, v[4 * k + 1] = u.y, v[4 * k + 2] = u.z, v[4 * k + 3] = u.w;
+              }
             }
-            finish_fours<MODE, decltype(kind)::value, 4>(p, fj, w, n, bias, v);
+            finish_fours<MODE, decltype(kind)::value, 4>(p, fj, w, n, step, bias, v);
           }
         };
         if (out == kOutBf16) rows(std::integral_constant<int, kOutBf16>());

@@ -510,15 +510,40 @@ __device__ __forceinline__ uint4 load_streamed(const uint8_t *p) {
   return r;
 }
 
-// 16 bytes of a row from byte k on, zeros past the row's K bytes; nothing past
-// them is read.
+// The first n < 8 bytes at p, on 8 bytes; nothing past them is read.
+__device__ __forceinline__ uint64_t load_some(const uint8_t *p, int n) {
+  uint64_t v = 0;
+  if (n & 4) v = load_global(reinterpret_cast<const uint32_t *>(p));
+  if (n & 2) v |= (uint64_t)load_global(reinterpret_cast<const uint16_t *>(p + (n & 4))) << (8 * (n & 4));
+  if (n & 1) v |= (uint64_t)load_global(p + (n & 6)) << (8 * (n & 6));
+  return v;
+}
+// 16 bytes of a row on 16 bytes from byte k (a multiple of 16) on, zeros past the
+// row's K bytes; nothing past them is read.
 __device__ __forceinline__ uint4 load_tail(const uint8_t *row, int k, int K) {
-  if (k + 16 <= K) return load_global(reinterpret_cast<const uint4 *>(row + k));
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (k + i < K) w[i >> 2] |= (uint32_t)load_global(row + k + i) << (8 * (i & 3));
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  const int n = K - k;
+  if (n >= 16) return load_global(reinterpret_cast<const uint4 *>(row + k));
+  uint64_t lo = 0, hi = 0;
+  if (n >= 8) {
+    lo = load_global(reinterpret_cast<const uint64_t *>(row + k));
+    hi = load_some(row + k + 8, n - 8);
+  } else if (n > 0) {
+    lo = load_some(row + k, n);
+  }
+  return make_uint4((uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32));
+}
+
+// The approximate units, without their handling of denormals: 2^x within 2^-22
+// of itself and 1 / x within an ulp.
+__device__ __forceinline__ float exp2_unit(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_unit(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // True in one lane of a converged warp.  Around tcgen05 and bulk-copy

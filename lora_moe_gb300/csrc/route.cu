@@ -10,9 +10,9 @@
 // among equals holds the lowest index.  The topk-th largest of the lanes' maxima
 // is a bound that all chosen experts reach; those that do are few (topk to 2
 // topk, mostly): a lane takes each and counts the ones before it, which is its
-// place (route_fast).  What that form leaves (numbers that are none, masked
-// experts under a bias, more than 32 experts that reach the bound, groups that do
-// not end with lanes) takes the largest topk times (route_general).  Bound by
+// place (route_fast).  What that form leaves (numbers that are none, more than 32
+// experts that reach the bound, fewer candidates than places) takes the largest
+// topk times (route_general).  Bound by
 // latency for a few tokens, by instructions for many (the logits' bytes are less).
 //
 // Which experts are chosen is what arithmetic in 64 bits says.  Without a bias
@@ -270,18 +270,6 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-// The approximate units, without their handling of denormals: 2^x within 2^-22
-// of itself and 1 / x within an ulp.
-__device__ __forceinline__ float exp2_unit(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_unit(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 constexpr float kLog2e = 1.44269504f;
 // Scores that only order experts.  x log2(e) is rounded twice, so that exp(x) is
 // within 2^-22 + |x| 2^-23 of itself, and zero below 2^-126.  A sigmoid, whose
@@ -295,8 +283,10 @@ __device__ __forceinline__ float order_sigmoid(float x) {
 
 // What does not depend on the token.
 struct Lane {
-  int lane, span, group;   // span: lanes of a group (a power of two); group: of this lane's experts
-  bool ok;                 // the fast form takes the groups and the bias
+  int lane, span, group;   // span: lanes of a group, a power of two, or 0; group: of this lane's experts
+  int size;                // experts of a group
+  uint32_t inv;            // e / size is e * inv >> 20
+  bool ok;                 // the biases are ordinary numbers
 };
 
 // Experts of a token that reach the bound: expert and choice, then a key (the
@@ -327,8 +317,7 @@ __device__ __noinline__ double exact_choice(const RouteArgs &p, long long row, i
   return (p.sigmoid ? sigmoid(x) : exp(x - top) / sum) + (p.bias ? (double)load_global(p.bias + expert) : 0.0);
 }
 
-// One token without NaN or +inf (SCORES: without -inf either); false where it
-// is left to the general form.
+// One token without NaN or +inf; false where it is left to the general form.
 template <int VPL, bool SCORES, bool FULL>
 __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[VPL], const float (&b)[VPL], const Lane &at,
                                            long long row, Picks &picks, Routed *out) {
@@ -337,7 +326,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const bool exists = FULL || e0 + i < p.E;
-    odd |= exists && (SCORES ? !(fabsf(l[i]) < INFINITY) : !(l[i] < INFINITY));
+    odd |= exists && !(l[i] < INFINITY);
   }
   if (__any_sync(kAll, odd)) return false;
 
@@ -367,11 +356,8 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
 #pragma unroll
       for (int i = 0; i < VPL; ++i) c[i] = c[i] * inv + b[i];
     }
-    if (!FULL) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (e0 + i >= p.E) c[i] = -INFINITY;
-    }
+    for (int i = 0; i < VPL; ++i) c[i] = l[i] > -INFINITY ? c[i] : -INFINITY;   // (of experts that do not exist, too)
   } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) c[i] = l[i];
@@ -380,20 +366,30 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
   auto doubt = [&](float v) { return slack + 1.1920929e-7f * fabsf(v); };
 
   if (p.groups > p.topk_groups) {
-    float a1 = c[0], a2 = -INFINITY;
-#pragma unroll
-    for (int i = 1; i < VPL; ++i) {
-      a2 = fmaxf(a2, fminf(a1, c[i]));
-      a1 = fmaxf(a1, c[i]);
-    }
-    for (int d = 1; d < at.span; d <<= 1) {
-      const float b1 = __shfl_xor_sync(kAll, a1, d), b2 = __shfl_xor_sync(kAll, a2, d);
+    auto merge = [](float &a1, float &a2, float b1, float b2) {
       a2 = fmaxf(fmaxf(a2, b2), fminf(a1, b1));
       a1 = fmaxf(a1, b1);
+    };
+    auto sum2 = [&](float a1, float a2) { return p.best == 2 && a2 > -INFINITY ? a1 + a2 : a1; };
+    float a1 = -INFINITY, a2 = -INFINITY, sums = -INFINITY, worth = -INFINITY;   // sums: of this lane's group; worth: of group `lane`
+    if (at.span) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) merge(a1, a2, c[i], -INFINITY);
+      for (int d = 1; d < at.span; d <<= 1) merge(a1, a2, __shfl_xor_sync(kAll, a1, d), __shfl_xor_sync(kAll, a2, d));
+      sums = sum2(a1, a2);
+      worth = __shfl_sync(kAll, sums, lane * at.span & 31);
+      if (lane >= p.groups) worth = -INFINITY;
+    } else {
+#pragma unroll 1
+      for (int g = 0; g < p.groups; ++g) {
+        float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) merge(b1, b2, (unsigned)(e0 + i - g * at.size) < (unsigned)at.size ? c[i] : -INFINITY, -INFINITY);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) merge(b1, b2, __shfl_xor_sync(kAll, b1, d), __shfl_xor_sync(kAll, b2, d));
+        if (lane == g) worth = sum2(b1, b2);
+      }
     }
-    const float sums = p.best == 2 && a2 > -INFINITY ? a1 + a2 : a1;
-    float worth = __shfl_sync(kAll, sums, lane * at.span & 31);   // of group `lane`
-    if (lane >= p.groups) worth = -INFINITY;
     uint32_t open = 0;
     float rest = worth, stays = 0.f;
     for (int k = 0; k < p.topk_groups; ++k) {
@@ -406,6 +402,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
       // the last that stays against the first that does not
       const float goes = warp_max(rest), near = p.best * doubt(fmaxf(fabsf(stays), fabsf(goes)));
       if (stays - goes <= near) {
+        if (!at.span) return false;
         // The groups near them again, from exact choices of those experts that may be their best.
         const bool close = sums >= stays - near && sums <= goes + near;
         const float least = (p.best == 2 && a2 > -INFINITY ? a2 : a1) - doubt(a1);
@@ -436,7 +433,11 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
         open = __ballot_sync(kAll, lane < p.groups && before < p.topk_groups);
       }
     }
-    if (!(open >> at.group & 1)) {
+    if (!at.span) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (!(open >> ((e0 + i) * at.inv >> 20 & 31) & 1)) c[i] = -INFINITY;
+    } else if (!(open >> at.group & 1)) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) c[i] = -INFINITY;
     }
@@ -583,12 +584,12 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 8 : VPL <= 16 ? 5 : 3)
   picks[warp].count = 0;
   __syncwarp();
   wait_for_prior_grid();
-  Lane at = {lane, 1, 0, true};
+  Lane at = {lane, 1, 0, 1, 0, true};
   if (p.groups > p.topk_groups) {
-    const int size = p.E / p.groups;
-    at.span = max(1, size / VPL);
-    at.group = lane / at.span;
-    at.ok = size % VPL == 0 && (at.span & (at.span - 1)) == 0;
+    at.size = p.E / p.groups;
+    at.inv = ((1u << 20) + at.size - 1) / at.size;   // (exact: e < 1024, so that e * (inv - 2^20 / size) < 2^10 <= 2^20 / size)
+    at.span = at.size % VPL == 0 && (at.size / VPL & (at.size / VPL - 1)) == 0 ? at.size / VPL : 0;
+    at.group = at.span ? lane / at.span : 0;
   }
   float b[VPL], l[VPL];
   if (SCORES) {
