@@ -28,8 +28,8 @@
  *       (_adjust_kernel_inputs).
  *
  * Beside the adapters, the 8-bit serving path of the same MoE layer (norm, base
- * experts' products, activation): the moe_*_fp8 and moe_fp8_* entry points,
- * below.
+ * experts' products, activation): the moe_*_fp8 and moe_fp8_* entry points; its
+ * router and its products with bf16 weights: moe_route and moe_bf16_*, below.
  *
  * Conventions for every entry point:
  *   - Pointers marked [device] must be device pointers of the current CUDA
@@ -614,8 +614,10 @@ int moe_fp8_grouped_matmul_naive(const moe_lora_fp8 *x, int x_per_pair, long lon
  * over the shares.  The same call gives the same bits.
  * ------------------------------------------------------------------------ */
 
-/* Activations (act above).  SILU: v / (1 + exp(-v)); GELU: v * Phi(v), by erfc;
- * GELU_TANH: 0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))). */
+/* Activations (act above).  SILU: v / (1 + exp(-v)); GELU: v * Phi(v); GELU_TANH:
+ * 0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))).  For an fp32 y by CUDA's expf and
+ * erfcf; for a bf16 one by approximations, off by at most 2^-16 of the value or 2^-21 of |v|,
+ * whichever is more. */
 #define MOE_ACT_NONE 0
 #define MOE_ACT_RELU 1
 #define MOE_ACT_SILU 2
@@ -631,8 +633,9 @@ int moe_fp8_grouped_matmul_naive(const moe_lora_fp8 *x, int x_per_pair, long lon
  *   y [device] bf16 or (y_f32) fp32 [M, ldy]
  * Sizes: M >= 0, N >= 1, K >= 1; x and w on 16 bytes with ldx, ldw multiples of
  * 8 (columns from K on are not used); bias, residual, y and their leading
- * dimensions are not restricted beyond their type's alignment (rows on 16
- * bytes are read and written 16 bytes at a time).
+ * dimensions are not restricted beyond their type's alignment (rows of y and the
+ * residual that allow it are read and written four elements at a time: N and
+ * the leading dimensions multiples of four, pointers on four elements).
  */
 int moe_bf16_matmul(const moe_lora_bf16 *x, long long ldx, const moe_lora_bf16 *w, long long ldw, const void *bias,
                     int bias_f32, const void *residual, long long ld_residual, void *y, long long ldy, int y_f32,

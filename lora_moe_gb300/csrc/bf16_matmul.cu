@@ -12,10 +12,19 @@
 //           columns: few pairs for each weight (decode), bound by the weight's
 //           bytes.  Where there are few items, clusters of CTAs split K, their
 //           partial sums exchanged through distributed shared memory and added
-//           in a fixed order.
+//           in a fixed order.  gpt-oss-shaped w2 decode (1.8 GB of weights): 264
+//           us, 6.9 TB/s; 64 x 2880 x 4096 with a residual 9.2 us, of which the
+//           bytes take 3.7, set-up and first loads 3.5, the exchange and the way
+//           out 2.5.
 //   wide    pairs of CTAs (cta_group::2), 256 of the weight's rows by up to 256
-//           pairs, on rows gathered into the blocks' order: bound by the tensor cores.
-// Products of few rows and small weights are bf16_stream.cu's.
+//           pairs, on rows gathered into the blocks' order: bound by the tensor
+//           cores, and over seconds by power.  Dense 8192 x 4096 x 14336: 490 us
+//           (1.96 PFLOP/s), 575 in calls that go on for seconds; Mixtral-shaped
+//           w13 prefill 2.19 ms (1.76 PFLOP/s) and 2.53.  Experts of few rows are
+//           bound by the weight's bytes: 1024 tokens, 8 of 128 experts of 2048 x
+//           1536, 148 us, 123 of them at the copy rate.  In chunks, K split over
+//           two pairs: 4096 x 256, K of 7168, to fp32 20.4 us.
+// Products of few rows are bf16_stream.cu's.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -843,8 +852,10 @@ void wide_shape(const Bf16Args &a, Kernel kernel, bool chunked, const DeviceInfo
   }
 }
 
-// Height of a sorted call's tiles.
-int sorted_height(const Bf16Args &a) { return a.pairs <= 96ll * a.E ? 128 : kTileRows; }
+// Height of a sorted call's tiles: of lower ones the ring holds more.  128 experts
+// of 2048 x 1536, us with 128 / 256 rows: 64 pairs an expert 147 / 151, 96 156 / 160,
+// 128 166 / 172; above, most experts would have more tiles than they need.
+int sorted_height(const Bf16Args &a) { return a.pairs <= 128ll * a.E ? 128 : kTileRows; }
 
 template <int MODE, bool CHUNKED>
 int launch_wide(const Bf16Args &a, void *workspace, const DeviceInfo &dev, cudaStream_t stream) {
@@ -892,16 +903,24 @@ int launch_wide(const Bf16Args &a, void *workspace, const DeviceInfo &dev, cudaS
                           maps, a, list, cfg);
 }
 
-// A round is a GB300's 152 SMs, not the current device's: the workspace's size
-// is asked for on hosts without one.
+// Sorted calls run the wide kernel from 12 pairs an expert on (on average), the
+// narrow one, in units of 16, below: an expert's units read its weight again.  128
+// experts of 2048 x 1536, us narrow / wide: 4 pairs an expert 119 / 120, 8 123 / 126,
+// 16 129 / 130 (with a skewed router 146 / 128), 24 169 / 132, 64 377 / 147; 8
+// experts of 4096 x 14336 and 12 pairs 147 / 140.  The narrow one also while a round of its
+// items covers the output.  A round is a GB300's 152 SMs, not the current device's: the
+// workspace's size is asked for on hosts without one.
 constexpr long long kRoundItems = 152;
 bool sorted_is_wide(const Bf16Args &a) {
   const long long units = a.pairs / 16 + std::min(a.E, a.pairs);
-  return a.pairs >= 20ll * a.E && units * ((a.N + kRows - 1) / kRows) > kRoundItems;
+  return a.pairs >= 12ll * a.E && units * ((a.N + kRows - 1) / kRows) > kRoundItems;
 }
 
 // Up to this many bytes of weights, calls of single pairs or of at most 16 rows
-// run the kernel that streams the weight through registers.
+// run the kernel that streams the weight through registers: it starts sooner.  us,
+// streaming / narrow: one token's eight experts of 1536 x 2048 (50 MB) 9.7 / 12.3,
+// one row by 4096 x 4096 7.5 / 10.0, 16 rows by 8192 x 4096 14.5 / 15.1, 8 rows by 8192 x
+// 8192 (134 MB) 22.8 / 24.6.
 constexpr double kStreamBytes = 256e6;
 
 }  // namespace
@@ -926,6 +945,7 @@ int launch_bf16_matmul(const Bf16Args &a, ProductMode mode, void *workspace, con
     return launch_narrow<16, kSorted>(a, dev, s);
   }
   if (small && a.pairs <= 16) return launch_bf16_stream(a, mode, dev, s);
+  // (32 x 4096 x 4096 9.2 us, 11.5 wide; 64 rows 10.3 and 12.1; by 28672 x 8192 77.6 and 83.0)
   if (a.pairs <= 16) return launch_narrow<16, kDense>(a, dev, s);
   if (a.pairs <= 32) return launch_narrow<32, kDense>(a, dev, s);
   if (a.pairs <= 64) return launch_narrow<64, kDense>(a, dev, s);

@@ -7,7 +7,10 @@
 // operand ring, tensor memory or cluster to set up.  A warp multiplies 16
 // weight rows by 8 or 16 pairs with warp-level MMAs (m16n8k16, fp32 sums of 64
 // columns, added in fp32) over its share of K; the CTA's warps split K or take
-// further rows, and their sums meet in shared memory in a fixed order.
+// further rows, and their sums meet in shared memory in a fixed order.  Measured:
+// one row by 128 x 2048 2.4 us, by 4096 x 4096 7.3; one token's eight experts of
+// 1536 x 2048 (50 MB) 9.6 us, 5.2 TB/s (12.3 on tcgen05); one row by 28672 x 8192
+// 74.3 us, 6.3 TB/s.
 //
 // The tensor core sees the columns of a group of 64 in an order of its own:
 // lane (r, t) holds bytes [16t, 16t + 16) and [64 + 16t, 64 + 16t + 16) of its

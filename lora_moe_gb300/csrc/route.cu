@@ -12,8 +12,10 @@
 // topk, mostly): a lane takes each and counts the ones before it, which is its
 // place (route_fast).  What that form leaves (numbers that are none, more than 32
 // experts that reach the bound, fewer candidates than places) takes the largest
-// topk times (route_general).  Bound by
-// latency for a few tokens, by instructions for many (the logits' bytes are less).
+// topk times (route_general).  Bound by latency for a few tokens, by instructions
+// for many: 16384 tokens of 256 experts take about 420 a token by their logits
+// (8.6 us; the bytes, 2.6) and 800 under a bias in groups (20.3 us), and one token
+// 1.6 us.  Taking the largest eight times for all of them took 21.6 and 48 us.
 //
 // Which experts are chosen is what arithmetic in 64 bits says.  Without a bias
 // (and sums of a group's scores) the logits decide, which needs no arithmetic.
