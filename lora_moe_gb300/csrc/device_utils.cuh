@@ -20,10 +20,6 @@ constexpr unsigned long long kWaitTimeoutNs = 4000000000ull;
 // flag and the clock again.  The thread wakes as soon as the phase completes;
 // the hint only spares the issue slots that polling would take.
 constexpr uint32_t kSuspendHintNs = 20000u;
-// So many sleeps come before the first look at the clock, so that ordinary waits
-// do without one (128 x 2880 x 4096 in bf16, K split over eight CTAs: 16.4 us with
-// it, 16.0 without).
-constexpr int kSleepsBeforeClock = 4;
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -93,10 +89,6 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t *bar, uint32_t pari
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
                                           int32_t *err) {
   if (mbar_try_wait(bar, parity)) return true;
-  for (int i = 0; i < kSleepsBeforeClock; ++i) {
-    if (*abort) return false;
-    if (mbar_try_wait_sleep(bar, parity)) return true;
-  }
   const unsigned long long t0 = global_timer_ns();
   while (true) {
     if (*abort) return false;
@@ -111,10 +103,8 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
 
 // Bounded wait used before a CTA exits: ignores the abort flag.
 __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
-  for (int i = 0; i < kSleepsBeforeClock; ++i)
-    if (mbar_try_wait_sleep(bar, parity)) return;
   const unsigned long long t0 = global_timer_ns();
-  while (!mbar_try_wait_sleep(bar, parity))
+  while (!mbar_try_wait(bar, parity))
     if (global_timer_ns() - t0 > kWaitTimeoutNs) return;
 }
 // The same for a ring of which `uses` uses of consecutive slots were begun:
@@ -122,7 +112,10 @@ __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity) {
 // slot completes phase n).  What completes phases asynchronously (copies,
 // commits) writes to this CTA's shared memory, so the CTA must not exit before.
 __device__ __forceinline__ void drain_ring(uint64_t *bars, uint32_t slots, uint32_t uses) {
-  for (uint32_t s = 0; s < slots && s < uses; ++s) drain_wait(&bars[s], ((uses - 1 - s) / slots) & 1);
+  const unsigned long long t0 = global_timer_ns();
+  for (uint32_t s = 0; s < slots && s < uses; ++s)
+    while (!mbar_try_wait(&bars[s], ((uses - 1 - s) / slots) & 1))
+      if (global_timer_ns() - t0 > kWaitTimeoutNs) return;
 }
 
 // The same by a whole warp, whose lanes wait for a slot each.
@@ -160,8 +153,6 @@ __device__ __forceinline__ void mbar_wait_lean(uint32_t bar, uint32_t parity, vo
     return ok != 0;
   };
   if (done(false)) return;
-  for (int i = 0; i < kSleepsBeforeClock; ++i)
-    if (*abort || done(true)) return;
   const uint32_t t0 = global_timer_lo();
   while (!*abort && !done(true)) {
     if (global_timer_lo() - t0 > (uint32_t)kWaitTimeoutNs) {
@@ -199,10 +190,6 @@ __device__ __forceinline__ bool mbar_try_wait_cluster_sleep(uint64_t *bar, uint3
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort,
                                                   int32_t *err) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
-  for (int i = 0; i < kSleepsBeforeClock; ++i) {
-    if (*abort) return false;
-    if (mbar_try_wait_cluster_sleep(bar, parity)) return true;
-  }
   const unsigned long long t0 = global_timer_ns();
   while (true) {
     if (*abort) return false;

@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "blocks.cuh"
 #include "device_utils.cuh"
@@ -85,6 +86,31 @@ struct NarrowCtrl {
   int live;                                  // units in the list
   int warp_live[kNarrowThreads / 32];
 };
+
+// The sums of one CTA's positions over CS ranks, in rank order; Q of 4
+// positions (or 2) at a time.
+template <int CS, int W>
+__device__ __forceinline__ void sum_ranks(const float *buf, int per_rank, int at, int row, float (&v)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = 0.f;
+#pragma unroll
+  for (int q = 0; q < CS; ++q) {
+    const float *src = buf + ((q * per_rank + at) * kRows + row) * W;
+    if constexpr (W == 4) {
+      const float4 u = *reinterpret_cast<const float4 *>(src);
+      v[0] += u.x;
+      v[1] += u.y;
+      v[2] += u.z;
+      v[3] += u.w;
+    } else if constexpr (W == 2) {
+      const float2 u = *reinterpret_cast<const float2 *>(src);
+      v[0] += u.x;
+      v[1] += u.y;
+    } else {
+      v[0] += *src;
+    }
+  }
+}
 
 template <int BT, int MODE>
 __global__ void __launch_bounds__(kNarrowThreads, 1)
@@ -311,13 +337,58 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         for (int c = 0; c < kLive; ++c) store(block_pair<MODE>(p, b, c, BT), acc[c]);
         continue;
       }
-      join_ranks<BT, MODE == kNaive>(acc, cs, wk.rank, row, smem + cfg.off_red, &ctl.red_full, abort, p.err,
-                                     [&](int t, const auto &v) {
-#pragma unroll
-                                       for (int i = 0; i < (int)(sizeof(v) / sizeof(float)); ++i)
-                                         store(block_pair<MODE>(p, b, t + i, BT), v[i]);
-                                     });
+      // Rank q sums the positions [q * tc, (q + 1) * tc) of every rank's
+      // partial sums, in rank order (one position: rank 0 does).  There is one
+      // item at most, so that the buffer is used once, and every CTA waits for
+      // all that is sent to it: nothing reaches a CTA that has left.
+      const int tc = MODE == kNaive ? 1 : BT / cs, lg = __ffs(tc) - 1;
+      const uint32_t red_base = smem_addr(smem + cfg.off_red), red_bar = smem_addr(&ctl.red_full);
+      const bool receives = MODE != kNaive || wk.rank == 0;
+      if (row == 0 && receives) mbar_arrive_expect_tx(&ctl.red_full, (MODE == kNaive ? cs : BT) * kRows * 4);
+      cluster_wait();
       waited = true;
+      if constexpr (MODE == kNaive) {
+        st_async_f1(cluster_map(red_base + (wk.rank * kRows + row) * 4, 0), acc[0], cluster_map(red_bar, 0));
+      } else if (tc >= 4) {
+#pragma unroll
+        for (int c = 0; c < BT; c += 4) {
+          const int q = c >> lg, quad = (c - (q << lg)) >> 2;
+          st_async_v4(cluster_map(red_base + (((wk.rank * tc) >> 2) + quad) * kRows * 16 + row * 16, q),
+                      make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]), cluster_map(red_bar, q));
+        }
+      } else {   // two positions a rank
+#pragma unroll
+        for (int c = 0; c < BT; c += 2)
+          st_async_f2(cluster_map(red_base + (wk.rank * kRows + row) * 8, c >> 1), acc[c], acc[c + 1],
+                      cluster_map(red_bar, c >> 1));
+      }
+      if (!receives) continue;
+      mbar_wait_cluster(&ctl.red_full, 0, abort, p.err);
+      const float *buf = reinterpret_cast<const float *>(smem + cfg.off_red);
+      auto finish = [&](auto ranks) {
+        constexpr int CS = decltype(ranks)::value;
+        if constexpr (MODE == kNaive) {
+          float v[1];
+          sum_ranks<CS>(buf, 1, 0, row, v);
+          store(b, v[0]);
+        } else if constexpr (BT / CS >= 4) {
+#pragma unroll 4
+          for (int quad = 0; quad < BT / CS / 4; ++quad) {
+            float v[4];
+            sum_ranks<CS>(buf, BT / CS / 4, quad, row, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store(block_pair<MODE>(p, b, wk.rank * (BT / CS) + quad * 4 + i, BT), v[i]);
+          }
+        } else {
+          float v[2];
+          sum_ranks<CS>(buf, 1, 0, row, v);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) store(block_pair<MODE>(p, b, wk.rank * 2 + i, BT), v[i]);
+        }
+      };
+      if (cs == 2) finish(std::integral_constant<int, 2>());
+      else if (cs == 4) finish(std::integral_constant<int, 4>());
+      else finish(std::integral_constant<int, 8>());
     }
   }
   if (cs > 1 && !waited) cluster_wait();

@@ -32,6 +32,17 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 
+// 16 bytes of a row from column k on, zeros past the row's K columns; nothing
+// past them is read.
+__device__ __forceinline__ uint4 load_row_tail(const uint8_t *row, int k, int K) {
+  if (k + 16 <= K) return load_global(reinterpret_cast<const uint4 *>(row + k));
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (k + i < K) w[i >> 2] |= (uint32_t)load_global(row + k + i) << (8 * (i & 3));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 __device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -93,10 +104,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) fp8_stream_kernel
           a[u][2] = load_streamed(w1 + k);
           a[u][3] = load_streamed(w1 + k + 64);
         } else {
-          a[u][0] = load_tail(w0, k, p.K);
-          a[u][1] = load_tail(w0, k + 64, p.K);
-          a[u][2] = load_tail(w1, k, p.K);
-          a[u][3] = load_tail(w1, k + 64, p.K);
+          a[u][0] = load_row_tail(w0, k, p.K);
+          a[u][1] = load_row_tail(w0, k + 64, p.K);
+          a[u][2] = load_row_tail(w1, k, p.K);
+          a[u][3] = load_row_tail(w1, k + 64, p.K);
         }
       }
       uint4 x[NT][U][2];
@@ -117,8 +128,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MODE)) fp8_stream_kernel
               x[j][u][0] = load_global(reinterpret_cast<const uint4 *>(xr + k));
               x[j][u][1] = load_global(reinterpret_cast<const uint4 *>(xr + k + 64));
             } else {
-              x[j][u][0] = load_tail(xr, k, p.K);
-              x[j][u][1] = load_tail(xr, k + 64, p.K);
+              x[j][u][0] = load_row_tail(xr, k, p.K);
+              x[j][u][1] = load_row_tail(xr, k + 64, p.K);
             }
           }
           if (r0 >= 0) sx[j][u][0] = load_global(s0 + kb + u);
