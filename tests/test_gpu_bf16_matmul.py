@@ -93,6 +93,25 @@ def test_dense_random(act, M, dtype):
     assert_rounded(y, ref + r.double(), bound, act)
 
 
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M", [2, 40, 100, 6000])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_activations(act, M, dtype):
+    """Every product is by one or zero, so that the activation's own error shows: the header's bound for a bf16 y; for an
+    fp32 one a few roundings (of the argument, 2^-23 of |v| times a slope of at most 1.13, and of the result)."""
+    N = 64
+    v = (torch.arange(M * N, device="cuda").double() / (M * N) - 0.5) * 60
+    x = operand(v.view(M, N))
+    y = torch.empty((M, N), dtype=dtype, device="cuda")
+    B.moe_bf16_matmul(x, torch.eye(N, device="cuda").to(BF), y, activation=ACTS[act])
+    ref = act64(x.double(), act)
+    if dtype == BF:
+        bound = torch.maximum(2.0 ** -16 * ref.abs(), 2.0 ** -21 * x.double().abs())
+    else:
+        bound = 2.0 ** -20 * ref.abs() + 2.0 ** -22 * x.double().abs() * (act != "none")
+    assert_rounded(y, ref, bound, act)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 200, 7168), (12, 200, 7168), (60, 200, 7168), (300, 200, 7168), (6000, 512, 7168)])
 def test_fp32_sums_do_not_drift(M, N, K):
     """Rows whose products all have one sign: what truncating additions lose adds up.  Runs of at most 256 columns lose
