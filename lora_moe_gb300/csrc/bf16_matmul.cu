@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (cs > 1) cluster_arrive_release();   // this CTA's barriers are initialised; waited for before anything is sent
-  let_next_grid_start();
   wait_for_prior_grid();
+  let_next_grid_start();
   const uint32_t tmem = ctl.tmem;
   const int all_units = num_units<MODE>(p, BT);
   int units = all_units;
@@ -441,8 +441,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   cluster_wait();
   __syncthreads();
   tc_fence_after();
-  let_next_grid_start();
   wait_for_prior_grid();
+  let_next_grid_start();
   const uint32_t tmem = ctl.tmem;
   const int height = cfg.tile_rows;   // of a dense call's tiles
   const int ntiles = MODE == kDense ? (p.pairs + height - 1) / height : load_global(&tiles[0].row0);
@@ -622,8 +622,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             finish_fours<MODE, decltype(kind)::value, 4>(p, fj, w, n, step, bias, v);
           }
         };
+        // (an fp32 y is added up in chunks)
         if (out == kOutBf16) rows(std::integral_constant<int, kOutBf16>());
-        else if (MODE == kDense && out == kOutF32) rows(std::integral_constant<int, kOutF32>());
+        else if (CHUNKED && out == kOutF32) rows(std::integral_constant<int, kOutF32>());
         else rows(std::integral_constant<int, kOutSingly>());
         __syncwarp();
       };

@@ -473,7 +473,10 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 __device__ __forceinline__ void wait_for_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Lets the next grid in the stream start, as far as there is room for it, once
-// every CTA of this one has; it waits for this grid's end before it touches memory.
+// every CTA of this one has; it waits for this grid's end before it reads what this one
+// writes.  After wait_for_prior_grid() in every kernel: the next grid may read
+// inputs that this one does not write before it waits (the adapters' kernel reads
+// its slots' indexes), and what wrote those has ended by then.
 // (Its set-up runs beside this one's end: 64 x 2880 x 4096 in bf16 10.5 -> 9.2 us, call
 // after call.  Kernels with little to set up gain nothing: single rows and the router
 // do without.)

@@ -22,8 +22,8 @@ __global__ void __launch_bounds__(kGatherThreads)
                   uint8_t *xg, long long ld) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bs = p.block;
-  let_next_grid_start();
   wait_for_prior_grid();
+  let_next_grid_start();
   const int nb = num_blocks(p);
   if (blockIdx.x == 0) {
     // Tile list.  Blocks of one expert are neighbours: a run.  A block heads a

@@ -252,3 +252,44 @@ def test_single_pairs_too_many_to_stream():
     y, err = torch.empty((M, topk, N), dtype=BF, device="cuda"), err_flag()
     B.moe_bf16_grouped_matmul_naive(x, w, y, ids, x_per_pair=True, err_flag=err)
     assert torch.equal(y.view(M * topk, N), grouped64(x, w, ids, True)[0].to(BF)) and err.item() == 0
+
+
+@pytest.mark.parametrize("M,topk", [(4, 2), (40, 2), (300, 4)])
+def test_adapters_behind_a_product(M, topk):
+    """Slots' indexes and flags that are written just before a product, whose end the adapters' kernel starts beside."""
+    g = gen(M)
+    E, L, r, K, N, block = 8, 2, 8, 256, 256, 16
+    x, w = operand(whole(g, M, K)), operand(whole(g, N, K))
+    a, b = whole(g, L, E, r, K, most=1).to(BF), whole(g, L, E, N, r, most=1).to(BF)
+    ids = routes(M, topk, E, g)
+    lora = torch.arange(M, device="cuda", dtype=I32) % L
+    slots = [torch.tensor(v, dtype=I32, device="cuda") for v in ([0, 1], [-1, 1], [0, -1], [0, 1])]
+    flags = [torch.tensor(v, dtype=I32, device="cuda") for v in ([1, 1], [1, 1], [1, 1], [1, 0])]
+    blocks = B.AlignBuffers(M, topk, E, L, L, block)
+    now, on = slots[0].clone(), flags[0].clone()
+    B.moe_lora_align(ids, lora, now, E, L, block, blocks.sorted_token_ids, blocks.expert_ids, blocks.num_tokens_post_padded,
+                     workspace=blocks.workspace)
+    base, err = torch.empty((M, N), dtype=BF, device="cuda"), err_flag()
+
+    def call(i, y, apart):
+        now.copy_(slots[i])
+        on.copy_(flags[i])
+        if apart:
+            torch.cuda.synchronize()
+        B.moe_bf16_matmul(x, w, base, err_flag=err)
+        if apart:
+            torch.cuda.synchronize()
+        B.moe_lora_fused_shrink_expand_ex(x, a, b, y, blocks.sorted_token_ids, blocks.expert_ids,
+                                          blocks.num_tokens_post_padded, now, topk, block, adapter_enabled=on, err_flag=err)
+        if apart:
+            torch.cuda.synchronize()
+    want = [torch.zeros((M, topk, N), dtype=BF, device="cuda") for _ in slots]
+    for i, y in enumerate(want):
+        call(i, y, True)
+    assert not torch.equal(want[0], want[1]) and not torch.equal(want[0], want[2]) and not torch.equal(want[0], want[3])
+    got = [torch.zeros((M, topk, N), dtype=BF, device="cuda") for _ in range(80)]
+    for i, y in enumerate(got):
+        call(i * 7 // 4 % 4, y, False)
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i * 7 // 4 % 4])
+    assert err.item() == 2      # MOE_LORA_DEVERR_LORA_ID: slots without an adapter are reported, and nothing else
