@@ -681,12 +681,13 @@ int moe_bf16_grouped_matmul_naive(const moe_lora_bf16 *x, int x_per_pair, long l
  *   s[e] = softmax over the experts of logits[m], or (SIGMOID) 1 / (1 + exp(-logits[m][e]))
  *   c[e] = s[e] + bias[e]          the choice; without a bias the logits decide, in whose order s is
  *   topk_ids[m]     = the topk experts with the largest c, in descending order, the lowest index first among equals
- *   topk_weights[m] = s[id] of each, divided by their sum when `renormalize` (and the sum is not zero), times scale
+ *   topk_weights[m] = s[id] of each, divided by their sum when `renormalize` (unless none is a candidate), times scale
  * With num_groups > topk_groups, only the experts of topk_groups of num_groups
  * equal groups of neighbours are candidates: those groups whose group_best (1 or 2)
  * largest c have the largest sum, the lowest index first among equals.
- * The order is that of c in 64-bit arithmetic; the weights are computed in fp32
- * (within 2^-19 of their value) or better.
+ * The order is that of c (without a bias, of the logits), the groups' that of their sums, in
+ * 64-bit arithmetic; the weights are within 2^-19 of their value (2^-18 over more than
+ * 256 experts), or within 2^-140.
  * An expert whose logit (or c) is -inf or NaN is no candidate: it comes after
  * all candidates, as those of the other groups do, by index, with a weight of
  * zero; a row of nothing else has weights of zero.  A row with a NaN logit, or a

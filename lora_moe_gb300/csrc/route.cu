@@ -18,7 +18,7 @@
 // 1.6 us.  Taking the largest eight times for all of them took 21.6 and 48 us.
 //
 // Which experts are chosen is what arithmetic in 64 bits says.  Without a bias
-// (and sums of a group's scores) the logits decide, which needs no arithmetic.
+// the logits decide, which needs no arithmetic, but for sums of a group's scores.
 // With one, c is computed in fp32 with a bound of its error, and where two
 // neighbours of the order lie within that bound it is done again in fp64: for
 // few tokens, as the bound is 1e-6 of the scores.
@@ -96,6 +96,14 @@ __device__ __forceinline__ float logit_at(const RouteArgs &p, long long i) {
   return p.logits_f32 ? load_global(static_cast<const float *>(p.logits) + i)
                       : bf16_bits_to_float(load_global(static_cast<const uint16_t *>(p.logits) + i));
 }
+
+// exp(a - b) for numbers whose difference is at most zero, to two ulp: what the difference
+// loses to rounding (2^-18 of the result from -64 on) is multiplied in again.
+__device__ __forceinline__ float exp_diff(float a, float b) {
+  const float d = a - b, t = d - a, lost = (a - (d - t)) - (b + t), e = expf(d);
+  return d > -128.f ? fmaf(e, lost, e) : 0.f;
+}
+__device__ __forceinline__ double exp_diff(double a, double b) { return exp(a - b); }
 
 struct Routed {
   int id;         // of place `lane`, in lanes below topk
@@ -206,6 +214,12 @@ __device__ __noinline__ Routed route_general(const RouteArgs &p, long long row) 
       const int g = g0 >= 0 ? g0 : (e0 + i) / size;
       if (g < p.groups && !(open >> g & 1)) c[i] = kLow;
     }
+    // (the scores were for the groups: without a bias the logits decide)
+    if (!p.bias) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (c[i] > kLow) c[i] = T(l[i]);
+    }
   }
 
   Key key[VPL], best = 0;
@@ -222,10 +236,10 @@ __device__ __noinline__ Routed route_general(const RouteArgs &p, long long row) 
     const int from = __ffs(__ballot_sync(kAll, best == m)) - 1;
     const int e = __shfl_sync(kAll, e0 + at, from);
     const T v = from_key(m);
-    if (close(before, v, 1.f)) {
+    if (p.bias && close(before, v, 1.f)) {
       // equal inputs are equal: the lowest index is first, whatever the scores' errors
       const bool same = logit_at(p, row + last) == logit_at(p, row + e) &&
-                        (!p.bias || load_global(p.bias + last) == load_global(p.bias + e));
+                        load_global(p.bias + last) == load_global(p.bias + e);
       unsure |= !same;
     }
     before = v;
@@ -246,16 +260,18 @@ __device__ __noinline__ Routed route_general(const RouteArgs &p, long long row) 
         if (key[i] > best) best = key[i], at = i;
     }
   }
-  if (sizeof(T) == 4 && scores) unsure |= close(before, from_key(warp_max(best)), 1.f);
+  if (sizeof(T) == 4 && p.bias) unsure |= close(before, from_key(warp_max(best)), 1.f);
   r.unsure = unsure;
   if (unsure) return r;
 
+  // s = exp(a - ref) / under: under a renormalisation by the largest of the chosen, as
+  // their sum may be out of range otherwise
+  const bool have = lane < p.topk && mine > kLow;
+  const float x = !have ? -INFINITY : scores ? logit_at(p, row + r.id) : (float)mine;
+  const float a = p.sigmoid ? fminf(x, 0.f) : x;
+  const float ref = p.renormalize ? from_key(warp_max(to_key(a))) : p.sigmoid ? 0.f : top;
   T s = 0;
-  if (lane < p.topk && mine > kLow) {
-    float x = (float)mine;   // without scores, the logit itself
-    if (scores) x = logit_at(p, row + r.id);
-    s = score(x);
-  }
+  if (have) s = exp_diff(T(a), T(ref)) / (p.sigmoid ? 1 + exp(-fabs(T(x))) : p.renormalize ? T(1) : sum);
   if (p.renormalize) {
     const T total = warp_sum(s);
     if (total > 0) s = s / total;
@@ -319,10 +335,15 @@ __device__ __noinline__ double exact_choice(const RouteArgs &p, long long row, i
   return (p.sigmoid ? sigmoid(x) : exp(x - top) / sum) + (p.bias ? (double)load_global(p.bias + expert) : 0.0);
 }
 
+// What orders the experts: the logits; the logits, and sums of scores their groups; scores
+// and the bias.
+enum { kByLogits, kByLogitsInGroups, kByChoice };
+
 // One token without NaN or +inf; false where it is left to the general form.
-template <int VPL, bool SCORES, bool FULL>
+template <int VPL, int ORDER, bool FULL>
 __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[VPL], const float (&b)[VPL], const Lane &at,
                                            long long row, Picks &picks, Routed *out) {
+  constexpr bool SCORES = ORDER != kByLogits, CHOICE = ORDER == kByChoice;
   const int lane = at.lane, e0 = lane * VPL;
   bool odd = false;
 #pragma unroll
@@ -351,12 +372,12 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
     if (p.sigmoid) {
       slack = 4.7683716e-7f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) c[i] = order_sigmoid(l[i]) + b[i];
+      for (int i = 0; i < VPL; ++i) c[i] = order_sigmoid(l[i]) + (CHOICE ? b[i] : 0.f);
     } else {
       const float inv = rcp_unit(sum);
       slack = inv * ((VPL + 32) * 2 * 5.9604645e-8f);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) c[i] = c[i] * inv + b[i];
+      for (int i = 0; i < VPL; ++i) c[i] = c[i] * inv + (CHOICE ? b[i] : 0.f);
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) c[i] = l[i] > -INFINITY ? c[i] : -INFINITY;   // (of experts that do not exist, too)
@@ -443,6 +464,11 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
 #pragma unroll
       for (int i = 0; i < VPL; ++i) c[i] = -INFINITY;
     }
+    // (the scores were for the groups: without a bias the logits decide)
+    if (ORDER == kByLogitsInGroups) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = c[i] > -INFINITY ? l[i] : -INFINITY;
+    }
   }
 
   // the bound: at least topk lanes reach it (every finite choice does where fewer have one)
@@ -455,7 +481,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
     if (best == bound) best = -INFINITY;
   }
   if (bound == -INFINITY) bound = -FLT_MAX;
-  else if (SCORES) bound -= doubt(bound);   // and what is as large but for errors
+  else if (CHOICE) bound -= doubt(bound);   // and what is as large but for errors
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) mine += c[i] >= bound;
@@ -492,7 +518,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
   const unsigned long long first = picks.entry[lane], after = picks.entry[min(lane + 1, 31)];
   expert = have ? (int)(uint32_t)first : -1;
   float mine_c = __uint_as_float((uint32_t)(first >> 32));
-  if constexpr (SCORES) {
+  if constexpr (CHOICE) {
     const float next = __uint_as_float((uint32_t)(after >> 32));
     if (__any_sync(kAll, lane < p.topk && lane + 1 < count && mine_c - next <= doubt(fmaxf(fabsf(mine_c), fabsf(next))))) {
       // again in 64 bits, which tell equal inputs from others
@@ -511,13 +537,20 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
   __syncwarp();
   picks.entry[lane] = 0;   // (for the next token)
 
-  const float logit = !SCORES ? mine_c : (lane < p.topk ? logit_at(p, row + expert) : 0.f);
-  // (where the softmax's sum cancels, the largest of the chosen is as good as the row's)
-  const float ref = SCORES || !p.renormalize ? top : __shfl_sync(kAll, logit, 0);
+  // s = exp(a - ref) / under, all chosen being finite: under a renormalisation by the
+  // largest of them, as their sum may be out of range otherwise
+  const float logit = !CHOICE ? mine_c : (lane < p.topk ? logit_at(p, row + expert) : -INFINITY);
+  const float a = p.sigmoid ? fminf(logit, 0.f) : logit;
+  float ref = p.sigmoid ? 0.f : top;
+  if (p.renormalize) ref = CHOICE ? warp_max(a) : __shfl_sync(kAll, a, 0);
   float s = 0.f;
   if (lane < p.topk) {
-    const float e = expf(p.sigmoid ? -fabsf(logit) : logit - ref);
-    s = p.sigmoid ? __fdividef(logit < 0.f ? e : 1.f, 1.f + e) : e;
+    if (p.sigmoid) {
+      const float e = expf(-fabsf(logit));
+      s = __fdividef(ref < 0.f ? exp_diff(a, ref) : logit < 0.f ? e : 1.f, 1.f + e);
+    } else {
+      s = exp_diff(a, ref);
+    }
   }
   float scale = p.scale;
   if (p.renormalize) {
@@ -575,7 +608,7 @@ __device__ __forceinline__ void load_logits(const RouteArgs &p, long long at, in
   else load_row<VPL, uint16_t>(static_cast<const uint16_t *>(p.logits) + at, n, vec, -INFINITY, v);
 }
 
-template <int VPL, bool SCORES, bool FULL>
+template <int VPL, int ORDER, bool FULL>
 __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 8 : VPL <= 16 ? 5 : 3)
     route_kernel(const __grid_constant__ RouteArgs p, bool vec) {
   __shared__ Picks picks[kThreads / 32];
@@ -594,8 +627,8 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 8 : VPL <= 16 ? 5 : 3)
     at.group = at.span ? lane / at.span : 0;
   }
   float b[VPL], l[VPL];
-  if (SCORES) {
-    load_row<VPL, float>(p.bias + lane * VPL, p.bias ? n : 0, vec, 0.f, b);
+  if (ORDER == kByChoice) {
+    load_row<VPL, float>(p.bias + lane * VPL, n, vec, 0.f, b);
     bool odd = false;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) odd |= !(fabsf(b[i]) < INFINITY);
@@ -608,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, VPL <= 8 ? 8 : VPL <= 16 ? 5 : 3)
     if (m + warps < p.M) load_logits<VPL>(p, (m + warps) * p.ld + lane * VPL, n, vec, next);
     const long long row = m * p.ld;
     Routed r;
-    if (!at.ok || !route_fast<VPL, SCORES, FULL>(p, l, b, at, row, picks[warp], &r)) {
+    if (!at.ok || !route_fast<VPL, ORDER, FULL>(p, l, b, at, row, picks[warp], &r)) {
       r = route_general<float, VPL>(p, row);
       if (r.unsure) r = route_general<double, VPL>(p, row);
     }
@@ -627,9 +660,11 @@ template <int VPL>
 int launch_vpl(const RouteArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
   const bool vec = a.E % VPL == 0 && on16(a.logits) && on16(a.bias) && a.ld % (a.logits_f32 ? 4 : 8) == 0;
   const unsigned grid = (unsigned)std::min<long long>((a.M + kThreads / 32 - 1) / (kThreads / 32), dev.sm_count * 8ll);
-  const bool scores = a.bias || (a.groups > a.topk_groups && a.best == 2), full = a.E == 32 * VPL;
-  const auto kernel = scores ? (full ? route_kernel<VPL, true, true> : route_kernel<VPL, true, false>)
-                             : (full ? route_kernel<VPL, false, true> : route_kernel<VPL, false, false>);
+  const bool full = a.E == 32 * VPL;
+  const auto kernel = a.bias ? (full ? route_kernel<VPL, kByChoice, true> : route_kernel<VPL, kByChoice, false>)
+                      : a.groups > a.topk_groups && a.best == 2
+                          ? (full ? route_kernel<VPL, kByLogitsInGroups, true> : route_kernel<VPL, kByLogitsInGroups, false>)
+                          : (full ? route_kernel<VPL, kByLogits, true> : route_kernel<VPL, kByLogits, false>);
   return launch_dependent(kernel, grid, kThreads, 1, 0, stream, a, vec);
 }
 

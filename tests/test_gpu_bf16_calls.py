@@ -293,3 +293,73 @@ def test_adapters_behind_a_product(M, topk):
     for i, y in enumerate(got):
         assert torch.equal(y, want[i * 7 // 4 % 4])
     assert err.item() == 2      # MOE_LORA_DEVERR_LORA_ID: slots without an adapter are reported, and nothing else
+
+
+@pytest.mark.parametrize("M,E,N,K,block", [(3, 4, 70, 100, 0), (3, 4, 70, 100, 16), (50, 6, 260, 200, 64), (900, 4, 300, 256, 128),
+                                           (5, 1, 33, 64, 32)])
+def test_the_same_expert_twice(M, E, N, K, block):
+    """Pairs of one token that name one expert are pairs of their own."""
+    g = gen(M + N)
+    ids = torch.randint(0, E, (M, 1), generator=g, device="cuda").expand(M, min(E, 3)).to(I32).contiguous()
+    x, w = operand(whole(g, ids.numel(), K)), experts(whole(g, E, N, K))
+    y, err = torch.empty((*ids.shape, N), dtype=BF, device="cuda"), err_flag()
+    if block:
+        B.moe_bf16_grouped_matmul(x, w, y, *align(ids, E, block), block, x_per_pair=True, err_flag=err)
+    else:
+        B.moe_bf16_grouped_matmul_naive(x, w, y, ids, x_per_pair=True, err_flag=err)
+    assert torch.equal(y.view(-1, N), grouped64(x, w, ids, True)[0].to(BF)) and err.item() == 0
+
+
+@pytest.mark.parametrize("M,topk,block", [(1, 32, 0), (20, 32, 16), (700, 32, 64), (13000, 1, 128)])
+def test_1024_experts(M, topk, block):
+    g = gen(M)
+    E, N, K = 1024, 136, 72
+    ids = routes(M, topk, E, g, "skew" if M > 1000 else "even")
+    x, w = operand(whole(g, M, K)), experts(whole(g, E, N, K))
+    y, err = torch.empty((M, topk, N), dtype=BF, device="cuda"), err_flag()
+    if block:
+        B.moe_bf16_grouped_matmul(x, w, y, *align(ids, E, block), block, err_flag=err)
+    else:
+        B.moe_bf16_grouped_matmul_naive(x, w, y, ids, err_flag=err)
+    assert torch.equal(y.view(-1, N), grouped64(x, w, ids, False)[0].to(BF)) and err.item() == 0
+
+
+def test_two_graphs_share_a_workspace():
+    """One after the other on a stream, in any order."""
+    layers = [Layer(1500, 3), Layer(1400, 4)]
+    space = max((a.space for a in layers), key=torch.Tensor.numel)
+    graphs = []
+    for a in layers:
+        a.space = space
+        a.run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            a.run()
+        graphs.append(graph)
+    for order in ((0, 1), (1, 0), (0, 0, 1, 1)):
+        for a in layers:
+            a.y.fill_(float("nan"))
+        for i in order:
+            graphs[i].replay()
+        for a in layers:
+            a.check()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_many_rows(dtype):
+    """More rows than tiles of any grid, few columns."""
+    g = gen(5)
+    M, N, K = 700001, 24, 40
+    x, w = operand(whole(g, M, K)), operand(whole(g, N, K))
+    y, err = torch.empty((M, N), dtype=dtype, device="cuda"), err_flag()
+    B.moe_bf16_matmul(x, w, y, err_flag=err)
+    assert torch.equal(y, (x.double() @ w.double().t()).to(dtype)) and err.item() == 0
+    ids, weights = torch.empty((M, 3), dtype=I32, device="cuda"), torch.empty((M, 3), device="cuda")
+    B.moe_route(y, ids, weights)
+    assert torch.equal(ids.long(), torch.sort(y.double(), dim=1, descending=True, stable=True).indices[:, :3])
+    B.moe_route(y, ids, weights, num_groups=6, topk_groups=2, group_best=1)
+    best = torch.sort(y.double().view(M, 6, 4).amax(2), dim=1, descending=True, stable=True).indices[:, :2]
+    inside = torch.zeros((M, 6), dtype=torch.bool, device="cuda").scatter_(1, best, True).repeat_interleave(4, 1)
+    masked = y.double().masked_fill(~inside, -float("inf"))
+    assert torch.equal(ids.long(), torch.sort(masked, dim=1, descending=True, stable=True).indices[:, :3])

@@ -237,6 +237,38 @@ def test_large_logits(sigmoid):
     assert torch.equal(ids.long(), want) and torch.isfinite(weights).all()
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("M,E,groups,topk_groups,topk", [(40, 200, 4, 3, 16), (3, 200, 5, 4, 16), (40, 256, 8, 4, 8),
+                                                         (300, 60, 4, 2, 10), (20, 64, 2, 1, 32)])
+@pytest.mark.parametrize("scale", [1.0, 300.0])
+@pytest.mark.parametrize("bad", [False, True])
+def test_logits_decide_within_groups_chosen_by_scores(sigmoid, M, E, groups, topk_groups, topk, scale, bad):
+    """Scores that are all one, or zero, in any arithmetic, and those that are close, by their logits."""
+    x = _logits(M, E, BF, scale=scale)
+    if bad:      # rows that the general form takes
+        x[:, 0] = INF if sigmoid else x[:, 1]
+        x[:, E // groups:E // groups * 2] = x[:, :1]
+    check(x, topk, sigmoid=sigmoid, groups=groups, topk_groups=topk_groups, best=2, renormalize=False)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("E,topk", [(16, 5), (64, 16), (200, 8), (256, 20)])
+@pytest.mark.parametrize("scale", [10.0, 60.0])
+@pytest.mark.parametrize("masked", [False, True])
+def test_weights_of_far_logits(sigmoid, renormalize, biased, E, topk, scale, masked):
+    """Differences of logits that fp32 rounds, and chosen experts whose scores are all tiny: a bias chooses them."""
+    x = _logits(60, E, F32, scale=scale)
+    bias = None
+    if biased:
+        bias = 4 * torch.rand(E, generator=torch.Generator().manual_seed(E)).cuda()
+        x = x - 3 * scale * (bias > bias.median())
+    if masked:      # all but few: rows that the general form takes
+        x[:, topk - 2:] = -INF
+    check(x, topk, bias=bias, sigmoid=sigmoid, renormalize=renormalize)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("pad,lead", [(1, 0), (8, 8), (3, 5)])
 @pytest.mark.parametrize("E", [8, 64, 100, 256, 520])
