@@ -608,7 +608,7 @@ int moe_fp8_grouped_matmul_naive(const moe_lora_fp8 *x, int x_per_pair, long lon
  *   y[f][n] = weight[f] * act( sum_k x[r][k] * w[e][n][k] + bias[e][n] ) + residual[f][n]
  * from bf16 x and w, in fp32, rounded once to y's type.  The tensor cores add
  * exact products of two bf16 in fp32, over runs of at most 256 columns where y is fp32 or
- * the kernel is one of those for few rows, else over all of K (each addition
+ * the kernel is one of those for few rows, else of at most 1024 (each addition
  * there may truncate); runs are added in ascending order, where K is split
  * over a cluster's CTAs or a CTA's warps ascending within each share and then
  * over the shares.  The same call gives the same bits.

@@ -58,6 +58,7 @@ struct Bf16Cfg {
   int nt;          // output tiles along N
   int cluster;     // CTAs of a cluster, which splits K
   int tile_rows;   // pairs of a tile (wide, dense)
+  int chunk;       // groups of K that the tensor cores add up (wide, chunked)
   int stage_bytes; // (wide)
   int off_red, off_tile, off_list, off_ctrl;
   int list;        // units that the list of live ones holds (0: none is made)
@@ -69,8 +70,12 @@ struct Bf16Cfg {
 constexpr int kMaxRing = 5;    // stages: 5 gave 264 us, 4 265, 3 272, 6 272 and 12 278 (64 tokens, 4 of 128 experts of 2880 x 2880)
 constexpr int kMaxSmem = 227 * 1024;
 // Groups of K whose products the tensor cores add up.  Their additions truncate,
-// so a long sum drifts; the epilogue adds the chunks in fp32, rounding to nearest.
-constexpr int kChunk = 4;
+// so a long sum drifts (K of 7168, products of one sign: 2.4e-5 of the sum); the
+// epilogue adds the chunks in fp32, rounding to nearest.  The wide kernel's chunks
+// are longer where y is bf16, 2^-17 of the sum at most: us with 4 / 8 / 16 groups and with all of
+// K, 8192 x 4096 x 14336 565 / 531 / 491 / 489, sorted 4096 tokens, 8 of 64 experts
+// of 2048 x 2048 261 / 236 / 222 / 221.
+constexpr int kChunk = 4, kLongChunk = 16;
 
 template <int BT>
 struct Narrow {
@@ -350,9 +355,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
 // and half of the pairs', at most 32 KB a group, and 128 x 256 of an
 // accumulator in tensor memory, twice.
 //
-// CHUNKED = false: an accumulator takes all of K; one is read while the next
-// item's is added up.  CHUNKED: an accumulator takes a chunk of K, and the
-// epilogue adds the chunks in registers (fp32 outputs, see kChunk).  A cluster
+// CHUNKED = false: an accumulator takes all of K, at most kLongChunk groups; one is read
+// while the next item's is added up.  CHUNKED: an accumulator takes a chunk of K, and the
+// epilogue adds the chunks in registers.  (A K of one chunk by the second: 8192 x 512
+// x 8192 59 -> 68 us, 2048 x 1024 x 8192 25.7 -> 27.5.)  A cluster
 // of several pairs splits K where there are few items: each pair's sums go to
 // the pair that owns the columns, in the operand ring's memory.
 constexpr int kWideThreads = 384;
@@ -412,7 +418,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   volatile int *abort = &ctl.abort;
   const int rank = blockIdx.x & 1;   // rank 0 issues the pair's MMAs
   // the pair in its cluster, and its share of K
-  const int pairs = CHUNKED ? cfg.cluster >> 1 : 1, q = CHUNKED ? (blockIdx.x >> 1) % pairs : 0;
+  constexpr bool kSplit = CHUNKED && MODE == kDense;
+  const int pairs = kSplit ? cfg.cluster >> 1 : 1, q = kSplit ? (blockIdx.x >> 1) % pairs : 0;
   const int kb0 = (int)((long long)p.KB * q / pairs), kb1 = (int)((long long)p.KB * (q + 1) / pairs);
   const int leader = q * 2;          // the pair's rank 0 in the cluster
 
@@ -522,9 +529,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const uint32_t idesc = make_idesc_bf16(2 * kRows, columns(rows));
         more = wk.advance();
         rows = more ? tile(wk.t).rows : 0;   // the next item's, on its way meanwhile
-        for (int kb = kb0; kb < kb1; ++kb) {
-          const int at = CHUNKED ? (kb - kb0) % kChunk : kb;
-          const bool last = kb + 1 == kb1 || (CHUNKED && at == kChunk - 1);   // of the accumulator
+        for (int kb = kb0, at = 0; kb < kb1; ++kb) {   // at: group of the accumulator
+          const bool last = kb + 1 == kb1 || (CHUNKED && at + 1 == cfg.chunk);
           if (at == 0) mbar_wait(&ctl.tempty[a], aph ^ 1, abort, p.err);
           mbar_wait(&ctl.full[s], ph, abort, p.err);
           tc_fence_after();
@@ -538,7 +544,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           __syncwarp();
           if (++s == stages) { s = 0; ph ^= 1; }
+          ++at;
           if (last) {
+            at = 0;
             a ^= 1;
             if (a == 0) aph ^= 1;
           }
@@ -547,7 +555,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (elect_one()) tc_commit_pair(&ctl.done, both);
     }
     __syncwarp();
-    if (CHUNKED && pairs > 1) {   // the ring is free for other pairs' sums
+    if (kSplit && pairs > 1) {   // the ring is free for other pairs' sums
       cluster_arrive_release();
       cluster_wait();
     }
@@ -622,9 +630,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             finish_fours<MODE, decltype(kind)::value, 4>(p, fj, w, n, step, bias, v);
           }
         };
-        // (an fp32 y is added up in chunks)
+        // (an fp32 y is added up in chunks, and dense)
         if (out == kOutBf16) rows(std::integral_constant<int, kOutBf16>());
-        else if (CHUNKED && out == kOutF32) rows(std::integral_constant<int, kOutF32>());
+        else if (kSplit && out == kOutF32) rows(std::integral_constant<int, kOutF32>());
         else rows(std::integral_constant<int, kOutSingly>());
         __syncwarp();
       };
@@ -656,7 +664,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
           for (int j = 0; j < kPart / 2; ++j) acc[i][j] = 0;
 #pragma unroll 1
-        for (int kb = kb0; kb < kb1; kb += kChunk) {
+        for (int kb = kb0; kb < kb1; kb += cfg.chunk) {
           mbar_wait_lean(smem_addr(&ctl.tfull[0]) + a * 8, aph, abort, p.err);
           tc_fence_after();
 #pragma unroll
@@ -673,7 +681,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           hand_back();
         }
-        if (pairs > 1) {
+        if (kSplit && pairs > 1) {
           // Pair q has its share of every part's columns: `own` quads from `first` on.  A sum's place: [quad of the
           // owner's][source][this thread].  One item a cluster, so that the memory is used once; what is sent to a CTA
           // is waited for there.
@@ -751,7 +759,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
       }
     }
-    if (CHUNKED && pairs > 1 && !met) {
+    if (kSplit && pairs > 1 && !met) {
       cluster_arrive_release();
       cluster_wait();
     }
@@ -824,6 +832,12 @@ bool register_shares_fit(Kernel kernel) {
   return attr.numRegs * kWideThreads >= 128 * kWideRegsIssue + 256 * kWideRegsEpilogue;
 }
 
+// Dense calls in chunks of kChunk groups: fp32 outputs, and those whose tiles leave
+// pairs of CTAs to split K.
+bool in_short_chunks(const Bf16Args &a, const DeviceInfo &dev) {
+  return a.y_f32 || tile_bound(a, false, kTileRows) * ((a.N + kWideN - 1) / kWideN) * 4 <= dev.sm_count;
+}
+
 // Height of a dense call's tiles, and the pairs of CTAs that split K: the
 // cheapest by a count of clocks, whose constants were measured.  A group of 64
 // columns takes a pair 2 clk for each of the tile's rows in the tensor cores,
@@ -832,9 +846,9 @@ bool register_shares_fit(Kernel kernel) {
 // 7168: 22.0 us in 128 rows by two pairs, 23.6 in 192 by three).  Several rounds
 // of items, or a share below two chunks, are not split.
 template <typename Kernel>
-void wide_shape(const Bf16Args &a, Kernel kernel, bool chunked, const DeviceInfo &dev, Bf16Cfg *cfg, long long *items) {
+void wide_shape(const Bf16Args &a, Kernel kernel, bool split, const DeviceInfo &dev, Bf16Cfg *cfg, long long *items) {
   double best = 0;
-  for (int pairs = 1; pairs <= (chunked ? 4 : 1); ++pairs) {
+  for (int pairs = 1; pairs <= (split ? 4 : 1); ++pairs) {
     if (pairs > 1 && a.KB < pairs * 2 * kChunk) break;
     const int fit = std::min(resident_clusters(kernel, 2 * pairs, cfg->smem_bytes, kWideThreads, dev), dev.sm_count / (2 * pairs));
     for (int rows = kTileRows; rows >= 64; rows -= 32) {
@@ -876,6 +890,8 @@ int launch_wide(const Bf16Args &a, void *workspace, const DeviceInfo &dev, cudaS
     cfg.smem_bytes = cfg.off_ctrl + (int)sizeof(WideCtrl);
   };
   ring(height);
+  const bool fine = MODE == kDense && in_short_chunks(a, dev);
+  cfg.chunk = fine ? kChunk : kLongChunk;
   if (CHUNKED) {
     static const bool fits = register_shares_fit(kernel);
     if (!fits) return MOE_LORA_ERR_LAUNCH;
@@ -896,7 +912,7 @@ int launch_wide(const Bf16Args &a, void *workspace, const DeviceInfo &dev, cudaS
   cfg.cluster = 2;
   long long items = tiles * cfg.nt;   // (the sorted arrays' own tiles are no more, but for entries that no align writes)
   if (MODE == kDense) {
-    wide_shape(a, kernel, CHUNKED, dev, &cfg, &items);
+    wide_shape(a, kernel, fine, dev, &cfg, &items);
     ring(cfg.tile_rows);
   }
   const long long clusters = std::min<long long>(items, dev.sm_count / cfg.cluster);
@@ -942,7 +958,9 @@ int launch_bf16_matmul(const Bf16Args &a, ProductMode mode, void *workspace, con
   const bool small = (mode == kNaive ? (double)a.pairs : 1.0) * a.N * a.K * 2 <= kStreamBytes;
   if (mode == kNaive) return small ? launch_bf16_stream(a, mode, dev, s) : launch_narrow<16, kNaive>(a, dev, s);
   if (mode == kSorted) {
-    if (sorted_is_wide(a)) return launch_wide<kSorted, false>(a, workspace, dev, s);
+    if (sorted_is_wide(a))
+      return a.KB > kLongChunk ? launch_wide<kSorted, true>(a, workspace, dev, s)
+                               : launch_wide<kSorted, false>(a, workspace, dev, s);
     return launch_narrow<16, kSorted>(a, dev, s);
   }
   if (small && a.pairs <= 16) return launch_bf16_stream(a, mode, dev, s);
@@ -950,10 +968,7 @@ int launch_bf16_matmul(const Bf16Args &a, ProductMode mode, void *workspace, con
   if (a.pairs <= 16) return launch_narrow<16, kDense>(a, dev, s);
   if (a.pairs <= 32) return launch_narrow<32, kDense>(a, dev, s);
   if (a.pairs <= 64) return launch_narrow<64, kDense>(a, dev, s);
-  // chunks where the output is fp32 (all of K added up by the tensor cores is
-  // 2.4e-5 off for 7168 products of one sign), or where K is split
-  const long long items = tile_bound(a, false, kTileRows) * ((a.N + kWideN - 1) / kWideN);
-  if (a.y_f32 || items * 4 <= dev.sm_count) return launch_wide<kDense, true>(a, nullptr, dev, s);
+  if (a.KB > kLongChunk || in_short_chunks(a, dev)) return launch_wide<kDense, true>(a, nullptr, dev, s);
   return launch_wide<kDense, false>(a, nullptr, dev, s);
 }
 
