@@ -105,6 +105,12 @@ __device__ __forceinline__ float exp_diff(float a, float b) {
 }
 __device__ __forceinline__ double exp_diff(double a, double b) { return exp(a - b); }
 
+// How far the fp32 sum `worth` of two choices a1 and a2 may be off (a2 of zero: of one choice): the scores' errors (slack
+// is twice that of one), half an ulp of each choice, whose biases may be far larger than their sum, and of the sum.
+__device__ __forceinline__ float sum_error(float slack, float a1, float a2, float worth) {
+  return slack + 6e-8f * fabsf(a1) + 6e-8f * fabsf(a2) + 6e-8f * fabsf(worth);
+}
+
 struct Routed {
   int id;         // of place `lane`, in lanes below topk
   float weight;
@@ -167,24 +173,32 @@ __device__ __noinline__ Routed route_general(const RouteArgs &p, long long row) 
   float slack = 0.f;
   if (sizeof(T) == 4 && scores)
     slack = (p.sigmoid ? 1.f : from_key(warp_max(to_key((float)largest)))) * ((VPL + 16) * 2 * 5.9604645e-8f);
-  auto close = [&](T hi, T lo, float times) {
+  auto close = [&](T hi, T lo) {
     return sizeof(T) == 4 && scores && hi < INFINITY && lo > -INFINITY &&
-           hi - lo <= times * (slack + 2.3841858e-7f * fmaxf(fabsf((float)hi), fabsf((float)lo)));
+           hi - lo <= slack + 2.3841858e-7f * fmaxf(fabsf((float)hi), fabsf((float)lo));
   };
   bool unsure = false;
 
   if (p.groups > p.topk_groups) {
     const int size = E / p.groups;
-    T worth = kLow;   // of group `lane`
-    auto sum2 = [&](T a1, T a2) { return p.best == 2 && a2 > kLow ? a1 + a2 : a1; };
+    T worth = kLow, error = 0;   // of group `lane`; error: how far its worth may be off (T = float)
+    auto sum2 = [&](T a1, T a2) {
+      const bool two = p.best == 2 && a2 > kLow;
+      worth = two ? a1 + a2 : a1;
+      if (sizeof(T) == 4 && scores && a1 > kLow && a1 < INFINITY) {
+        if (two) worth = worth > FLT_MAX ? FLT_MAX : worth < -FLT_MAX ? -FLT_MAX : worth;
+        error = sum_error(slack, (float)a1, two ? (float)a2 : 0.f, (float)worth);
+      }
+    };
     const int span = size / VPL;   // lanes of a group
     if (size % VPL == 0 && (span & (span - 1)) == 0) {
       T a1 = kLow, a2 = kLow;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) merge2(a1, a2, c[i], kLow);
       for (int d = 1; d < span; d <<= 1) merge2(a1, a2, __shfl_xor_sync(kAll, a1, d), __shfl_xor_sync(kAll, a2, d));
-      worth = __shfl_sync(kAll, sum2(a1, a2), lane * span & 31);
-      if (lane >= p.groups) worth = kLow;
+      a1 = __shfl_sync(kAll, a1, lane * span & 31);
+      a2 = __shfl_sync(kAll, a2, lane * span & 31);
+      if (lane < p.groups) sum2(a1, a2);
     } else {
       for (int g = 0; g < p.groups; ++g) {
         T a1 = kLow, a2 = kLow;
@@ -193,7 +207,7 @@ __device__ __noinline__ Routed route_general(const RouteArgs &p, long long row) 
           if ((unsigned)(e0 + i - g * size) < (unsigned)size) merge2(a1, a2, c[i], kLow);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) merge2(a1, a2, __shfl_xor_sync(kAll, a1, d), __shfl_xor_sync(kAll, a2, d));
-        if (lane == g) worth = sum2(a1, a2);
+        if (lane == g) sum2(a1, a2);
       }
     }
     int before = 0;   // groups that come before group `lane`
@@ -203,11 +217,12 @@ __device__ __noinline__ Routed route_general(const RouteArgs &p, long long row) 
     }
     const bool stays = lane < p.groups && before < p.topk_groups;
     const uint32_t open = __ballot_sync(kAll, stays);
-    // the last that stays against the first that does not
-    const int last = __ffs(__ballot_sync(kAll, lane < p.groups && before == p.topk_groups - 1)) - 1;
-    const int next = __ffs(__ballot_sync(kAll, lane < p.groups && before == p.topk_groups)) - 1;
-    const T hi = __shfl_sync(kAll, worth, last), lo = __shfl_sync(kAll, worth, next);
-    unsure |= close(hi, lo, (float)p.best);
+    // the least that one which stays may be worth, against the most that one which does not may be
+    if (sizeof(T) == 4 && scores) {
+      const float least = -from_key(warp_max(to_key(stays ? __fadd_ru((float)error, -(float)worth) : -INFINITY)));
+      const float most = from_key(warp_max(to_key(lane < p.groups && !stays && worth > kLow ? __fadd_ru((float)worth, (float)error) : -INFINITY)));
+      unsure |= most > -INFINITY && !(least > most);
+    }
     const int g0 = size % VPL == 0 ? e0 / size : -1;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
@@ -236,7 +251,7 @@ __device__ __noinline__ Routed route_general(const RouteArgs &p, long long row) 
     const int from = __ffs(__ballot_sync(kAll, best == m)) - 1;
     const int e = __shfl_sync(kAll, e0 + at, from);
     const T v = from_key(m);
-    if (p.bias && close(before, v, 1.f)) {
+    if (p.bias && close(before, v)) {
       // equal inputs are equal: the lowest index is first, whatever the scores' errors
       const bool same = logit_at(p, row + last) == logit_at(p, row + e) &&
                         load_global(p.bias + last) == load_global(p.bias + e);
@@ -260,7 +275,7 @@ __device__ __noinline__ Routed route_general(const RouteArgs &p, long long row) 
         if (key[i] > best) best = key[i], at = i;
     }
   }
-  if (sizeof(T) == 4 && p.bias) unsure |= close(before, from_key(warp_max(best)), 1.f);
+  if (sizeof(T) == 4 && p.bias) unsure |= close(before, from_key(warp_max(best)));
   r.unsure = unsure;
   if (unsure) return r;
 
@@ -393,15 +408,14 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
       a2 = fmaxf(fmaxf(a2, b2), fminf(a1, b1));
       a1 = fmaxf(a1, b1);
     };
-    auto sum2 = [&](float a1, float a2) { return p.best == 2 && a2 > -INFINITY ? a1 + a2 : a1; };
-    float a1 = -INFINITY, a2 = -INFINITY, sums = -INFINITY, worth = -INFINITY;   // sums: of this lane's group; worth: of group `lane`
+    float a1 = -INFINITY, a2 = -INFINITY, g1 = -INFINITY, g2 = -INFINITY;   // the two largest of this lane's group, and of group `lane`
     if (at.span) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) merge(a1, a2, c[i], -INFINITY);
       for (int d = 1; d < at.span; d <<= 1) merge(a1, a2, __shfl_xor_sync(kAll, a1, d), __shfl_xor_sync(kAll, a2, d));
-      sums = sum2(a1, a2);
-      worth = __shfl_sync(kAll, sums, lane * at.span & 31);
-      if (lane >= p.groups) worth = -INFINITY;
+      g1 = __shfl_sync(kAll, a1, lane * at.span & 31);
+      g2 = __shfl_sync(kAll, a2, lane * at.span & 31);
+      if (lane >= p.groups) g1 = g2 = -INFINITY;
     } else {
 #pragma unroll 1
       for (int g = 0; g < p.groups; ++g) {
@@ -410,34 +424,40 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
         for (int i = 0; i < VPL; ++i) merge(b1, b2, (unsigned)(e0 + i - g * at.size) < (unsigned)at.size ? c[i] : -INFINITY, -INFINITY);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) merge(b1, b2, __shfl_xor_sync(kAll, b1, d), __shfl_xor_sync(kAll, b2, d));
-        if (lane == g) worth = sum2(b1, b2);
+        if (lane == g) g1 = b1, g2 = b2;
       }
     }
+    // (finite choices have a finite sum here: near ties of such are done again in 64 bits)
+    const bool two = p.best == 2 && g2 > -INFINITY;
+    const float worth = two ? fminf(fmaxf(g1 + g2, -FLT_MAX), FLT_MAX) : g1;
     uint32_t open = 0;
-    float rest = worth, stays = 0.f;
+    float rest = worth;
     for (int k = 0; k < p.topk_groups; ++k) {
-      stays = warp_max(rest);
-      const int from = __ffs(__ballot_sync(kAll, rest == stays)) - 1;
+      const float next = warp_max(rest);
+      const int from = __ffs(__ballot_sync(kAll, rest == next)) - 1;
       open |= 1u << from;
       if (lane == from) rest = -INFINITY;
     }
     if (SCORES) {
-      // the last that stays against the first that does not
-      const float goes = warp_max(rest), near = p.best * doubt(fmaxf(fabsf(stays), fabsf(goes)));
-      if (stays - goes <= near) {
+      // the least that one which stays may be worth, against the most that one which does not may be
+      const bool stays = open >> lane & 1;
+      const float error = sum_error(slack, g1, two ? g2 : 0.f, worth);
+      const float least = -warp_max(stays ? __fadd_ru(error, -worth) : -INFINITY);
+      const float most = warp_max(!stays && worth > -INFINITY ? __fadd_ru(worth, error) : -INFINITY);
+      if (most > -INFINITY && !(least > most)) {
         if (!at.span) return false;
-        // The groups near them again, from exact choices of those experts that may be their best.
-        const bool close = sums >= stays - near && sums <= goes + near;
-        const float least = (p.best == 2 && a2 > -INFINITY ? a2 : a1) - doubt(a1);
-        double exact = worth;
-        if (lane < p.groups && worth >= stays - near && worth <= goes + near) exact = -INFINITY;
+        // The groups that may belong on the other side again, from exact choices of those experts that may be their best.
+        const bool again = worth > -INFINITY && (stays ? __fadd_rd(worth, -error) <= most : __fadd_ru(worth, error) >= least);
+        const bool close = __ballot_sync(kAll, again) >> at.group & 1;
+        const float last = p.best == 2 && a2 > -INFINITY ? a2 : a1, need_from = last - 2.f * doubt(last);
+        double exact = again ? -INFINITY : worth;
         double second = -INFINITY;
         for (int i = 0; i < VPL; ++i) {   // (one expert a lane at a time, where any has one)
           float ci = 0.f;
 #pragma unroll
           for (int k = 0; k < VPL; ++k)
             if (k == i) ci = c[k];
-          const bool need = close && ci >= least;
+          const bool need = close && ci >= need_from;
           uint32_t who = __ballot_sync(kAll, need);
           if (!who) continue;
           const double x = exact_choice<VPL>(p, row, need ? e0 + i : -1);
