@@ -948,10 +948,10 @@ size_t bf16_sorted_workspace(const Bf16Args &a) {
 
 bool bf16_items_fit(const Bf16Args &a, ProductMode mode) {
   if (mode == kDense ? a.pairs > 64 : mode == kSorted && sorted_is_wide(a))
-    return tile_bound(a, mode == kSorted, mode == kSorted ? sorted_height(a) : 64) * ((a.N + kWideN - 1) / kWideN) <= INT32_MAX / 16;
+    return tile_bound(a, mode == kSorted, mode == kSorted ? sorted_height(a) : 64) * ((a.N + kWideN - 1) / kWideN) <= kMostItems / 16;
   // every unit that the sorted arrays can hold, whatever they hold
   const long long units = mode == kSorted ? (long long)a.max_blocks * (a.block / 16) : unit_bound(a, mode, 16);
-  return units * ((a.N + kRows - 1) / kRows) <= INT32_MAX;
+  return units * ((a.N + kRows - 1) / kRows) <= kMostItems;
 }
 
 int launch_bf16_matmul(const Bf16Args &a, ProductMode mode, void *workspace, const DeviceInfo &dev, cudaStream_t s) {

@@ -783,10 +783,10 @@ size_t fp8_sorted_workspace(const Fp8Args &a) {
 
 bool fp8_items_fit(const Fp8Args &a, ProductMode mode) {
   if (mode == kDense ? a.pairs > 64 : mode == kSorted && fp8_sorted_is_wide(a))
-    return tile_bound(a, mode == kSorted, kTileRows) * ((a.N + kWideN - 1) / kWideN) <= INT32_MAX / 16;
+    return tile_bound(a, mode == kSorted, kTileRows) * ((a.N + kWideN - 1) / kWideN) <= kMostItems / 16;
   // every unit that the sorted arrays can hold, whatever they hold
   const long long units = mode == kSorted ? (long long)a.max_blocks * (a.block / 16) : unit_bound(a, mode, 16);
-  return units * ((a.N + kRows - 1) / kRows) <= INT32_MAX;
+  return units * ((a.N + kRows - 1) / kRows) <= kMostItems;
 }
 
 int launch_fp8_matmul(const Fp8Args &a, ProductMode mode, void *workspace, const DeviceInfo &dev, cudaStream_t s) {

@@ -42,6 +42,9 @@ __device__ __forceinline__ void list_units(const PairBlocks &p, int units, int *
   __syncthreads();
 }
 
+// Most items of a call: NarrowWork steps past the last by up to a grid, which has a CTA an SM at most.
+constexpr long long kMostItems = INT32_MAX - (1 << 16);
+
 // The items of a CTA, in the order of its warps' loops: all of K, or (a cluster
 // of cs > 1 CTAs, which has one item at most) this CTA's share of it.
 struct NarrowWork {
