@@ -616,8 +616,8 @@ int moe_fp8_grouped_matmul_naive(const moe_lora_fp8 *x, int x_per_pair, long lon
 
 /* Activations (act above).  SILU: v / (1 + exp(-v)); GELU: v * Phi(v); GELU_TANH:
  * 0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))).  For an fp32 y by CUDA's expf and
- * erfcf; for a bf16 one by approximations, off by at most 2^-16 of the value or 2^-21 of |v|,
- * whichever is more. */
+ * erfcf; for a bf16 one by approximations, off by at most 2^-16 of the value (2^-14 where
+ * v < -5), or 2^-118. */
 #define MOE_ACT_NONE 0
 #define MOE_ACT_RELU 1
 #define MOE_ACT_SILU 2

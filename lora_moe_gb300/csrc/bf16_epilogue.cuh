@@ -33,17 +33,21 @@ __device__ __forceinline__ float times_sigmoid(float v, float z) {
 }
 
 // v * Phi(v), Phi(v) = erfc(-v / sqrt(2)) / 2: erfc keeps the bits that 1 + erf(v)
-// loses for v < 0.  FAST: the rational approximation 7.1.26 of Abramowitz and
-// Stegun, "Handbook of Mathematical Functions", erfc(x) = (a1 t + .. + a5 t^5)
-// exp(-x^2), t = 1 / (1 + 0.3275911 x), within 1.5e-7 for x >= 0.
+// loses for v < 0.  FAST: erfc(x) = (a1 t + .. + a7 t^7) exp(-x^2), t = 1 / (1 + 0.51 x),
+// the polynomial fitted to erfc(x) exp(x^2) in relation to its value: within 2^-20 of
+// it for 0 <= x <= 10, so that the tail of v < 0 keeps its bits too (an error in
+// relation to one leaves gelu(-8) 1e-2 off, past half a step of bf16).  The argument of exp
+// is rounded: 2^-16 of the value at x = 9.
 template <bool FAST>
 __device__ __forceinline__ float gelu(float v) {
   if constexpr (FAST) {
-    const float x = 0.70710678f * fabsf(v), t = rcp_unit(1.f + 0.3275911f * x);
-    float q = 1.061405429f * t - 1.453152027f;
-    q = q * t + 1.421413741f;
-    q = q * t - 0.284496736f;
-    q = (q * t + 0.254829592f) * t * exp2_unit(-0.72134752f * v * v);   // erfc(x); x^2 log2(e) = v^2 log2(e) / 2
+    const float x = 0.70710678f * fabsf(v), t = rcp_unit(1.f + 0.51f * x);
+    float q = 0.0945045054f * t - 0.35915038f;
+    q = q * t + 0.358466744f;
+    q = q * t + 0.0550384037f;
+    q = q * t + 0.279071361f;
+    q = q * t + 0.284151375f;
+    q = (q * t + 0.287917554f) * t * exp2_unit(-0.72134752f * v * v);   // erfc(x); x^2 log2(e) = v^2 log2(e) / 2
     return v * (v < 0.f ? 0.5f * q : 1.f - 0.5f * q);
   } else {
     return 0.5f * v * erfcf(-0.70710678118654752f * v);
