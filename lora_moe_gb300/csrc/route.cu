@@ -431,25 +431,27 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
     const bool two = p.best == 2 && g2 > -INFINITY;
     const float worth = two ? fminf(fmaxf(g1 + g2, -FLT_MAX), FLT_MAX) : g1;
     uint32_t open = 0;
-    float rest = worth;
+    float rest = worth, last = 0.f;   // last: what the last one that stays is worth
     for (int k = 0; k < p.topk_groups; ++k) {
-      const float next = warp_max(rest);
-      const int from = __ffs(__ballot_sync(kAll, rest == next)) - 1;
+      last = warp_max(rest);
+      const int from = __ffs(__ballot_sync(kAll, rest == last)) - 1;
       open |= 1u << from;
       if (lane == from) rest = -INFINITY;
     }
     if (SCORES) {
-      // the least that one which stays may be worth, against the most that one which does not may be
+      // The least that one which stays may be worth, against the most that one which does not may be; both in relation to
+      // `last`, from which near ones differ exactly.
       const bool stays = open >> lane & 1;
       const float error = sum_error(slack, g1, two ? g2 : 0.f, worth);
-      const float least = -warp_max(stays ? __fadd_ru(error, -worth) : -INFINITY);
-      const float most = warp_max(!stays && worth > -INFINITY ? __fadd_ru(worth, error) : -INFINITY);
-      if (most > -INFINITY && !(least > most)) {
+      const float edge = stays ? __fadd_ru(error, __fadd_ru(last, -worth)) : __fadd_ru(error, __fadd_ru(worth, -last));
+      const float least = -warp_max(stays ? edge : -INFINITY);
+      const float most = warp_max(!stays && worth > -INFINITY ? edge : -INFINITY);
+      if (last > -INFINITY && !(least > most)) {   // (with no candidates in the last, the others have none)
         if (!at.span) return false;
         // The groups that may belong on the other side again, from exact choices of those experts that may be their best.
-        const bool again = worth > -INFINITY && (stays ? __fadd_rd(worth, -error) <= most : __fadd_ru(worth, error) >= least);
+        const bool again = worth > -INFINITY && (stays ? -edge <= most : edge >= least);
         const bool close = __ballot_sync(kAll, again) >> at.group & 1;
-        const float last = p.best == 2 && a2 > -INFINITY ? a2 : a1, need_from = last - 2.f * doubt(last);
+        const float least_c = p.best == 2 && a2 > -INFINITY ? a2 : a1, need_from = least_c - 2.f * doubt(least_c);
         double exact = again ? -INFINITY : worth;
         double second = -INFINITY;
         for (int i = 0; i < VPL; ++i) {   // (one expert a lane at a time, where any has one)
