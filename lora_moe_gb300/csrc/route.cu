@@ -451,7 +451,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
         // The groups that may belong on the other side again, from exact choices of those experts that may be their best.
         const bool again = worth > -INFINITY && (stays ? -edge <= most : edge >= least);
         const bool close = __ballot_sync(kAll, again) >> at.group & 1;
-        const float least_c = p.best == 2 && a2 > -INFINITY ? a2 : a1, need_from = least_c - 2.f * doubt(least_c);
+        const float least_c = p.best == 2 && a2 > -INFINITY ? a2 : a1, need_from = fmaxf(least_c - 2.f * doubt(least_c), -FLT_MAX);
         double exact = again ? -INFINITY : worth;
         double second = -INFINITY;
         for (int i = 0; i < VPL; ++i) {   // (one expert a lane at a time, where any has one)
@@ -502,8 +502,8 @@ __device__ __forceinline__ bool route_fast(const RouteArgs &p, const float (&l)[
     bound = warp_max(best);
     if (best == bound) best = -INFINITY;
   }
-  if (bound == -INFINITY) bound = -FLT_MAX;
-  else if (CHOICE) bound -= doubt(bound);   // and what is as large but for errors
+  if (CHOICE) bound -= doubt(bound);   // and what is as large but for errors
+  bound = fmaxf(bound, -FLT_MAX);      // (-inf: experts of closed groups, and those that do not exist)
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) mine += c[i] >= bound;
