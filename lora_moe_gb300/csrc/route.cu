@@ -681,7 +681,7 @@ bool on16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 template <int VPL>
 int launch_vpl(const RouteArgs &a, const DeviceInfo &dev, cudaStream_t stream) {
   const bool vec = a.E % VPL == 0 && on16(a.logits) && on16(a.bias) && a.ld % (a.logits_f32 ? 4 : 8) == 0;
-  const unsigned grid = (unsigned)std::min<long long>((a.M + kThreads / 32 - 1) / (kThreads / 32), dev.sm_count * 8ll);
+  const unsigned grid = (unsigned)std::min<long long>(((long long)a.M + kThreads / 32 - 1) / (kThreads / 32), dev.sm_count * 8ll);
   const bool full = a.E == 32 * VPL;
   const auto kernel = a.bias ? (full ? route_kernel<VPL, kByChoice, true> : route_kernel<VPL, kByChoice, false>)
                       : a.groups > a.topk_groups && a.best == 2
