@@ -686,8 +686,8 @@ int moe_bf16_grouped_matmul_naive(const moe_lora_bf16 *x, int x_per_pair, long l
  * equal groups of neighbours are candidates: those groups whose group_best (1 or 2)
  * largest c have the largest sum, the lowest index first among equals.
  * The order is that of c (without a bias, of the logits), the groups' that of their sums, in
- * 64-bit arithmetic; the weights are within 2^-19 of their value (2^-18 over more than
- * 256 experts), or within 2^-140.
+ * 64-bit arithmetic, for biases of any size and sign; the weights are within 2^-19 of their
+ * value (2^-18 over more than 256 experts), or within 2^-140 times max(scale, 1).
  * An expert whose logit (or c) is -inf or NaN is no candidate: it comes after
  * all candidates, as those of the other groups do, by index, with a weight of
  * zero; a row of nothing else has weights of zero.  A row with a NaN logit, or a

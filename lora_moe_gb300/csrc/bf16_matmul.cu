@@ -18,9 +18,9 @@
 //           out 2.5.
 //   wide    pairs of CTAs (cta_group::2), 256 of the weight's rows by up to 256
 //           pairs, on rows gathered into the blocks' order: bound by the tensor
-//           cores, and over seconds by power.  Dense 8192 x 4096 x 14336: 490 us
-//           (1.96 PFLOP/s), 575 in calls that go on for seconds; Mixtral-shaped
-//           w13 prefill 2.19 ms (1.76 PFLOP/s) and 2.53.  Experts of few rows are
+//           cores, and over seconds by power.  Dense 8192 x 4096 x 14336: 488 us
+//           (1.97 PFLOP/s), 570 in calls that go on for seconds; Mixtral-shaped
+//           w13 prefill 2.28 ms (1.69 PFLOP/s) and 2.49.  Experts of few rows are
 //           bound by the weight's bytes: 1024 tokens, 8 of 128 experts of 2048 x
 //           1536, 148 us, 123 of them at the copy rate.  In chunks, K split over
 //           two pairs: 4096 x 256, K of 7168, to fp32 20.4 us.
@@ -67,7 +67,7 @@ struct Bf16Cfg {
 
 // ------------------------------------------------------------------ narrow
 
-constexpr int kMaxRing = 5;    // stages: 5 gave 264 us, 4 265, 3 272, 6 272 and 12 278 (64 tokens, 4 of 128 experts of 2880 x 2880)
+constexpr int kMaxRing = 5;    // stages: 5 gave 264 us, 4 265, 3 272 and 6 272 (64 tokens, 4 of 128 experts of 2880 x 2880)
 constexpr int kMaxSmem = 227 * 1024;
 // Groups of K whose products the tensor cores add up.  Their additions truncate,
 // so a long sum drifts (K of 7168, products of one sign: 2.4e-5 of the sum); the
@@ -936,8 +936,11 @@ bool sorted_is_wide(const Bf16Args &a) {
 // Up to this many bytes of weights, calls of single pairs or of at most 16 rows
 // run the kernel that streams the weight through registers: it starts sooner.  us,
 // streaming / narrow: one token's eight experts of 1536 x 2048 (50 MB) 9.7 / 12.3,
-// one row by 4096 x 4096 7.5 / 10.0, 16 rows by 8192 x 4096 14.5 / 15.1, 8 rows by 8192 x
-// 8192 (134 MB) 22.8 / 24.6.
+// one row by 4096 x 4096 7.5 / 10.0, 16 rows by 8192 x 4096 (67 MB) 14.5 / 15.1.  Around the
+// limit: single pairs, 201 MB 32.4 / 37.5, 268 MB 51 / 42, 537 MB 85 / 81; one row, 134 MB
+// 22.8 / 23.0, 235 MB 38.0 / 38.7, 268 MB 43.0 / 42.8, 470 MB 73.0 / 73.8; 8 rows, 134 MB 23.5 /
+// 23.2, 235 MB 39.3 / 38.8.  (9 to 16 rows would gain from a lower one: 134 MB 24.9 / 23.5,
+// 235 MB 44.4 / 39.1.)
 constexpr double kStreamBytes = 256e6;
 
 }  // namespace
@@ -964,7 +967,10 @@ int launch_bf16_matmul(const Bf16Args &a, ProductMode mode, void *workspace, con
     return launch_narrow<16, kSorted>(a, dev, s);
   }
   if (small && a.pairs <= 16) return launch_bf16_stream(a, mode, dev, s);
-  // (32 x 4096 x 4096 9.2 us, 11.5 wide; 64 rows 10.3 and 12.1; by 28672 x 8192 77.6 and 83.0)
+  // Up to 64 rows, one unit of the narrow kernel.  us, narrow / wide: 32 x 4096 x 4096 9.2 / 11.5;
+  // 64 rows 10.3 / 12.1, by 28672 x 8192 77.6 / 83.0; in two units and more, which read the weight again, 65 x 4096 x
+  // 4096 12.8 / 12.5, 128 rows 13.0 / 12.8, 256 16.6 / 14.8, 512 29 / 17; 128 x 4096 x 2880 12.8 / 11.8, 128 x 8192
+  // x 28672 142 / 89.  (Small weights would gain: 128 x 2048 x 1536 6.2 / 7.7, by 128 columns 5.0 / 6.5.)
   if (a.pairs <= 16) return launch_narrow<16, kDense>(a, dev, s);
   if (a.pairs <= 32) return launch_narrow<32, kDense>(a, dev, s);
   if (a.pairs <= 64) return launch_narrow<64, kDense>(a, dev, s);

@@ -9,8 +9,8 @@
 // columns, added in fp32) over its share of K; the CTA's warps split K or take
 // further rows, and their sums meet in shared memory in a fixed order.  Measured:
 // one row by 128 x 2048 2.4 us, by 4096 x 4096 7.3; one token's eight experts of
-// 1536 x 2048 (50 MB) 9.6 us, 5.2 TB/s (12.3 on tcgen05); one row by 28672 x 8192
-// 74.3 us, 6.3 TB/s.
+// 1536 x 2048 (50 MB) 9.6 us, 5.2 TB/s (12.3 on tcgen05); one row by 14336 x 8192
+// (235 MB) 38.0 us, 6.2 TB/s.
 //
 // The tensor core sees the columns of a group of 64 in an order of its own:
 // lane (r, t) holds bytes [16t, 16t + 16) and [64 + 16t, 64 + 16t + 16) of its

@@ -14,14 +14,16 @@
 // experts that reach the bound, fewer candidates than places) takes the largest
 // topk times (route_general).  Bound by latency for a few tokens, by instructions
 // for many: 16384 tokens of 256 experts take about 420 a token by their logits
-// (8.6 us; the bytes, 2.6) and 800 under a bias in groups (20.3 us), and one token
-// 1.6 us.  Taking the largest eight times for all of them took 21.6 and 48 us.
+// (9.6 us; the bytes, 2.6) and 870 under a bias in groups (20.7 us), and one token
+// 1.7 us.  Taking the largest eight times for all of them took 21.6 and 48 us.
 //
 // Which experts are chosen is what arithmetic in 64 bits says.  Without a bias
 // the logits decide, which needs no arithmetic, but for sums of a group's scores.
 // With one, c is computed in fp32 with a bound of its error, and where two
 // neighbours of the order lie within that bound it is done again in fp64: for
-// few tokens, as the bound is 1e-6 of the scores.
+// few tokens, as the bound is 1e-6 of the scores.  A bias adds half an ulp of the choice, which moves no
+// choice past another (rounding keeps the order); in a group's sum of two, where biases may cancel,
+// it moves sums past one another, so that each group's doubt counts both of its choices (sum_error).
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -120,7 +122,8 @@ struct Routed {
 // One token, whatever its logits.  Apart, so that the fast form keeps its
 // registers.  Errors of fp32 scores: expf, its argument and the quotient within
 // 2^-21 of s (an ulp, half an ulp of 1 + e and of the quotient, and for the
-// softmax |x| exp(-|x|) half ulps of x); a sum of VPL + 5 steps, (VPL + 5) half ulps.
+// softmax |x| exp(-|x|) half ulps of x); a sum of VPL + 5 steps, (VPL + 5) half ulps.  The
+// biases' roundings are counted where choices are compared (close) or added up (sum_error).
 template <typename T, int VPL>
 __device__ __noinline__ Routed route_general(const RouteArgs &p, long long row) {
   const int lane = threadIdx.x & 31;

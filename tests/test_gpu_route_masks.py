@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from test_gpu_route import INF, check, run
+from test_gpu_route import INF, check, route64, run
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +54,17 @@ def test_logits_of_the_lowest_value(E, topk, sigmoid):
         # a row of nothing else: equal scores (too small for 64 bits where they are a sigmoid's), of which each has its share
         ids, weights = run(low, topk, bias=bias, sigmoid=sigmoid)
         assert ids[0].tolist() == list(range(topk)) and ((weights - 1 / topk).abs() <= 2.0 ** -19 / topk).all()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("scale", [1e-30, 1e30])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_weights_of_a_scale(sigmoid, scale, renormalize):
+    """Scores near the smallest fp32 times a large number: an absolute error of the scores is scaled with them."""
+    logits = torch.randn((50, 64), generator=torch.Generator("cuda").manual_seed(1), device="cuda") - 95
+    if not sigmoid:
+        logits[:, 0] = 0
+    ids, weights = run(logits, 6, sigmoid=sigmoid, renormalize=renormalize, scale=scale)
+    want, w64 = route64(logits, 6, sigmoid=sigmoid, renormalize=renormalize, scale=scale)
+    assert torch.equal(ids.cpu(), want)
+    assert ((weights.cpu().double() - w64).abs() <= 2.0 ** -19 * w64.abs() + 2.0 ** -140 * max(scale, 1)).all()
